@@ -336,6 +336,125 @@ GDN_API gdn_status_t gdn_decode_multi(const gdn_dims_t *dims, int T, const void 
                                       float *S, void *out, const int32_t *n_keep, gdn_stream_t stream);
 
 /*
+ * The selective state-space mixer: the other linear-time token mixer that hybrid
+ * models interleave with the gated delta rule.  It shares this library's short
+ * convolution (here with a bias) and its decay, and writes without erasing; the
+ * pages have no counterpart.  Per token, with g = h / (H / G) the group of head h:
+ *
+ *   xh_t = SiLU(ShortConv(x_t) + conv_b),  Bh_t and Ch_t likewise
+ *   D_t  = softplus(dt_logit_t + b_dt_h)         (the step)
+ *   a_t  = exp(-exp(A_h) D_t)                    (the decay)
+ *   S_t  = a_t S_{t-1} + D_t Bh_t xh_t^T         S in R^{N x P}, fp32, row-major [N][P]
+ *   y_t  = S_t^T Ch_t + D_h xh_t
+ *   out_t = y_t SiLU(z_t)                        (z NULL: out_t = y_t)
+ *
+ * The B and C of a group serve its H / G heads.  Channels of conv_w, conv_b and the
+ * histories are ordered [x: H P | B: G N | C: G N].
+ */
+typedef struct {
+    int32_t num_seqs;      /* sequences (step: batch size B) */
+    int32_t total_tokens;  /* packed tokens N_tok (step: must equal num_seqs) */
+    int32_t H, G;          /* heads, and groups that share B and C; G divides H */
+    int32_t P, N;          /* head dim and state dim, 64 or 128 */
+    int32_t conv_k;        /* ShortConv width, 4 */
+    gdn_dtype_t in_dtype;  /* x, B, C, dt_logit, z and the histories */
+    gdn_dtype_t out_dtype; /* out */
+    /* elements from one token to the next, 0 = packed (H P, G N, G N, H P, H): column
+     * blocks of one projection result are read where they lie */
+    int64_t ld_x, ld_B, ld_C, ld_z, ld_dt;
+} gdn_ssm_dims_t;
+
+/*
+ * gdn_ssm_prefill -- the mixer over a packed batch of sequences.
+ *
+ *   x         [N_tok, H, P], B, C [N_tok, G, N] raw (pre-conv), dt_logit [N_tok, H],
+ *             z [N_tok, H, P] or NULL, all in_dtype, token strides ld_*
+ *   conv_w    [H P + 2 G N, 4] fp32; conv_b [H P + 2 G N] fp32 or NULL (zeros)
+ *   A, b_dt   [H] fp32; D [H] fp32 or NULL (zeros)
+ *   S0        [N_seq, H, N, P] fp32 initial states, or NULL for zeros
+ *   conv_hist [N_seq, 3, H P + 2 G N] in_dtype: the raw channels of the three tokens
+ *             before each sequence, oldest first, or NULL for zeros
+ *   cu_seqlens [N_seq + 1] int32 DEVICE prefix offsets as for gdn_prefill, or NULL for
+ *             equal lengths.  cu[N_seq] may be less than N_tok: the tokens behind it
+ *             are not read and their rows of out stay as they were.  Offsets are
+ *             clamped to [0, N_tok] and to non-decreasing pairs.
+ *   out       [N_tok, H, P] packed, out_dtype, written
+ *   S_final   [N_seq, H, N, P] fp32 final states, written, or NULL; may be S0
+ *   conv_tail [N_seq, 3, H P + 2 G N] in_dtype, written, or NULL: the history that
+ *             continues each sequence (a later prefill's or a step's conv_hist); may
+ *             be conv_hist
+ *
+ * With S_final and conv_tail fed back, a sequence run in pieces gives the result of
+ * one run.  `out` must not alias any input; S_final and conv_tail alias at most the
+ * same buffer of the input they continue.  x, B, C, z, conv_w, conv_b, S0, conv_hist,
+ * out, S_final, conv_tail 16-byte aligned, and ld_x, ld_B, ld_C, ld_z multiples of 16
+ * bytes (GDN_ERR_ALIGNMENT otherwise); dt_logit, A, b_dt, D, cu_seqlens aligned to
+ * their elements.  Token tensors may be NULL when total_tokens is 0.  Sequences and
+ * heads up to 65535 (GDN_ERR_UNSUPPORTED above).
+ * All arithmetic and the state are fp32.  Stream-ordered workspace of
+ * gdn_ssm_prefill_workspace_size() bytes from the library's pool.
+ */
+GDN_API gdn_status_t gdn_ssm_prefill(const gdn_ssm_dims_t *dims, const void *x, const void *B, const void *C,
+                                     const void *dt_logit, const float *conv_w, const float *conv_b,
+                                     const float *A, const float *b_dt, const float *D, const void *z,
+                                     const float *S0, const void *conv_hist, const int32_t *cu_seqlens, void *out,
+                                     float *S_final, void *conv_tail, gdn_stream_t stream);
+
+/* Bytes of device workspace one gdn_ssm_prefill call with these dims uses (host call). */
+GDN_API gdn_status_t gdn_ssm_prefill_workspace_size(const gdn_ssm_dims_t *dims, size_t *bytes);
+
+/*
+ * gdn_ssm_decode_step -- one token for each of B = dims->num_seqs sequences, updating
+ * the state and the convolution history in place.
+ *   x [B, H, P], B, C [B, G, N], dt_logit [B, H], z [B, H, P] or NULL  (row strides ld_*)
+ *   conv_w, conv_b, A, b_dt, D   as for gdn_ssm_prefill
+ *   conv_hist [B, 3, H P + 2 G N] in_dtype, in/out: shifted by one, the current raw
+ *             token becomes the newest row
+ *   S         [B, H, N, P] fp32, in/out
+ *   out       [B, H, P] packed, out_dtype, written
+ * dims->total_tokens must equal dims->num_seqs.  No workspace.  Alignment as above.
+ */
+GDN_API gdn_status_t gdn_ssm_decode_step(const gdn_ssm_dims_t *dims, const void *x, const void *B, const void *C,
+                                         const void *dt_logit, const float *conv_w, const float *conv_b,
+                                         void *conv_hist, const float *A, const float *b_dt, const float *D,
+                                         const void *z, float *S, void *out, gdn_stream_t stream);
+
+/*
+ * gdn_quant_fp8 -- values to 8-bit floating point (e4m3) with one fp32 scale per block
+ * of 1 x 128 (block_rows = 1: activations) or 128 x 128 elements (block_rows = 128:
+ * weights); the last block of a row or column may be smaller:
+ *   amax = max(max |x|, 2^-64),  scale = amax / 448,  q = e4m3(x (448 / amax))
+ * in fp32 with IEEE divisions, rounded to nearest even.  A block with a NaN gets a NaN
+ * scale.
+ *   x      [rows, cols] in_dtype, rows ld_x elements apart
+ *   q      [rows, cols] bytes, rows ld_q apart, written
+ *   scale  [ceil(rows / block_rows), ceil(cols / 128)] fp32 packed, written
+ * cols a multiple of 16 (GDN_ERR_INVALID_ARG); x and q 16-byte aligned, ld_x a multiple
+ * of 16 bytes and ld_q of 16 (GDN_ERR_ALIGNMENT).  rows = 0 or cols = 0 writes nothing.
+ * One kernel; no workspace.
+ */
+GDN_API gdn_status_t gdn_quant_fp8(int rows, int cols, const void *x, int64_t ld_x, gdn_dtype_t in_dtype,
+                                   int block_rows, void *q, int64_t ld_q, float *scale, gdn_stream_t stream);
+
+/*
+ * gdn_gemm_fp8 -- C [M, N] = A [M, K] B^T with e4m3 operands in 8-bit blocks of 128 along
+ * K, each with its scale: the layer's projections at half the weight bytes.
+ *   C[m, n] = sum_b a_scale[m, b] b_scale[n / 128, b] sum_{k in block b} A[m, k] B[n, k]
+ *   A       [M, K] e4m3, rows lda bytes apart; a_scale [M, ceil(K / 128)] fp32 packed
+ *           (gdn_quant_fp8 with block_rows = 1)
+ *   B       [N, K] e4m3 (a weight as [out features, in features]), rows ldb bytes
+ *           apart; b_scale [ceil(N / 128), ceil(K / 128)] fp32 packed (block_rows = 128)
+ *   C       [M, N] out_dtype, rows ldc elements apart, written
+ * Products are exact, sums are fp32.  K, lda and ldb multiples of 16; A and B 16-byte
+ * aligned, C to its elements (16 bytes and ldc a multiple of 16 bytes are faster).
+ * M = 0 or N = 0 writes nothing.  One kernel; no workspace.  The sum's order depends on
+ * the sizes only.  An expired wait raises GDN_ERRF_FP8.
+ */
+GDN_API gdn_status_t gdn_gemm_fp8(int M, int N, int K, const void *A, int64_t lda, const float *a_scale,
+                                  const void *B, int64_t ldb, const float *b_scale, void *C, int64_t ldc,
+                                  gdn_dtype_t out_dtype, gdn_stream_t stream);
+
+/*
  * gdn_prefill_noalloc -- gdn_prefill for callers that cannot allocate device
  * memory.  The pages have no counterpart: this is an interface choice of the
  * library.  Callers that may not call cudaMalloc or any allocator while they
@@ -433,6 +552,7 @@ GDN_API int gdn_last_call_slots(void);
 #define GDN_ERRF_DECODE 4u  /* streaming decode kernel (gdn_decode_step) */
 #define GDN_ERRF_QSA 8u     /* QSA indexer score kernel (gdn_qsa_indexer) */
 #define GDN_ERRF_GEMM 16u   /* projection GEMMs (gdn_layer_forward) */
+#define GDN_ERRF_FP8 64u    /* 8-bit product (gdn_gemm_fp8) */
 
 /*
  * gdn_device_error_status -- reads the current device's error words into

@@ -317,16 +317,17 @@ int gdn_last_call_slots(void) { return tl_slots; }
 
 gdn_status_t gdn_device_error_status(unsigned *flags, int clear, gdn_stream_t stream) {
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    unsigned w[5] = {0, 0, 0, 0, 0};
+    unsigned w[6] = {0, 0, 0, 0, 0, 0};
     cudaError_t e = gdn::prep_error_word(&w[0], clear != 0, s);
     if (e == cudaSuccess) e = gdn::chain_error_word(&w[1], clear != 0, s);
     if (e == cudaSuccess) e = gdn::decode_error_word(&w[2], clear != 0, s);
     if (e == cudaSuccess) e = gdn::qsa_error_word(&w[3], clear != 0, s);
     if (e == cudaSuccess) e = gdn::gemm_error_word(&w[4], clear != 0, s);
+    if (e == cudaSuccess) e = gdn::fp8_error_word(&w[5], clear != 0, s);
     if (e != cudaSuccess) return GDN_ERR_CUDA;
     const unsigned f = (w[0] ? GDN_ERRF_PREP : 0u) | (w[1] ? GDN_ERRF_CHAIN : 0u) |
                        (w[2] ? GDN_ERRF_DECODE : 0u) | (w[3] ? GDN_ERRF_QSA : 0u) |
-                       (w[4] ? GDN_ERRF_GEMM : 0u);
+                       (w[4] ? GDN_ERRF_GEMM : 0u) | (w[5] ? GDN_ERRF_FP8 : 0u);
     if (flags) *flags = f;
     return f ? GDN_ERR_TIMEOUT : GDN_OK;
 }
@@ -783,6 +784,178 @@ gdn_status_t gdn_decode_multi(const gdn_dims_t *dims, int T, const void *q, cons
     if (e == cudaSuccess)
         e = slot_launch(&slot, a.stream, [&] { return gdn::launch_decode_stream(a, T, n_keep); });
     if (e == cudaSuccess) e = record(g_ev_end, a.stream);
+    return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+}  // extern "C"
+
+namespace {
+
+// Checks shared by the state-space mixer's calls; fills the sizes and strides of *a.
+gdn_status_t ssm_dims(const gdn_ssm_dims_t *d, bool step, gdn::SsmArgs *a) {
+    if (!d) return GDN_ERR_INVALID_ARG;
+    if (d->num_seqs <= 0 || d->total_tokens < 0 || d->H <= 0 || d->G <= 0 || d->P <= 0 || d->N <= 0 || d->conv_k <= 0)
+        return GDN_ERR_INVALID_ARG;
+    if ((d->in_dtype != GDN_F32 && d->in_dtype != GDN_BF16) || (d->out_dtype != GDN_F32 && d->out_dtype != GDN_BF16))
+        return GDN_ERR_INVALID_ARG;
+    if (d->H % d->G != 0) return GDN_ERR_INVALID_ARG;
+    if (step && d->total_tokens != d->num_seqs) return GDN_ERR_INVALID_ARG;
+    if ((d->P != 64 && d->P != 128) || (d->N != 64 && d->N != 128) || d->conv_k != 4) return GDN_ERR_UNSUPPORTED;
+    // grid limits: one grid row per sequence and per head
+    if (d->num_seqs > 65535 || d->H > 65535) return GDN_ERR_UNSUPPORTED;
+    if ((int64_t)d->H * d->P + 2 * (int64_t)d->G * d->N > (int64_t)1 << 24) return GDN_ERR_UNSUPPORTED;
+    a->n_seq = d->num_seqs;
+    a->n_tok = d->total_tokens;
+    a->H = d->H;
+    a->G = d->G;
+    a->P = d->P;
+    a->N = d->N;
+    a->in_bf16 = d->in_dtype == GDN_BF16;
+    a->out_bf16 = d->out_dtype == GDN_BF16;
+    const int64_t hp = (int64_t)d->H * d->P, gn = (int64_t)d->G * d->N;
+    const int64_t given[5] = {d->ld_x, d->ld_B, d->ld_C, d->ld_z, d->ld_dt}, packed[5] = {hp, gn, gn, hp, d->H};
+    long long *ld[5] = {&a->ld_x, &a->ld_B, &a->ld_C, &a->ld_z, &a->ld_dt};
+    const int64_t vec = a->in_bf16 ? 8 : 4;   // elements of 16 bytes
+    for (int i = 0; i < 5; ++i) {
+        if (given[i] < 0 || (given[i] > 0 && given[i] < packed[i])) return GDN_ERR_INVALID_ARG;
+        *ld[i] = given[i] ? given[i] : packed[i];
+        if (i < 4 && *ld[i] % vec != 0) return GDN_ERR_ALIGNMENT;
+    }
+    return GDN_OK;
+}
+
+// Pointer checks of both calls: `tok` tensors are required unless there are no
+// tokens, `need` always; all 16-byte aligned except the element-aligned ones.
+gdn_status_t ssm_pointers(const gdn::SsmArgs &a) {
+    const bool no_tokens = a.n_tok == 0;
+    const uintptr_t in_sz = a.in_bf16 ? 2 : 4;
+    const void *tok[] = {a.x, a.B, a.C, a.out};
+    for (const void *p : tok) {
+        if (!p && !no_tokens) return GDN_ERR_INVALID_ARG;
+        if (p && !aligned16(p)) return GDN_ERR_ALIGNMENT;
+    }
+    if (!a.dt && !no_tokens) return GDN_ERR_INVALID_ARG;
+    if (a.dt && !aligned_to(a.dt, in_sz)) return GDN_ERR_ALIGNMENT;
+    if (!a.conv_w || !a.A || !a.b_dt) return GDN_ERR_INVALID_ARG;
+    const void *opt16[] = {a.conv_w, a.conv_b, a.z, a.S0, a.hist, a.S_final, a.tail};
+    for (const void *p : opt16)
+        if (p && !aligned16(p)) return GDN_ERR_ALIGNMENT;
+    const void *opt4[] = {a.A, a.b_dt, a.D, a.cu_seqlens};
+    for (const void *p : opt4)
+        if (p && !aligned_to(p, 4)) return GDN_ERR_ALIGNMENT;
+    return GDN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+gdn_status_t gdn_ssm_prefill_workspace_size(const gdn_ssm_dims_t *dims, size_t *bytes) {
+    gdn::SsmArgs a = {};
+    const gdn_status_t st = ssm_dims(dims, false, &a);
+    if (st != GDN_OK) return st;
+    if (!bytes) return GDN_ERR_INVALID_ARG;
+    *bytes = gdn::ssm_workspace_bytes(a);
+    return GDN_OK;
+}
+
+gdn_status_t gdn_ssm_prefill(const gdn_ssm_dims_t *dims, const void *x, const void *B, const void *C,
+                             const void *dt_logit, const float *conv_w, const float *conv_b, const float *A,
+                             const float *b_dt, const float *D, const void *z, const float *S0,
+                             const void *conv_hist, const int32_t *cu_seqlens, void *out, float *S_final,
+                             void *conv_tail, gdn_stream_t stream) {
+    tl_launches = 0;
+    tl_slots = 0;
+    gdn::SsmArgs a = {};
+    gdn_status_t st = ssm_dims(dims, false, &a);
+    if (st != GDN_OK) return st;
+    if (!cu_seqlens && a.n_tok % a.n_seq != 0) return GDN_ERR_INVALID_ARG;
+    a.x = x; a.B = B; a.C = C; a.dt = dt_logit; a.z = z;
+    a.conv_w = conv_w; a.conv_b = conv_b; a.A = A; a.b_dt = b_dt; a.D = D; a.S0 = S0;
+    a.hist = conv_hist;
+    a.cu_seqlens = cu_seqlens;
+    a.out = out;
+    a.S_final = S_final;
+    a.tail = conv_tail;
+    a.stream = reinterpret_cast<cudaStream_t>(stream);
+    if ((st = ssm_pointers(a)) != GDN_OK) return st;
+    const size_t ws_bytes = gdn::ssm_workspace_bytes(a);
+    char *ws = nullptr;
+    if (ws_bytes > 0) {
+        cudaMemPool_t pool;
+        if (get_pool(&pool) != cudaSuccess) return GDN_ERR_CUDA;
+        if (cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws), ws_bytes, pool, a.stream) != cudaSuccess)
+            return GDN_ERR_CUDA;
+    }
+    cudaError_t e = record(g_ev_begin, a.stream);
+    if (e == cudaSuccess) e = gdn::launch_ssm_prefill(a, ws);
+    if (e == cudaSuccess) e = record(g_ev_end, a.stream);
+    if (ws) {
+        const cudaError_t ef = cudaFreeAsync(ws, a.stream);
+        if (e == cudaSuccess) e = ef;
+    }
+    return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+gdn_status_t gdn_ssm_decode_step(const gdn_ssm_dims_t *dims, const void *x, const void *B, const void *C,
+                                 const void *dt_logit, const float *conv_w, const float *conv_b, void *conv_hist,
+                                 const float *A, const float *b_dt, const float *D, const void *z, float *S,
+                                 void *out, gdn_stream_t stream) {
+    tl_launches = 0;
+    tl_slots = 0;
+    gdn::SsmArgs a = {};
+    gdn_status_t st = ssm_dims(dims, true, &a);
+    if (st != GDN_OK) return st;
+    a.x = x; a.B = B; a.C = C; a.dt = dt_logit; a.z = z;
+    a.conv_w = conv_w; a.conv_b = conv_b; a.A = A; a.b_dt = b_dt; a.D = D;
+    a.hist = conv_hist;
+    a.out = out;
+    a.S_final = S;
+    a.stream = reinterpret_cast<cudaStream_t>(stream);
+    if (!conv_hist || !S) return GDN_ERR_INVALID_ARG;
+    if ((st = ssm_pointers(a)) != GDN_OK) return st;
+    cudaError_t e = record(g_ev_begin, a.stream);
+    if (e == cudaSuccess) e = gdn::launch_ssm_decode(a);
+    if (e == cudaSuccess) e = record(g_ev_end, a.stream);
+    return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+gdn_status_t gdn_quant_fp8(int rows, int cols, const void *x, int64_t ld_x, gdn_dtype_t in_dtype, int block_rows,
+                           void *q, int64_t ld_q, float *scale, gdn_stream_t stream) {
+    tl_launches = 0;
+    tl_slots = 0;
+    if (rows < 0 || cols < 0 || (block_rows != 1 && block_rows != 128)) return GDN_ERR_INVALID_ARG;
+    if (in_dtype != GDN_F32 && in_dtype != GDN_BF16) return GDN_ERR_INVALID_ARG;
+    if (rows == 0 || cols == 0) return GDN_OK;
+    if (!x || !q || !scale || cols % 16 != 0 || ld_x < cols || ld_q < cols) return GDN_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(q) || !aligned_to(scale, 4) || ld_q % 16 != 0 ||
+        ld_x % (in_dtype == GDN_BF16 ? 8 : 4) != 0)
+        return GDN_ERR_ALIGNMENT;
+    // grid limits: 64 row blocks, or one row of 128 x 128 blocks, per CTA row
+    if ((int64_t)rows * ((cols + 127) / 128) > (int64_t)1 << 36 || (block_rows == 128 && rows > 65535 * 128))
+        return GDN_ERR_UNSUPPORTED;
+    const cudaError_t e = gdn::launch_quant_fp8(rows, cols, x, ld_x, in_dtype == GDN_BF16, block_rows, q, ld_q, scale,
+                                                reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+gdn_status_t gdn_gemm_fp8(int M, int N, int K, const void *A, int64_t lda, const float *a_scale, const void *B,
+                          int64_t ldb, const float *b_scale, void *C, int64_t ldc, gdn_dtype_t out_dtype,
+                          gdn_stream_t stream) {
+    tl_launches = 0;
+    tl_slots = 0;
+    if (M < 0 || N < 0 || K <= 0) return GDN_ERR_INVALID_ARG;
+    if (out_dtype != GDN_F32 && out_dtype != GDN_BF16) return GDN_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return GDN_OK;
+    if (!A || !B || !C || !a_scale || !b_scale || K % 16 != 0 || lda < K || ldb < K || ldc < N)
+        return GDN_ERR_INVALID_ARG;
+    if (!aligned16(A) || !aligned16(B) || lda % 16 != 0 || ldb % 16 != 0 || !aligned_to(a_scale, 4) ||
+        !aligned_to(b_scale, 4) || !aligned_to(C, out_dtype == GDN_BF16 ? 2 : 4))
+        return GDN_ERR_ALIGNMENT;
+    // tile coordinates stay within int32
+    if (M > 0x7fffff00 || N > 0x7fffff00 || K > 0x7fffff00) return GDN_ERR_UNSUPPORTED;
+    const cudaError_t e = gdn::launch_gemm_fp8(M, N, K, A, lda, a_scale, B, ldb, b_scale, C, ldc,
+                                               out_dtype == GDN_BF16, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 

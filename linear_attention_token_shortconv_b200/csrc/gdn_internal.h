@@ -69,6 +69,7 @@ cudaError_t make_tma_3d(TmaMap *out, const void *base, bool bf16, int inner, int
 cudaError_t make_tma_rows_f32(TmaMap *out, const void *base, int cols, int rows, int box_cols, int box_rows);
 cudaError_t make_tma_mat_bf16(TmaMap *out, const void *base, int inner, int rows, int ld, int box_inner,
                               int box_rows);
+cudaError_t make_tma_mat_u8(TmaMap *out, const void *base, int inner, int rows, long long ld, int box_rows);
 cudaError_t make_tma_plain_bf16(TmaMap *out, const void *base, int rank, const long long *dims,
                                 const long long *strides, const int *box);
 // K7: C [M, N] = A [M, K] B [K, N], bf16 row-major with leading dimensions lda,
@@ -137,6 +138,37 @@ cudaError_t launch_decode_stream(const DecodeArgs &a);
 // T (1..4) consecutive tokens per sequence: q, k, v, z, out [B, T, H, d], gate
 // logits [B, T, H]; the state and history advance by n_keep[b] tokens (NULL: T).
 cudaError_t launch_decode_stream(const DecodeArgs &a, int T, const int32_t *n_keep);
+
+// K8: the selective state-space mixer.  x [N_tok, H, P], B, C [N_tok, G, N], z, dt
+// [N_tok, H] with token strides ld_* (elements); channels [x | B | C] of conv_w,
+// conv_b, hist and tail (both [n_seq, 3, channels]).  The step has n_tok = n_seq and
+// updates hist and S_final in place.
+struct SsmArgs {
+    int n_seq, n_tok, H, G, P, N;
+    bool in_bf16, out_bf16;
+    const void *x, *B, *C, *dt, *z;
+    long long ld_x, ld_B, ld_C, ld_dt, ld_z;
+    const float *conv_w, *conv_b, *A, *b_dt, *D, *S0;
+    const void *hist;
+    const int32_t *cu_seqlens;
+    void *out;
+    float *S_final;
+    void *tail;
+    cudaStream_t stream;
+};
+size_t ssm_workspace_bytes(const SsmArgs &a);
+cudaError_t launch_ssm_prefill(const SsmArgs &a, void *ws);
+cudaError_t launch_ssm_decode(const SsmArgs &a);
+
+// K9: e4m3 values with one fp32 scale per 1 x 128 (block_rows = 1) or 128 x 128
+// block, and the product of two such matrices, C [M, N] = A [M, K] B^T with B [N, K].
+cudaError_t launch_quant_fp8(int rows, int cols, const void *x, long long ld_x, bool bf16_in, int block_rows,
+                             void *q, long long ld_q, float *scale, cudaStream_t stream);
+cudaError_t launch_gemm_fp8(int M, int N, int K, const void *A, long long lda, const float *a_scale, const void *B,
+                            long long ldb, const float *b_scale, void *C, long long ldc, bool out_bf16,
+                            cudaStream_t stream);
+cudaError_t fp8_error_word(unsigned *v, bool clear, cudaStream_t s);
+cudaError_t fp8_wait_selftest(uint32_t max_polls, cudaStream_t s);
 
 // SM count of the current device (queried once per device, then cached).
 cudaError_t sm_count(int *out);

@@ -1,0 +1,427 @@
+// K9b -- the product of two e4m3 matrices with block scales on tcgen05:
+//
+//   C [M, N] = sum over K blocks b of 128 of
+//              a_scale[m, b] b_scale[n / 128, b] sum_{k in b} A[m, k] B[n, k]
+//
+// A [M, K] (rows: tokens), B [N, K] (rows: output features, as a linear layer keeps
+// its weight), both K-contiguous; C bf16 or fp32.
+//
+// The scales change with every K block, so the tensor cores cannot accumulate over K
+// on their own: each block's 128 x BN product goes to its own TMEM buffer (four
+// K = 32 MMAs, one 128-byte swizzled row of each operand), and the epilogue warps
+// read it, multiply by the block's scale and add it into fp32 registers while the
+// next block's MMAs fill another buffer.
+//
+// Roles: warp 0 lane 0 loads by TMA, warp 1 lane 0 issues the MMAs (and owns the
+// TMEM), the others are the epilogue.  Every wait is bounded; one that expires raises
+// the error word and an abort flag that the other roles check.
+//
+// Two operand orders.  Many tokens: tokens are the MMA's 128 rows and features its BN
+// columns.  At most 64 tokens: features are the 128 rows and the tokens the 16, 32 or
+// 64 columns, so that no row of the tile is empty while the weights stream by.
+//
+// Where the tiles leave SMs idle the K range is split over the CTAs of a cluster: each
+// writes its fp32 part to its own shared memory, and after a cluster barrier every CTA
+// adds a share of the tile over the cluster in rank order (the sum's order is fixed).
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include <cstring>
+
+#include "gdn_device.cuh"
+#include "gdn_internal.h"
+#include "umma.cuh"
+
+namespace gdn {
+
+__device__ unsigned int g_fp8_err;
+
+namespace fp8 {
+constexpr int BM = 128, BK = 128;
+constexpr uint32_t MAX_POLLS = 1u << 24;
+
+template <int BN_, bool SWAP_> struct Shape {
+    static constexpr int BN = BN_;
+    static constexpr bool SWAP = SWAP_;
+    static constexpr int A_ST = BM * BK, B_ST = BN * BK, ST = A_ST + B_ST;
+    static constexpr int NS = 196608 / ST < 8 ? 196608 / ST : 8;
+    static constexpr int NT = 512 / BN < 4 ? 512 / BN : 4;            // TMEM buffers
+    static constexpr uint32_t TMEM_COLS = NT * BN;                      // 64 .. 512, a power of two
+    static constexpr int EPI_WARPS = BN >= 128 ? 8 : 4;
+    static constexpr int EPC = EPI_WARPS == 8 ? BN / 2 : BN;            // columns of an epilogue thread
+    static constexpr int THREADS = 64 + 32 * EPI_WARPS;
+    static constexpr int OFF_BAR = NS * ST;
+    static constexpr int SMEM = OFF_BAR + 256 + 1024;                   // barriers; alignment slack
+    static constexpr int PART_LD = SWAP ? BM : BN + 4;                  // split: row length of the fp32 part
+    static_assert((SWAP ? BN * BM : BM * (BN + 4)) * 4 <= OFF_BAR, "the split's part fits in the stages");
+};
+}  // namespace fp8
+
+struct Fp8Maps {
+    CUtensorMap a, b;   // MMA rows (box 128 x 128 bytes) and columns (box 128 bytes x BN)
+};
+
+namespace {
+
+// kind::f8f6f4, e4m3 operands (format 0), fp32 result; both operands K-major.
+__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(umma::smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ float ld_cluster(uint32_t addr, int rank) {
+    uint32_t remote;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote));   // no clobber: loads overlap
+    return v;
+}
+
+__device__ __forceinline__ void store8v(__nv_bfloat16 *p, const float *x) {
+    uint4 u;
+    uint32_t *w = reinterpret_cast<uint32_t *>(&u);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
+        memcpy(w + e, &b, 4);
+    }
+    *reinterpret_cast<uint4 *>(p) = u;
+}
+__device__ __forceinline__ void store8v(float *p, const float *x) {
+    reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+
+}  // namespace
+
+template <class Sh, typename Tout>
+__global__ void __launch_bounds__(Sh::THREADS, 1)
+gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const float *__restrict__ a_scale,
+                const float *__restrict__ b_scale, Tout *__restrict__ C, long long ldc, int split) {
+    using namespace fp8;
+    constexpr int BN = Sh::BN, NS = Sh::NS, NT = Sh::NT, EPC = Sh::EPC;
+    constexpr bool SWAP = Sh::SWAP;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = umma::align_smem<1024>(smem_raw);
+    uint64_t *full = reinterpret_cast<uint64_t *>(sm + Sh::OFF_BAR), *empty = full + NS;
+    uint64_t *tfull = empty + NS, *tempty = tfull + NT, *mma_done = tempty + NT;
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(mma_done + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tslot + 1);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rows = SWAP ? N : M, cols = SWAP ? M : N;              // of the MMA's operands
+    const int tiles_r = (rows + BM - 1) / BM, tiles_c = (cols + BN - 1) / BN;
+    const int kbs = (K + BK - 1) / BK;
+    const long long n_tiles = (long long)tiles_r * tiles_c;
+    // split > 1: one tile per cluster, rank `part` takes K blocks [k_lo, k_hi)
+    const int part = split > 1 ? (int)(blockIdx.x % split) : 0;
+    const long long first = blockIdx.x / split, step = gridDim.x / split;
+    const int k_lo = (int)((long long)kbs * part / split), k_hi = (int)((long long)kbs * (part + 1) / split);
+
+    if (tid == 0) {
+        for (int i = 0; i < NS; ++i) {
+            umma::mbar_init(full + i, 1);
+            umma::mbar_init(empty + i, 1);
+        }
+        for (int i = 0; i < NT; ++i) {
+            umma::mbar_init(tfull + i, 1);
+            umma::mbar_init(tempty + i, Sh::EPI_WARPS);
+        }
+        umma::mbar_init(mma_done, 1);
+        *abort_flag = 0;
+        umma::fence_mbar_init();
+    }
+    if (warp == 1) umma::tmem_alloc(tslot, Sh::TMEM_COLS);
+    umma::tc_fence_before();
+    __syncthreads();
+    umma::tc_fence_after();
+    const uint32_t tbase = *tslot;
+
+    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+        if (*abort_flag) return false;
+        if (umma::mbar_wait_bounded(bar, parity, MAX_POLLS)) return true;
+        atomicOr(&g_fp8_err, 1u);
+        *abort_flag = 1;
+        return false;
+    };
+
+    if (warp == 0 && lane == 0) {
+        // ---------------------------------------------------------------- producer
+        umma::prefetch_tensormap(&maps.a);
+        umma::prefetch_tensormap(&maps.b);
+        int st = 0, issued = 0;
+        uint32_t ph = 1;
+        bool ok = true;
+        for (long long t = first; ok && t < n_tiles; t += step) {
+            const int tr = (int)(t % tiles_r), tc = (int)(t / tiles_r);
+            for (int kb = k_lo; kb < k_hi; ++kb) {
+                if (!(ok = wait(empty + st, ph))) break;
+                uint8_t *buf = sm + st * Sh::ST;
+                umma::mbar_expect_tx(full + st, Sh::ST);
+                umma::tma_load_3d(buf, &maps.a, BK * kb, 0, BM * tr, full + st);
+                umma::tma_load_3d(buf + Sh::A_ST, &maps.b, BK * kb, 0, BN * tc, full + st);
+                if (issued < NS) ++issued;
+                if (++st == NS) { st = 0; ph ^= 1; }
+            }
+        }
+        // after an abort, loads still in flight land before the CTA leaves
+        if (*abort_flag)
+            for (int i = 0; i < issued; ++i) {
+                if (--st < 0) { st = NS - 1; ph ^= 1; }
+                umma::mbar_wait_bounded(full + st, ph ^ 1, MAX_POLLS);
+            }
+    } else if (warp == 1 && lane == 0) {
+        // --------------------------------------------------------------- MMA issuer
+        const uint32_t idesc = umma::idesc_f16(BM, BN, false, false);   // format 0 is e4m3 in this kind
+        const uint32_t base = umma::smem_u32(sm);
+        int st = 0, ts = 0;
+        uint32_t ph = 0, tph = 1;
+        bool ok = true, any = false;
+        for (long long t = first; ok && t < n_tiles; t += step) {
+            for (int kb = k_lo; kb < k_hi; ++kb) {
+                if (!(ok = wait(tempty + ts, tph)) || !(ok = wait(full + st, ph))) break;
+                umma::tc_fence_after();
+                const uint64_t ad = umma::sw128_desc(base + st * Sh::ST, 16, 1024);
+                const uint64_t bd = umma::sw128_desc(base + st * Sh::ST + Sh::A_ST, 16, 1024);
+#pragma unroll
+                for (int ks = 0; ks < BK / 32; ++ks)   // 32 bytes of K: start address + 2 (units of 16)
+                    mma_e4m3(tbase + ts * BN, ad + 2 * ks, bd + 2 * ks, idesc, ks > 0);
+                umma::mma_commit(empty + st);
+                umma::mma_commit(tfull + ts);
+                any = true;
+                if (++st == NS) { st = 0; ph ^= 1; }
+                if (++ts == NT) { ts = 0; tph ^= 1; }
+            }
+        }
+        // after an abort the epilogue may not have waited for the last MMAs: they
+        // complete before the tensor memory is released
+        if (any && *abort_flag) {
+            umma::mma_commit(mma_done);
+            umma::mbar_wait_bounded(mma_done, 0, MAX_POLLS);
+        }
+    } else if (warp >= 2) {
+        // ----------------------------------------------------------------- epilogue
+        // TMEM lane quadrant warp % 4: one row of the tile per lane; with 8 warps the
+        // second four take the upper half of the columns
+        const int qd = warp & 3, c0 = Sh::EPI_WARPS == 8 ? EPC * ((warp - 2) >> 2) : 0;
+        const uint32_t trow = tbase + ((uint32_t)(32 * qd) << 16) + c0;
+        int ts = 0;
+        uint32_t tph = 0;
+        bool ok = true;
+        for (long long t = first; ok && t < n_tiles; t += step) {
+            const int tr = (int)(t % tiles_r), tc = (int)(t / tiles_r);
+            const int row = BM * tr + 32 * qd + lane, col0 = BN * tc + c0;
+            // scales of this thread: its row's, and its columns' (one block of 128, or
+            // in the swapped order one per column: lane j holds column j's and j + 32's)
+            const float *srow = nullptr, *scol = nullptr, *scol2 = nullptr;
+            if constexpr (!SWAP) {
+                if (row < M) srow = a_scale + (size_t)row * kbs;
+                if (col0 < N) scol = b_scale + (size_t)(col0 >> 7) * kbs;
+            } else {
+                srow = b_scale + (size_t)tr * kbs;
+                if (lane < BN && col0 + lane < M) scol = a_scale + (size_t)(col0 + lane) * kbs;
+                if (BN > 32 && col0 + 32 + lane < M) scol2 = a_scale + (size_t)(col0 + 32 + lane) * kbs;
+            }
+            float acc[EPC];
+#pragma unroll
+            for (int j = 0; j < EPC; ++j) acc[j] = 0.f;
+            auto fetch = [&](int kb, float &r, float &c, float &c2) {
+                const bool in = kb < k_hi;
+                r = in && srow ? __ldg(srow + kb) : 0.f;
+                c = in && scol ? __ldg(scol + kb) : 0.f;
+                c2 = in && scol2 ? __ldg(scol2 + kb) : 0.f;
+            };
+            float r, c, c2;
+            fetch(k_lo, r, c, c2);
+            for (int kb = k_lo; kb < k_hi; ++kb) {
+                const float s = r * c, s2 = r * c2;
+                ok = __all_sync(0xffffffffu, wait(tfull + ts, tph));
+                if (!ok) break;
+                umma::tc_fence_after();
+                fetch(kb + 1, r, c, c2);
+                constexpr int W = EPC < 32 ? EPC : 32;
+#pragma unroll
+                for (int j0 = 0; j0 < EPC; j0 += W) {
+                    uint32_t v[W];
+                    if constexpr (W == 32) umma::tmem_ld32_nowait(trow + ts * BN + j0, v);
+                    else umma::tmem_ld16_nowait(trow + ts * BN + j0, v);
+                    umma::tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < W; ++j) {
+                        const float f = SWAP ? __shfl_sync(0xffffffffu, j0 ? s2 : s, j) : s;
+                        acc[j0 + j] = fmaf(__uint_as_float(v[j]), f, acc[j0 + j]);
+                    }
+                }
+                umma::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive(tempty + ts);
+                if (++ts == NT) { ts = 0; tph ^= 1; }
+            }
+            if (!ok) break;
+            if (split > 1) {
+                // this rank's part, in the stages (every load and MMA of the tile is done)
+                float *buf = reinterpret_cast<float *>(sm);
+                if constexpr (SWAP) {
+#pragma unroll
+                    for (int j = 0; j < EPC; ++j) buf[j * Sh::PART_LD + 32 * qd + lane] = acc[j];
+                } else {
+                    float *p = buf + (32 * qd + lane) * Sh::PART_LD + c0;
+#pragma unroll
+                    for (int j = 0; j < EPC; j += 4)
+                        *reinterpret_cast<float4 *>(p + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+                }
+            } else if constexpr (SWAP) {
+                if (row < N) {
+#pragma unroll
+                    for (int j = 0; j < EPC; ++j)
+                        if (col0 + j < M) C[(col0 + j) * ldc + row] = from_f32<Tout>(acc[j]);
+                }
+            } else if (row < M) {
+                Tout *crow = C + row * ldc + col0;
+                if ((reinterpret_cast<uintptr_t>(crow) & 15) == 0 && col0 + EPC <= N) {
+#pragma unroll
+                    for (int j = 0; j < EPC; j += 8) store8v(crow + j, acc + j);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < EPC; ++j)
+                        if (col0 + j < N) crow[j] = from_f32<Tout>(acc[j]);
+                }
+            }
+        }
+    }
+    umma::tc_fence_before();
+    __syncwarp();
+    if (split > 1) {
+        cluster_sync();
+        const int tr = (int)(first % tiles_r), tc = (int)(first / tiles_r);
+        const uint32_t base = umma::smem_u32(sm);
+        // elements of the tile in the order of C's rows; rank `part` adds its share
+        constexpr int INNER = SWAP ? BM : BN, OUTER = SWAP ? BN : BM;
+        const int total = INNER * OUTER, lo = total / split * part, hi = part + 1 == split ? total : lo + total / split;
+        const bool whole = *abort_flag == 0;   // after an abort the parts are not complete: write nothing
+        for (int i = lo + tid; whole && i < hi; i += Sh::THREADS) {
+            const int o = i / INNER, in = i % INNER;
+            const long long m = SWAP ? (long long)BN * tc + o : (long long)BM * tr + o;
+            const long long n = SWAP ? (long long)BM * tr + in : (long long)BN * tc + in;
+            if (m < M && n < N) {
+                float v = 0.f;
+                for (int p = 0; p < split; ++p) v += ld_cluster(base + (uint32_t)(o * Sh::PART_LD + in) * 4, p);
+                C[m * ldc + n] = from_f32<Tout>(v);
+            }
+        }
+        __syncwarp();
+        cluster_sync();   // no CTA leaves while another still reads its part
+    } else {
+        __syncthreads();
+    }
+    if (warp == 1) umma::tmem_dealloc(tbase, Sh::TMEM_COLS);
+}
+
+namespace {
+
+template <class Sh, typename Tout>
+cudaError_t launch_shape(int M, int N, int K, const void *A, long long lda, const float *a_scale, const void *B,
+                         long long ldb, const float *b_scale, void *C, long long ldc, int split, int sms,
+                         cudaStream_t stream) {
+    Fp8Maps m;
+    std::memset(&m, 0, sizeof m);
+    cudaError_t e;
+    e = make_tma_mat_u8(reinterpret_cast<TmaMap *>(&m.a), Sh::SWAP ? B : A, K, Sh::SWAP ? N : M, Sh::SWAP ? ldb : lda,
+                        fp8::BM);
+    if (e != cudaSuccess) return e;
+    e = make_tma_mat_u8(reinterpret_cast<TmaMap *>(&m.b), Sh::SWAP ? A : B, K, Sh::SWAP ? M : N, Sh::SWAP ? lda : ldb,
+                        Sh::BN);
+    if (e != cudaSuccess) return e;
+    auto *kernel = gemm_fp8_kernel<Sh, Tout>;
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM)) != cudaSuccess)
+        return e;
+    const long long rows = Sh::SWAP ? N : M, cols = Sh::SWAP ? M : N;
+    const long long tiles = ((rows + fp8::BM - 1) / fp8::BM) * ((cols + Sh::BN - 1) / Sh::BN);
+    const long long grid = split > 1 ? tiles * split : tiles < sms ? tiles : sms;
+    if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(Sh::THREADS);
+    cfg.dynamicSmemBytes = Sh::SMEM;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&cfg, kernel, m, M, N, K, a_scale, b_scale, static_cast<Tout *>(C), ldc, split)) !=
+        cudaSuccess)
+        return e;
+    return launched();
+}
+
+template <typename Tout>
+cudaError_t launch_typed(int M, int N, int K, const void *A, long long lda, const float *a_scale, const void *B,
+                         long long ldb, const float *b_scale, void *C, long long ldc, cudaStream_t stream) {
+    int sms = 0;
+    cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    const int kbs = (K + fp8::BK - 1) / fp8::BK;
+    auto tiles = [&](long long rows, long long cols, int bn) { return ((rows + 127) / 128) * ((cols + bn - 1) / bn); };
+    // K split until the tiles cover the SMs, at least two K blocks per rank
+    auto split_for = [&](long long n) {
+        int s = 1;
+        while (s < 8 && n * s * 2 <= sms && kbs >= 4 * s) s *= 2;
+        return s;
+    };
+#define GDN_FP8(BN, SWAP, S)                                                                                       \
+    launch_shape<fp8::Shape<BN, SWAP>, Tout>(M, N, K, A, lda, a_scale, B, ldb, b_scale, C, ldc, S, sms, stream)
+    if (M <= 64) {
+        const int s = split_for(tiles(N, M, 64));
+        if (M <= 16) return GDN_FP8(16, true, s);
+        if (M <= 32) return GDN_FP8(32, true, s);
+        return GDN_FP8(64, true, s);
+    }
+    if (tiles(M, N, 256) >= sms) return GDN_FP8(256, false, 1);
+    if (tiles(M, N, 128) >= sms) return GDN_FP8(128, false, 1);
+    return GDN_FP8(64, false, split_for(tiles(M, N, 64)));
+#undef GDN_FP8
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_fp8(int M, int N, int K, const void *A, long long lda, const float *a_scale, const void *B,
+                            long long ldb, const float *b_scale, void *C, long long ldc, bool out_bf16,
+                            cudaStream_t stream) {
+    return out_bf16 ? launch_typed<__nv_bfloat16>(M, N, K, A, lda, a_scale, B, ldb, b_scale, C, ldc, stream)
+                    : launch_typed<float>(M, N, K, A, lda, a_scale, B, ldb, b_scale, C, ldc, stream);
+}
+
+// One CTA waits, through the product's bounded wait, for a barrier phase that
+// nothing completes.
+__global__ void fp8_wait_selftest_kernel(uint32_t max_polls) {
+    __shared__ uint64_t bar;
+    if (threadIdx.x == 0) {
+        umma::mbar_init(&bar, 1);
+        umma::fence_mbar_init();
+    }
+    __syncthreads();
+    if (threadIdx.x == 0 && !umma::mbar_wait_bounded(&bar, 0, max_polls)) atomicOr(&g_fp8_err, 1u);
+}
+
+cudaError_t fp8_wait_selftest(uint32_t max_polls, cudaStream_t s) {
+    fp8_wait_selftest_kernel<<<1, 32, 0, s>>>(max_polls);
+    return cudaGetLastError();
+}
+
+cudaError_t fp8_error_word(unsigned *v, bool clear, cudaStream_t s) { return read_error_word(g_fp8_err, v, clear, s); }
+
+}  // namespace gdn

@@ -1,0 +1,134 @@
+// K9a -- values to e4m3 with one fp32 scale per block of 1 x 128 or 128 x 128
+// elements:
+//   amax = max(max |x|, 2^-64) over the block,
+//   scale = amax / 448,  q = e4m3(x * (448 / amax))       (448 = largest e4m3 value)
+// with IEEE fp32 divisions and one rounding to nearest even, so the bytes are a
+// function of the values alone.  The lower bound of amax keeps 448 / amax finite (a
+// block of zeros gives zeros).  The maximum is taken over the bits of |x|, where a
+// NaN is larger than every number: a block with a NaN gets a NaN scale.
+//
+// Memory-bound: x read once, q written once.  Sixteen lanes hold the 128 columns of
+// one block row in 16-byte loads (8 elements a lane), so a row block needs four
+// shuffles; four row blocks per half warp are in flight at once.  The 128 x 128 block
+// stays in registers (64 values a thread) between its maximum and its conversion.
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include "gdn_device.cuh"
+#include "gdn_internal.h"
+
+namespace gdn {
+namespace {
+
+constexpr float kFp8Max = 448.f;
+constexpr float kTiny = 5.421010862427522e-20f;   // 2^-64
+
+__device__ __forceinline__ uint32_t amax8(const float (&x)[8]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(x[e]) & 0x7fffffffu);
+    return m;
+}
+
+__device__ __forceinline__ uint2 to_e4m3x8(const float (&x)[8], float inv) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        w[e] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * e] * inv, x[2 * e + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+    return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+}
+
+__device__ __forceinline__ float block_amax(uint32_t bits) {
+    return __uint_as_float(max(bits, __float_as_uint(kTiny)));
+}
+
+constexpr int QB = 4;   // row blocks per half warp
+
+template <typename T>
+__global__ void __launch_bounds__(256)
+quant_rows_kernel(const T *__restrict__ x, long long ld_x, long long n_blocks, int cols, int cb,
+                  uint8_t *__restrict__ q, long long ld_q, float *__restrict__ scale) {
+    const int sub = threadIdx.x & 15;
+    const long long first = ((long long)blockIdx.x * 16 + (threadIdx.x >> 4)) * QB;
+    float v[QB][8];
+#pragma unroll
+    for (int i = 0; i < QB; ++i) {
+        const long long b = first + i, r = b / cb;
+        const int c = (int)(b - r * cb) * 128 + 8 * sub;
+        if (b < n_blocks && c < cols) load8(x + r * ld_x + c, v[i]);
+        else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < QB; ++i) {
+        uint32_t m = amax8(v[i]);
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float amax = block_amax(m);
+        const long long b = first + i, r = b / cb;
+        const int c = (int)(b - r * cb) * 128 + 8 * sub;
+        if (b < n_blocks) {
+            if (sub == 0) scale[b] = __fdiv_rn(amax, kFp8Max);
+            if (c < cols) *reinterpret_cast<uint2 *>(q + r * ld_q + c) = to_e4m3x8(v[i], __fdiv_rn(kFp8Max, amax));
+        }
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256)
+quant_tiles_kernel(const T *__restrict__ x, long long ld_x, int rows, int cols, uint8_t *__restrict__ q,
+                   long long ld_q, float *__restrict__ scale) {
+    __shared__ uint32_t part[8];
+    const int sub = threadIdx.x & 15, c = blockIdx.x * 128 + 8 * sub;
+    const long long r0 = (long long)blockIdx.y * 128 + (threadIdx.x >> 4);
+    float v[8][8];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (r0 + 16 * i < rows && c < cols) load8(x + (r0 + 16 * i) * ld_x + c, v[i]);
+        else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, amax8(v[i]));
+    m = __reduce_max_sync(0xffffffffu, m);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w) m = max(m, part[w]);
+    const float amax = block_amax(m), inv = __fdiv_rn(kFp8Max, amax);
+    if (threadIdx.x == 0) scale[(size_t)blockIdx.y * gridDim.x + blockIdx.x] = __fdiv_rn(amax, kFp8Max);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (r0 + 16 * i < rows && c < cols)
+            *reinterpret_cast<uint2 *>(q + (r0 + 16 * i) * ld_q + c) = to_e4m3x8(v[i], inv);
+}
+
+template <typename T>
+cudaError_t launch_quant(int rows, int cols, const void *x, long long ld_x, int block_rows, void *q, long long ld_q,
+                         float *scale, cudaStream_t stream) {
+    const int cb = (cols + 127) / 128;
+    if (block_rows == 1) {
+        const long long n = (long long)rows * cb, per_cta = 16 * QB;
+        quant_rows_kernel<T><<<(unsigned)((n + per_cta - 1) / per_cta), 256, 0, stream>>>(
+            static_cast<const T *>(x), ld_x, n, cols, cb, static_cast<uint8_t *>(q), ld_q, scale);
+    } else {
+        quant_tiles_kernel<T><<<dim3(cb, (rows + 127) / 128), 256, 0, stream>>>(
+            static_cast<const T *>(x), ld_x, rows, cols, static_cast<uint8_t *>(q), ld_q, scale);
+    }
+    return launched();
+}
+
+}  // namespace
+
+cudaError_t launch_quant_fp8(int rows, int cols, const void *x, long long ld_x, bool bf16_in, int block_rows,
+                             void *q, long long ld_q, float *scale, cudaStream_t stream) {
+    return bf16_in ? launch_quant<bf16>(rows, cols, x, ld_x, block_rows, q, ld_q, scale, stream)
+                   : launch_quant<float>(rows, cols, x, ld_x, block_rows, q, ld_q, scale, stream);
+}
+
+}  // namespace gdn

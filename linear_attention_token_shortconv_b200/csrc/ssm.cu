@@ -1,0 +1,363 @@
+// The selective state-space mixer on fp32 arithmetic: the prefill of fp32 tensors
+// (and of bf16 tensors with an fp32 result), the single-token step, and the
+// convolution history that joins the two.  Per head h of group g = h / (H / G):
+//
+//   xh = SiLU(conv4(x) + b),  Bh, Ch likewise        (causal depthwise, width 4)
+//   D_t = softplus(dt_t + b_dt),  a_t = exp(-exp(A) D_t)
+//   S_t = a_t S_{t-1} + D_t Bh_t xh_t^T              [N, P], fp32
+//   y_t = S_t^T Ch_t + D xh_t,   out = y SiLU(z)
+//
+// The prefill is two kernels.  ssm_act writes the convolved channels and (D_t, a_t)
+// of every token in fp32; ssm_scan runs the recurrence with the state in registers.
+// A column p of the state depends on no other column, so a CTA takes 32 columns of
+// one (sequence, head): 128 threads, each two columns of N / 8 rows, 8 lanes of a
+// warp sharing the columns and adding their parts of y by shuffles.  What bounds it
+// is the chain of tokens: per token and warp 3 N / 4 fp32 instructions and N / 16
+// shared loads at one warp per scheduler.
+#include <cuda_runtime.h>
+
+#include "ssm.cuh"
+
+namespace gdn {
+using ssm::Raw;
+using ssm::load4;
+using ssm::seq_range;
+
+namespace {
+
+template <typename T> Raw<T> raw_of(const SsmArgs &a) {
+    return Raw<T>{static_cast<const T *>(a.x), static_cast<const T *>(a.B), static_cast<const T *>(a.C),
+                  a.ld_x, a.ld_B, a.ld_C, a.H * a.P, a.G * a.N};
+}
+
+constexpr int ACT_TOK = 16;   // consecutive tokens per thread of ssm_act
+
+// act [N_tok, channels] = SiLU(conv + bias); step [N_tok, H] = (D_t, a_t).
+// blockIdx.x: run of ACT_TOK packed tokens, blockIdx.y * 256 + threadIdx.x: four
+// channels, then (past the channels) one head.
+template <typename T>
+__global__ void __launch_bounds__(256)
+ssm_act_kernel(const Raw<T> raw, const T *__restrict__ hist, const float *__restrict__ conv_w,
+               const float *__restrict__ conv_b, const T *__restrict__ dt, long long ld_dt,
+               const float *__restrict__ A, const float *__restrict__ b_dt, const int32_t *__restrict__ cu, int n_seq,
+               int n_tok, int H, float *__restrict__ act, float2 *__restrict__ step) {
+    const int chans = raw.hp + 2 * raw.gn;
+    const int v = blockIdx.y * blockDim.x + threadIdx.x;
+    const int t0 = blockIdx.x * ACT_TOK, t1 = min(t0 + ACT_TOK, n_tok);
+    if (v >= chans / 4) {
+        const int h = v - chans / 4;
+        if (h >= H) return;
+        const float rate = expf(__ldg(A + h)), bias = __ldg(b_dt + h);
+        for (int t = t0; t < t1; ++t) {
+            const float d = softplus_acc(to_f32(dt[t * ld_dt + h]) + bias);
+            step[(size_t)t * H + h] = make_float2(d, expf(-rate * d));
+        }
+        return;
+    }
+    const int c = 4 * v;
+    float4 w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = __ldg(reinterpret_cast<const float4 *>(conv_w) + c + e);
+    const float4 b4 = conv_b ? __ldg(reinterpret_cast<const float4 *>(conv_b) + v) : make_float4(0, 0, 0, 0);
+    int n = cu ? seq_of_token(cu, n_seq, t0) : t0 / (n_tok / n_seq);
+    int begin, end;
+    seq_range(cu, n_seq, n_tok, n, begin, end);
+    float4 r[4];   // raw rows t - 3 .. t
+    bool fresh = true;
+    for (int t = t0; t < t1; ++t) {
+        while (t >= end && n + 1 < n_seq) {
+            seq_range(cu, n_seq, n_tok, ++n, begin, end);
+            fresh = true;
+        }
+        if (t < begin || t >= end) { fresh = true; continue; }   // behind the last sequence
+        if (fresh) {
+#pragma unroll
+            for (int j = 0; j < 3; ++j) {
+                const int u = t - 3 + j;
+                if (u >= begin) r[j + 1] = load4(raw.at(u, c));
+                else if (hist) r[j + 1] = load4(hist + ((size_t)n * 3 + (u - begin + 3)) * chans + c);
+                else r[j + 1] = make_float4(0, 0, 0, 0);
+            }
+            fresh = false;
+        }
+        r[0] = r[1]; r[1] = r[2]; r[2] = r[3];
+        r[3] = load4(raw.at(t, c));
+        float4 o;
+        o.x = ssm::silu(fmaf(w[0].w, r[3].x, fmaf(w[0].z, r[2].x, fmaf(w[0].y, r[1].x, fmaf(w[0].x, r[0].x, b4.x)))));
+        o.y = ssm::silu(fmaf(w[1].w, r[3].y, fmaf(w[1].z, r[2].y, fmaf(w[1].y, r[1].y, fmaf(w[1].x, r[0].y, b4.y)))));
+        o.z = ssm::silu(fmaf(w[2].w, r[3].z, fmaf(w[2].z, r[2].z, fmaf(w[2].y, r[1].z, fmaf(w[2].x, r[0].z, b4.z)))));
+        o.w = ssm::silu(fmaf(w[3].w, r[3].w, fmaf(w[3].z, r[2].w, fmaf(w[3].y, r[1].w, fmaf(w[3].x, r[0].w, b4.w)))));
+        *reinterpret_cast<float4 *>(act + (size_t)t * chans + c) = o;
+    }
+}
+
+constexpr int SCAN_COLS = 32, SCAN_TOK = 16;
+
+template <int N, typename T, typename Tout>
+__global__ void __launch_bounds__(128)
+ssm_scan_kernel(const float *__restrict__ act, const float2 *__restrict__ step, const float *__restrict__ Dw,
+                const T *__restrict__ z, long long ld_z, const float *S0, const int32_t *__restrict__ cu, int n_seq,
+                int n_tok, int H, int G, int P, Tout *__restrict__ out, float *S_final) {
+    constexpr int R = N / 8;             // state rows of a thread
+    __shared__ __align__(16) float bs[SCAN_TOK][N], cs[SCAN_TOK][N], xs[SCAN_TOK][SCAN_COLS];
+    __shared__ float2 ds[SCAN_TOK];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int p0 = blockIdx.x * SCAN_COLS, h = blockIdx.y, n = blockIdx.z;
+    const int slice = lane & 7, col = 8 * warp + 2 * (lane >> 3);   // rows 4 slice + 32 i + e, columns col, col + 1
+    const int chans = H * P + 2 * G * N, g = h / (H / G);
+    int begin, end;
+    seq_range(cu, n_seq, n_tok, n, begin, end);
+    const size_t sbase = ((size_t)n * H + h) * N * P + p0 + col;
+    float2 S[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int row = 32 * (i / 4) + 4 * slice + (i & 3);
+        S[i] = S0 ? *reinterpret_cast<const float2 *>(S0 + sbase + (size_t)row * P) : make_float2(0.f, 0.f);
+    }
+    const float dw = Dw ? __ldg(Dw + h) : 0.f;
+    for (int t0 = begin; t0 < end; t0 += SCAN_TOK) {
+        const int len = min(SCAN_TOK, end - t0);
+        __syncthreads();
+        for (int i = tid; i < len * (N / 4); i += 128) {
+            const int r = i / (N / 4), q = i % (N / 4);
+            const float *row = act + (size_t)(t0 + r) * chans + H * P + g * N + 4 * q;
+            *reinterpret_cast<float4 *>(&bs[r][4 * q]) = __ldg(reinterpret_cast<const float4 *>(row));
+            *reinterpret_cast<float4 *>(&cs[r][4 * q]) = __ldg(reinterpret_cast<const float4 *>(row + G * N));
+        }
+        for (int i = tid; i < len * (SCAN_COLS / 4); i += 128) {
+            const int r = i / (SCAN_COLS / 4), q = i % (SCAN_COLS / 4);
+            *reinterpret_cast<float4 *>(&xs[r][4 * q]) =
+                __ldg(reinterpret_cast<const float4 *>(act + (size_t)(t0 + r) * chans + h * P + p0 + 4 * q));
+        }
+        if (tid < len) ds[tid] = __ldg(step + (size_t)(t0 + tid) * H + h);
+        __syncthreads();
+        for (int r = 0; r < len; ++r) {
+            const float2 da = ds[r];
+            const float2 x = *reinterpret_cast<const float2 *>(&xs[r][col]);
+            const float2 dx = make_float2(da.x * x.x, da.x * x.y);
+            const float2 aa = make_float2(da.y, da.y);
+            float2 y = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int i4 = 0; i4 < R / 4; ++i4) {
+                const float4 b = *reinterpret_cast<const float4 *>(&bs[r][32 * i4 + 4 * slice]);
+                const float4 c = *reinterpret_cast<const float4 *>(&cs[r][32 * i4 + 4 * slice]);
+                const float bb[4] = {b.x, b.y, b.z, b.w}, cc[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float2 &s = S[4 * i4 + e];
+                    s = ffma2(aa, s, fmul2(make_float2(bb[e], bb[e]), dx));
+                    y = ffma2(make_float2(cc[e], cc[e]), s, y);
+                }
+            }
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) {
+                y.x += __shfl_xor_sync(0xffffffffu, y.x, o);
+                y.y += __shfl_xor_sync(0xffffffffu, y.y, o);
+            }
+            if (slice < 2) {   // lane `slice` of the eight writes column col + slice
+                const long long t = t0 + r;
+                float v = slice ? fmaf(dw, x.y, y.y) : fmaf(dw, x.x, y.x);
+                const int p = p0 + col + slice;
+                if (z) v *= ssm::silu(to_f32(z[t * ld_z + (long long)h * P + p]));
+                out[(t * H + h) * P + p] = from_f32<Tout>(v);
+            }
+        }
+    }
+    if (S_final) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int row = 32 * (i / 4) + 4 * slice + (i & 3);
+            *reinterpret_cast<float2 *>(S_final + sbase + (size_t)row * P) = S[i];
+        }
+    }
+}
+
+// tail [n, j] = the raw channels of token end - 3 + j of sequence n, or the row of
+// the older history that lies as far back (zeros without one).  A thread reads its
+// four channels' rows before it writes them, so tail may be the history itself.
+template <typename T>
+__global__ void __launch_bounds__(256)
+ssm_tail_kernel(const Raw<T> raw, const T *hist, const int32_t *__restrict__ cu, int n_seq, int n_tok, T *tail) {
+    const int chans = raw.hp + 2 * raw.gn, c = 4 * (blockIdx.x * blockDim.x + threadIdx.x), n = blockIdx.y;
+    if (c >= chans) return;
+    typedef typename std::conditional<sizeof(T) == 2, uint2, uint4>::type V;   // four raw elements
+    int begin, end;
+    seq_range(cu, n_seq, n_tok, n, begin, end);
+    V r[3];
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+        const int t = end - 3 + j;
+        if (t >= begin) r[j] = *reinterpret_cast<const V *>(raw.at(t, c));
+        else if (hist) r[j] = *reinterpret_cast<const V *>(hist + ((size_t)n * 3 + (t - begin + 3)) * chans + c);
+        else r[j] = V{};
+    }
+#pragma unroll
+    for (int j = 0; j < 3; ++j) *reinterpret_cast<V *>(tail + ((size_t)n * 3 + j) * chans + c) = r[j];
+}
+
+template <typename T>
+cudaError_t launch_tail(const SsmArgs &a) {
+    const int chans = a.H * a.P + 2 * a.G * a.N;
+    const dim3 grid((chans / 4 + 255) / 256, a.n_seq);
+    ssm_tail_kernel<T><<<grid, 256, 0, a.stream>>>(raw_of<T>(a), static_cast<const T *>(a.hist), a.cu_seqlens, a.n_seq,
+                                                   a.n_tok, static_cast<T *>(a.tail));
+    return launched();
+}
+
+template <int N, typename T, typename Tout>
+cudaError_t launch_scan(const SsmArgs &a, const float *act, const float2 *step) {
+    const dim3 grid(a.P / SCAN_COLS, a.H, a.n_seq);
+    ssm_scan_kernel<N, T, Tout><<<grid, 128, 0, a.stream>>>(act, step, a.D, static_cast<const T *>(a.z), a.ld_z, a.S0,
+                                                            a.cu_seqlens, a.n_seq, a.n_tok, a.H, a.G, a.P,
+                                                            static_cast<Tout *>(a.out), a.S_final);
+    return launched();
+}
+
+size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+template <typename T, typename Tout>
+cudaError_t launch_fp32(const SsmArgs &a, char *ws) {
+    const int chans = a.H * a.P + 2 * a.G * a.N;
+    float *act = reinterpret_cast<float *>(ws);
+    float2 *step = reinterpret_cast<float2 *>(ws + round256((size_t)a.n_tok * chans * 4));
+    if (a.n_tok > 0) {
+        const dim3 grid((a.n_tok + ACT_TOK - 1) / ACT_TOK, (chans / 4 + a.H + 255) / 256);
+        ssm_act_kernel<T><<<grid, 256, 0, a.stream>>>(raw_of<T>(a), static_cast<const T *>(a.hist), a.conv_w, a.conv_b,
+                                                      static_cast<const T *>(a.dt), a.ld_dt, a.A, a.b_dt,
+                                                      a.cu_seqlens, a.n_seq, a.n_tok, a.H, act, step);
+        const cudaError_t e = launched();
+        if (e != cudaSuccess) return e;
+    }
+    return a.N == 128 ? launch_scan<128, T, Tout>(a, act, step) : launch_scan<64, T, Tout>(a, act, step);
+}
+
+}  // namespace
+
+size_t ssm_workspace_bytes(const SsmArgs &a) {
+    const size_t chans = (size_t)a.H * a.P + 2 * (size_t)a.G * a.N;
+    return round256((size_t)a.n_tok * chans * 4) + round256((size_t)a.n_tok * a.H * 8);
+}
+
+cudaError_t launch_ssm_prefill(const SsmArgs &a, void *ws) {
+    cudaError_t e;
+    if (a.in_bf16) {
+        e = a.out_bf16 ? launch_fp32<bf16, bf16>(a, static_cast<char *>(ws))
+                       : launch_fp32<bf16, float>(a, static_cast<char *>(ws));
+    } else {
+        e = a.out_bf16 ? launch_fp32<float, bf16>(a, static_cast<char *>(ws))
+                       : launch_fp32<float, float>(a, static_cast<char *>(ws));
+    }
+    if (e != cudaSuccess || !a.tail) return e;
+    // last: every reader of the history has finished, so the tail may replace it
+    return a.in_bf16 ? launch_tail<bf16>(a) : launch_tail<float>(a);
+}
+
+// ------------------------------------------------------------------ one token
+
+namespace {
+
+constexpr int DEC_THREADS = 256;
+
+// One CTA per (head, sequence): the state's loads are issued first, the convolution
+// of the head's x channels and of its group's B and C runs while they are in
+// flight, then every element is updated, written back and added into y.  The
+// history of the x channels, which no other CTA reads, is shifted here; that of
+// B and C, which all heads of a group read, by ssm_shift after this kernel.
+template <int N, int P, typename T, typename Tout>
+__global__ void __launch_bounds__(DEC_THREADS)
+ssm_decode_kernel(const Raw<T> raw, const T *__restrict__ dt, long long ld_dt, const float *__restrict__ conv_w,
+                  const float *__restrict__ conv_b, T *hist, const float *__restrict__ A,
+                  const float *__restrict__ b_dt, const float *__restrict__ Dw, const T *__restrict__ z,
+                  long long ld_z, float *S, Tout *__restrict__ out, int H, int G) {
+    constexpr int F4 = P / 4, ROWS = DEC_THREADS / F4, NV = N / ROWS;
+    __shared__ __align__(16) float xs[P], bs[N], cs[N];
+    __shared__ __align__(16) float part[ROWS][P];
+    const int tid = threadIdx.x, h = blockIdx.x, b = blockIdx.y, g = h / (H / G);
+    const int chans = raw.hp + 2 * raw.gn;
+    float4 *Sh = reinterpret_cast<float4 *>(S + ((size_t)b * H + h) * N * P);
+    float4 s[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) s[i] = __ldcs(Sh + tid + i * DEC_THREADS);
+    const float d = softplus_acc(to_f32(dt[b * ld_dt + h]) + __ldg(b_dt + h));
+    const float a = expf(-expf(__ldg(A + h)) * d);
+    for (int i = tid; i < P + 2 * N; i += DEC_THREADS) {
+        const int c = i < P ? h * P + i : i < P + N ? raw.hp + g * N + (i - P) : raw.hp + raw.gn + g * N + (i - P - N);
+        const float4 w = __ldg(reinterpret_cast<const float4 *>(conv_w) + c);
+        T *hb = hist + (size_t)b * 3 * chans + c;
+        const T r0 = hb[0], r1 = hb[chans], r2 = hb[2 * (size_t)chans], r3 = *raw.at(b, c);
+        float v = conv_b ? __ldg(conv_b + c) : 0.f;
+        v = fmaf(w.w, to_f32(r3), fmaf(w.z, to_f32(r2), fmaf(w.y, to_f32(r1), fmaf(w.x, to_f32(r0), v))));
+        v = ssm::silu(v);
+        if (i < P) {
+            xs[i] = v;
+            hb[0] = r1; hb[chans] = r2; hb[2 * (size_t)chans] = r3;
+        } else if (i < P + N) bs[i - P] = d * v;
+        else cs[i - P - N] = v;
+    }
+    __syncthreads();
+    const int q = tid % F4, row0 = tid / F4;
+    const float4 x = *reinterpret_cast<const float4 *>(&xs[4 * q]);
+    float4 y = make_float4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int row = row0 + i * ROWS;
+        const float bb = bs[row], cc = cs[row];
+        s[i].x = fmaf(a, s[i].x, bb * x.x); y.x = fmaf(cc, s[i].x, y.x);
+        s[i].y = fmaf(a, s[i].y, bb * x.y); y.y = fmaf(cc, s[i].y, y.y);
+        s[i].z = fmaf(a, s[i].z, bb * x.z); y.z = fmaf(cc, s[i].z, y.z);
+        s[i].w = fmaf(a, s[i].w, bb * x.w); y.w = fmaf(cc, s[i].w, y.w);
+        __stcs(Sh + tid + i * DEC_THREADS, s[i]);
+    }
+    *reinterpret_cast<float4 *>(&part[row0][4 * q]) = y;
+    __syncthreads();
+    if (tid < P) {
+        float v = 0.f;
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) v += part[r][tid];
+        if (Dw) v = fmaf(__ldg(Dw + h), xs[tid], v);
+        if (z) v *= ssm::silu(to_f32(z[b * ld_z + (long long)h * P + tid]));
+        out[((size_t)b * H + h) * P + tid] = from_f32<Tout>(v);
+    }
+}
+
+// Shifts the history of the B and C channels by the current token, four channels a thread.
+template <typename T>
+__global__ void __launch_bounds__(128) ssm_shift_kernel(const Raw<T> raw, T *hist) {
+    typedef typename std::conditional<sizeof(T) == 2, uint2, uint4>::type V;
+    const int chans = raw.hp + 2 * raw.gn, c = raw.hp + 4 * (blockIdx.x * blockDim.x + threadIdx.x), b = blockIdx.y;
+    if (c >= chans) return;
+    T *hb = hist + (size_t)b * 3 * chans + c;
+    const V r1 = *reinterpret_cast<V *>(hb + chans), r2 = *reinterpret_cast<V *>(hb + 2 * (size_t)chans);
+    const V r3 = *reinterpret_cast<const V *>(raw.at(b, c));
+    *reinterpret_cast<V *>(hb) = r1;
+    *reinterpret_cast<V *>(hb + chans) = r2;
+    *reinterpret_cast<V *>(hb + 2 * (size_t)chans) = r3;
+}
+
+template <int N, int P, typename T, typename Tout>
+cudaError_t launch_decode_typed(const SsmArgs &a) {
+    T *hist = static_cast<T *>(const_cast<void *>(a.hist));
+    ssm_decode_kernel<N, P, T, Tout><<<dim3(a.H, a.n_seq), DEC_THREADS, 0, a.stream>>>(
+        raw_of<T>(a), static_cast<const T *>(a.dt), a.ld_dt, a.conv_w, a.conv_b, hist, a.A, a.b_dt, a.D,
+        static_cast<const T *>(a.z), a.ld_z, a.S_final, static_cast<Tout *>(a.out), a.H, a.G);
+    const cudaError_t e = launched();
+    if (e != cudaSuccess) return e;
+    ssm_shift_kernel<T><<<dim3((2 * a.G * a.N / 4 + 127) / 128, a.n_seq), 128, 0, a.stream>>>(raw_of<T>(a), hist);
+    return launched();
+}
+
+template <int N, int P>
+cudaError_t launch_decode_dims(const SsmArgs &a) {
+    if (a.in_bf16)
+        return a.out_bf16 ? launch_decode_typed<N, P, bf16, bf16>(a) : launch_decode_typed<N, P, bf16, float>(a);
+    return a.out_bf16 ? launch_decode_typed<N, P, float, bf16>(a) : launch_decode_typed<N, P, float, float>(a);
+}
+
+}  // namespace
+
+cudaError_t launch_ssm_decode(const SsmArgs &a) {
+    if (a.N == 128) return a.P == 128 ? launch_decode_dims<128, 128>(a) : launch_decode_dims<128, 64>(a);
+    return a.P == 128 ? launch_decode_dims<64, 128>(a) : launch_decode_dims<64, 64>(a);
+}
+
+}  // namespace gdn

@@ -1,0 +1,51 @@
+// Device helpers shared by the state-space mixer's kernels (ssm*.cu).
+#pragma once
+
+#include "gdn_device.cuh"
+#include "gdn_internal.h"
+
+namespace gdn {
+namespace ssm {
+
+// Tokens [begin, end) of sequence n: from cu_seqlens, clamped to [0, n_tok] and to
+// begin <= end so that a bad offset reads and writes nothing out of range, or
+// equal lengths.
+__device__ __forceinline__ void seq_range(const int32_t *__restrict__ cu, int n_seq, int n_tok, int n, int &begin,
+                                          int &end) {
+    if (cu) {
+        begin = min(max(__ldg(cu + n), 0), n_tok);
+        end = min(max(__ldg(cu + n + 1), begin), n_tok);
+    } else {
+        const int L = n_tok / n_seq;
+        begin = n * L;
+        end = begin + L;
+    }
+}
+
+// 4 consecutive elements as floats (8 bytes of bf16 or 16 bytes of fp32).
+__device__ __forceinline__ float4 load4(const float *p) { return __ldg(reinterpret_cast<const float4 *>(p)); }
+__device__ __forceinline__ float4 load4(const bf16 *p) {
+    const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
+    return make_float4(bf16lo(u.x), bf16hi(u.x), bf16lo(u.y), bf16hi(u.y));
+}
+
+// SiLU with the full-precision exponential: the state takes its inputs from here
+// and is held to fp32 accuracy.  x = -inf gives 0 * inf = NaN as in the formula.
+__device__ __forceinline__ float silu(float x) { return x / (1.0f + expf(-x)); }
+
+// The mixer's channels [x (H P) | B (G N) | C (G N)] and their three raw sources.
+template <typename T> struct Raw {
+    const T *x, *B, *C;
+    long long ld_x, ld_B, ld_C;
+    int hp, gn;
+    // the raw row element of channel c of token t; vector loads of channels stay
+    // inside one source because hp and gn are multiples of 64
+    __device__ __forceinline__ const T *at(long long t, int c) const {
+        if (c < hp) return x + t * ld_x + c;
+        if (c < hp + gn) return B + t * ld_B + (c - hp);
+        return C + t * ld_C + (c - hp - gn);
+    }
+};
+
+}  // namespace ssm
+}  // namespace gdn

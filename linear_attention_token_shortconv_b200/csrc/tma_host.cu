@@ -109,4 +109,21 @@ cudaError_t make_tma_mat_bf16(TmaMap *out, const void *base, int inner, int rows
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// A row-major matrix of bytes [rows][inner] with leading dimension ld (a multiple of
+// 16) as a 3-D map {inner, 1, rows}, boxes {128, 1, box_rows}, 128-byte swizzle.
+// Bytes outside the matrix read as zero.
+cudaError_t make_tma_mat_u8(TmaMap *out, const void *base, int inner, int rows, long long ld, int box_rows) {
+    EncodeTiledFn fn;
+    cudaError_t e = encoder(&fn);
+    if (e != cudaSuccess) return e;
+    const cuuint64_t dims[3] = {(cuuint64_t)inner, 1, (cuuint64_t)rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld, (cuuint64_t)ld};
+    const cuuint32_t box[3] = {128, 1, (cuuint32_t)box_rows};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(reinterpret_cast<CUtensorMap *>(out->bytes), CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
+                    const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 }  // namespace gdn

@@ -28,8 +28,9 @@ EXPORTS = ("gdn_prefill", "gdn_prefill_workspace_size", "gdn_decode_step", "gdn_
            "gdn_selftest_wait_timeout", "gdn_decode_multi", "gdn_prefill_backward",
            "gdn_prefill_backward_workspace_size", "gdn_qsa_indexer", "gdn_qsa_indexer_workspace_size",
            "gdn_layer_forward", "gdn_layer_workspace_size", "gdn_prefill_ws", "gdn_prefill_conv_tail",
-           "gdn_gemm_bf16")
-ERRF_PREP, ERRF_CHAIN, ERRF_DECODE, ERRF_QSA, ERRF_GEMM = 1, 2, 4, 8, 16
+           "gdn_gemm_bf16", "gdn_ssm_prefill", "gdn_ssm_prefill_workspace_size", "gdn_ssm_decode_step",
+           "gdn_quant_fp8", "gdn_gemm_fp8")
+ERRF_PREP, ERRF_CHAIN, ERRF_DECODE, ERRF_QSA, ERRF_GEMM, ERRF_FP8 = 1, 2, 4, 8, 16, 64
 
 
 class GdnError(RuntimeError):
@@ -43,6 +44,12 @@ class Dims(ctypes.Structure):
                 ("H", ctypes.c_int32), ("dk", ctypes.c_int32), ("dv", ctypes.c_int32),
                 ("conv_k", ctypes.c_int32), ("in_dtype", ctypes.c_int32),
                 ("out_dtype", ctypes.c_int32)]
+
+
+class SsmDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_seqs", "total_tokens", "H", "G", "P", "N", "conv_k", "in_dtype",
+                                              "out_dtype")] + \
+               [(n, ctypes.c_int64) for n in ("ld_x", "ld_B", "ld_C", "ld_z", "ld_dt")]
 
 
 _lib = None
@@ -100,6 +107,17 @@ def load() -> ctypes.CDLL:
         lib.gdn_status_string.restype = ctypes.c_char_p
         lib.gdn_prefill_ws.argtypes = [D] + [P] * 15 + [ctypes.c_size_t, P]
         lib.gdn_prefill_ws.restype = ctypes.c_int
+        SD, I, L = ctypes.POINTER(SsmDims), ctypes.c_int, ctypes.c_int64
+        lib.gdn_ssm_prefill.argtypes = [SD] + [P] * 17
+        lib.gdn_ssm_prefill.restype = ctypes.c_int
+        lib.gdn_ssm_prefill_workspace_size.argtypes = [SD, ctypes.POINTER(ctypes.c_size_t)]
+        lib.gdn_ssm_prefill_workspace_size.restype = ctypes.c_int
+        lib.gdn_ssm_decode_step.argtypes = [SD] + [P] * 14
+        lib.gdn_ssm_decode_step.restype = ctypes.c_int
+        lib.gdn_quant_fp8.argtypes = [I, I, P, L, I, I, P, L, P, P]
+        lib.gdn_quant_fp8.restype = ctypes.c_int
+        lib.gdn_gemm_fp8.argtypes = [I, I, I, P, L, P, P, L, P, P, L, I, P]
+        lib.gdn_gemm_fp8.restype = ctypes.c_int
         lib.gdn_prefill_conv_tail.argtypes = [D] + [P] * 6
         lib.gdn_prefill_conv_tail.restype = ctypes.c_int
         _lib = lib
@@ -500,6 +518,174 @@ def decode_multi(q, k, v, conv_w, conv_hist, a_logit, b_logit, A, b_alpha, z, no
                                      _ptr(z), _ptr(norm_w), _ptr(S), _ptr(out), _ptr(n_keep),
                                      _stream(stream))
     _check(rc, "gdn_decode_multi")
+    return out
+
+
+def _token_ld(name, t, shape, dtype):
+    """Elements from one token of `t` to the next, after checking its shape and dtype.
+    Tokens may lie apart (a column block of a projection result); within a token the
+    elements must be packed."""
+    _expect(name, t, shape, dtype)
+    want = 1
+    for n, st in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if n != 1 and st != want:
+            raise ValueError(f"{name}: the elements of a token must be packed (strides {t.stride()})")
+        want *= n
+    if t.shape[0] <= 1:
+        return 0
+    if t.stride(0) < want:
+        raise ValueError(f"{name}: tokens overlap (strides {t.stride()})")
+    return t.stride(0)
+
+
+def _raw(t):
+    """Address of a strided tensor whose layout has been checked (None: absent)."""
+    return None if t is None or not t.numel() else t.data_ptr()
+
+
+def _ssm_dims(x, B, C, dt_logit, conv_w, conv_b, A, b_dt, D, z, out, n_seq):
+    if x.dim() != 3 or B.dim() != 3:
+        raise ValueError("x [N_tok, H, P] and B, C [N_tok, G, N] expected")
+    n_tok, H, P = x.shape
+    G, N = B.shape[1:]
+    if x.dtype not in (BF16, F32):
+        raise TypeError(f"x: dtype {x.dtype}, expected {BF16} or {F32}")
+    chans = H * P + 2 * G * N
+    lds = [_token_ld("x", x, (n_tok, H, P), x.dtype), _token_ld("B", B, (n_tok, G, N), x.dtype),
+           _token_ld("C", C, (n_tok, G, N), x.dtype),
+           0 if z is None else _token_ld("z", z, (n_tok, H, P), x.dtype),
+           _token_ld("dt_logit", dt_logit, (n_tok, H), x.dtype)]
+    _expect("conv_w", conv_w, (chans, None), F32)
+    _expect("conv_b", conv_b, (chans,), F32)
+    _expect("A", A, (H,), F32)
+    _expect("b_dt", b_dt, (H,), F32)
+    _expect("D", D, (H,), F32)
+    _expect("out", out, (n_tok, H, P), (F32, BF16))
+    return SsmDims(n_seq, n_tok, H, G, P, N, conv_w.shape[1], _dt(x), _dt(out), *lds), chans
+
+
+def ssm_prefill(x, B, C, dt_logit, conv_w, A, b_dt, *, conv_b=None, D=None, z=None, S0=None, conv_hist=None,
+                cu_seqlens=None, num_seqs=None, out=None, S_final=None, conv_tail=None, out_dtype=None,
+                want_state=True, stream=None):
+    """gdn_ssm_prefill on torch tensors: x, z [N_tok, H, P], B, C [N_tok, G, N],
+    dt_logit [N_tok, H] (tokens may lie apart, e.g. column blocks of one projection);
+    out_dtype defaults to x.dtype.  S_final may be S0 and conv_tail conv_hist.
+
+    Returns (out [N_tok, H, P], S_final [N_seq, H, N, P] or None, conv_tail [N_seq, 3,
+    H P + 2 G N] or None); the last two are made unless want_state is False."""
+    if cu_seqlens is not None:
+        n_seq = cu_seqlens.shape[0] - 1
+    else:
+        n_seq = num_seqs if num_seqs is not None else (S0.shape[0] if S0 is not None else 1)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
+    dims, chans = _ssm_dims(x, B, C, dt_logit, conv_w, conv_b, A, b_dt, D, z, out, n_seq)
+    state, hist = (n_seq, dims.H, dims.N, dims.P), (n_seq, 3, chans)
+    if want_state:
+        if S_final is None:
+            S_final = torch.empty(state, dtype=F32, device=x.device)
+        if conv_tail is None:
+            conv_tail = torch.empty(hist, dtype=x.dtype, device=x.device)
+    _expect("S0", S0, state, F32)
+    _expect("S_final", S_final, state, F32)
+    _expect("conv_hist", conv_hist, hist, x.dtype)
+    _expect("conv_tail", conv_tail, hist, x.dtype)
+    _expect("cu_seqlens", cu_seqlens, (n_seq + 1,), I32)
+    with torch.cuda.device(_device(x, B, C, dt_logit, conv_w, conv_b, A, b_dt, D, z, S0, conv_hist, cu_seqlens, out,
+                                   S_final, conv_tail)):
+        rc = load().gdn_ssm_prefill(ctypes.byref(dims), _raw(x), _raw(B), _raw(C), _raw(dt_logit), _ptr(conv_w),
+                                    _ptr(conv_b), _ptr(A), _ptr(b_dt), _ptr(D), _raw(z), _ptr(S0), _ptr(conv_hist),
+                                    _ptr(cu_seqlens), _ptr(out), _ptr(S_final), _ptr(conv_tail), _stream(stream))
+    _check(rc, "gdn_ssm_prefill")
+    return out, S_final, conv_tail
+
+
+def ssm_prefill_workspace_size(n_seq, n_tok, H, G, P, N, in_dtype=torch.bfloat16, out_dtype=None) -> int:
+    code = {BF16: GDN_BF16, F32: GDN_F32}
+    dims = SsmDims(n_seq, n_tok, H, G, P, N, 4, code[in_dtype], code[in_dtype if out_dtype is None else out_dtype])
+    n = ctypes.c_size_t(0)
+    _check(load().gdn_ssm_prefill_workspace_size(ctypes.byref(dims), ctypes.byref(n)),
+           "gdn_ssm_prefill_workspace_size")
+    return int(n.value)
+
+
+def ssm_decode_step(x, B, C, dt_logit, conv_w, conv_hist, A, b_dt, S, *, conv_b=None, D=None, z=None, out=None,
+                    out_dtype=None, stream=None):
+    """gdn_ssm_decode_step on torch tensors: x, z [B, H, P], B, C [B, G, N], dt_logit
+    [B, H] (rows may lie apart); conv_hist [B, 3, H P + 2 G N] and S [B, H, N, P] advance
+    in place.  out_dtype defaults to x.dtype.  Returns out [B, H, P]."""
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
+    dims, chans = _ssm_dims(x, B, C, dt_logit, conv_w, conv_b, A, b_dt, D, z, out, x.shape[0])
+    _expect("conv_hist", conv_hist, (dims.num_seqs, 3, chans), x.dtype)
+    _expect("S", S, (dims.num_seqs, dims.H, dims.N, dims.P), F32)
+    with torch.cuda.device(_device(x, B, C, dt_logit, conv_w, conv_b, conv_hist, A, b_dt, D, z, S, out)):
+        rc = load().gdn_ssm_decode_step(ctypes.byref(dims), _raw(x), _raw(B), _raw(C), _raw(dt_logit), _ptr(conv_w),
+                                        _ptr(conv_b), _ptr(conv_hist), _ptr(A), _ptr(b_dt), _ptr(D), _raw(z),
+                                        _ptr(S), _ptr(out), _stream(stream))
+    _check(rc, "gdn_ssm_decode_step")
+    return out
+
+
+E4M3 = torch.float8_e4m3fn
+
+
+def _matrix_ld(name, t, shape, dtypes):
+    """Row stride of a matrix with packed rows, after checking its shape and dtype."""
+    _expect(name, t, shape, dtypes)
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: rows must be contiguous (strides {t.stride()})")
+    if t.shape[0] <= 1:
+        return -(-t.shape[1] // 16) * 16   # one row: any pitch will do
+    if t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name}: rows overlap (strides {t.stride()})")
+    return t.stride(0)
+
+
+def quant_fp8(x, block_rows=1, *, q=None, scale=None, stream=None):
+    """gdn_quant_fp8 on torch tensors: x [rows, cols] bf16 or fp32 (rows may lie apart),
+    block_rows 1 (activations) or 128 (weights).
+
+    Returns (q [rows, cols] float8_e4m3fn, scale [ceil(rows / block_rows), ceil(cols /
+    128)] fp32) with x ~ q * scale of its block."""
+    if x.dim() != 2:
+        raise ValueError("x [rows, cols] expected")
+    rows, cols = x.shape
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows: 1 or 128 expected")
+    shape = (-(-rows // block_rows), -(-cols // 128))
+    if q is None:
+        q = torch.empty((rows, cols), dtype=E4M3, device=x.device)
+    if scale is None:
+        scale = torch.empty(shape, dtype=F32, device=x.device)
+    ld_x, ld_q = _matrix_ld("x", x, (rows, cols), (BF16, F32)), _matrix_ld("q", q, (rows, cols), E4M3)
+    _expect("scale", scale, shape, F32)
+    with torch.cuda.device(_device(x, q, scale)):
+        rc = load().gdn_quant_fp8(rows, cols, _raw(x), ld_x, _dt(x), block_rows, _raw(q), ld_q, _ptr(scale),
+                                  _stream(stream))
+    _check(rc, "gdn_quant_fp8")
+    return q, scale
+
+
+def gemm_fp8(a, a_scale, b, b_scale, *, out=None, out_dtype=torch.bfloat16, stream=None):
+    """gdn_gemm_fp8 on torch tensors: a [M, K] and b [N, K] float8_e4m3fn (rows may lie
+    apart), a_scale [M, ceil(K / 128)], b_scale [ceil(N / 128), ceil(K / 128)] fp32, as
+    quant_fp8 makes them with block_rows 1 and 128.  Returns a b^T [M, N] (bf16 or fp32)."""
+    if a.dim() != 2 or b.dim() != 2:
+        raise ValueError("a [M, K] and b [N, K] expected")
+    M, K = a.shape
+    N = b.shape[0]
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=a.device)
+    lda, ldb = _matrix_ld("a", a, (M, K), E4M3), _matrix_ld("b", b, (N, K), E4M3)
+    ldc = _matrix_ld("out", out, (M, N), (BF16, F32))
+    kb = -(-K // 128)
+    _expect("a_scale", a_scale, (M, kb), F32)
+    _expect("b_scale", b_scale, (-(-N // 128), kb), F32)
+    with torch.cuda.device(_device(a, a_scale, b, b_scale, out)):
+        rc = load().gdn_gemm_fp8(M, N, K, _raw(a), lda, _ptr(a_scale), _raw(b), ldb, _ptr(b_scale), _raw(out), ldc,
+                                 _dt(out), _stream(stream))
+    _check(rc, "gdn_gemm_fp8")
     return out
 
 
