@@ -391,8 +391,11 @@ typedef struct {
  * bytes (GDN_ERR_ALIGNMENT otherwise); dt_logit, A, b_dt, D, cu_seqlens aligned to
  * their elements.  Token tensors may be NULL when total_tokens is 0.  Sequences and
  * heads up to 65535 (GDN_ERR_UNSUPPORTED above).
- * All arithmetic and the state are fp32.  Stream-ordered workspace of
- * gdn_ssm_prefill_workspace_size() bytes from the library's pool.
+ * The state is held to fp32 on every path.  With bf16 tensors and a bf16 result the
+ * products of y take fp16-rounded operands with fp32 sums (chunks of 64 tokens on the
+ * tensor cores); otherwise all arithmetic is fp32.  Up to four kernels on `stream`, and
+ * a stream-ordered workspace of at most gdn_ssm_prefill_workspace_size() bytes from the
+ * library's pool.  An expired wait raises GDN_ERRF_SSM.
  */
 GDN_API gdn_status_t gdn_ssm_prefill(const gdn_ssm_dims_t *dims, const void *x, const void *B, const void *C,
                                      const void *dt_logit, const float *conv_w, const float *conv_b,
@@ -553,6 +556,7 @@ GDN_API int gdn_last_call_slots(void);
 #define GDN_ERRF_QSA 8u     /* QSA indexer score kernel (gdn_qsa_indexer) */
 #define GDN_ERRF_GEMM 16u   /* projection GEMMs (gdn_layer_forward) */
 #define GDN_ERRF_FP8 64u    /* 8-bit product (gdn_gemm_fp8) */
+#define GDN_ERRF_SSM 128u   /* state-space mixer, tensor-core path (gdn_ssm_prefill) */
 
 /*
  * gdn_device_error_status -- reads the current device's error words into

@@ -41,7 +41,7 @@ GDN_API gdn_status_t gdn_selftest_umma(int a_mn, int b_mn, int negate_a, int N, 
  * usable.
  *
  *   family     GDN_ERRF_PREP, GDN_ERRF_CHAIN, GDN_ERRF_DECODE, GDN_ERRF_QSA,
- *              GDN_ERRF_GEMM or GDN_ERRF_FP8 (one bit)
+ *              GDN_ERRF_GEMM, GDN_ERRF_FP8 or GDN_ERRF_SSM (one bit)
  *   max_polls  1 .. 65536
  *
  * Asynchronous on `stream`.  GDN_ERR_INVALID_ARG for another family value or

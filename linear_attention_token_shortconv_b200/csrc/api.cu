@@ -317,17 +317,19 @@ int gdn_last_call_slots(void) { return tl_slots; }
 
 gdn_status_t gdn_device_error_status(unsigned *flags, int clear, gdn_stream_t stream) {
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    unsigned w[6] = {0, 0, 0, 0, 0, 0};
+    unsigned w[7] = {0, 0, 0, 0, 0, 0, 0};
     cudaError_t e = gdn::prep_error_word(&w[0], clear != 0, s);
     if (e == cudaSuccess) e = gdn::chain_error_word(&w[1], clear != 0, s);
     if (e == cudaSuccess) e = gdn::decode_error_word(&w[2], clear != 0, s);
     if (e == cudaSuccess) e = gdn::qsa_error_word(&w[3], clear != 0, s);
     if (e == cudaSuccess) e = gdn::gemm_error_word(&w[4], clear != 0, s);
     if (e == cudaSuccess) e = gdn::fp8_error_word(&w[5], clear != 0, s);
+    if (e == cudaSuccess) e = gdn::ssm_error_word(&w[6], clear != 0, s);
     if (e != cudaSuccess) return GDN_ERR_CUDA;
     const unsigned f = (w[0] ? GDN_ERRF_PREP : 0u) | (w[1] ? GDN_ERRF_CHAIN : 0u) |
                        (w[2] ? GDN_ERRF_DECODE : 0u) | (w[3] ? GDN_ERRF_QSA : 0u) |
-                       (w[4] ? GDN_ERRF_GEMM : 0u) | (w[5] ? GDN_ERRF_FP8 : 0u);
+                       (w[4] ? GDN_ERRF_GEMM : 0u) | (w[5] ? GDN_ERRF_FP8 : 0u) |
+                       (w[6] ? GDN_ERRF_SSM : 0u);
     if (flags) *flags = f;
     return f ? GDN_ERR_TIMEOUT : GDN_OK;
 }
@@ -855,7 +857,16 @@ gdn_status_t gdn_ssm_prefill_workspace_size(const gdn_ssm_dims_t *dims, size_t *
     const gdn_status_t st = ssm_dims(dims, false, &a);
     if (st != GDN_OK) return st;
     if (!bytes) return GDN_ERR_INVALID_ARG;
-    *bytes = gdn::ssm_workspace_bytes(a);
+    int sms = 0;
+    if (gdn::sm_count(&sms) != cudaSuccess) {   // no device: the B200's
+        cudaGetLastError();
+        sms = 148;
+    }
+    // offsets may or may not be given: the larger of the two plans
+    static const int32_t some = 0;
+    *bytes = gdn::ssm_workspace_bytes(a, sms);
+    a.cu_seqlens = &some;
+    *bytes = max(*bytes, gdn::ssm_workspace_bytes(a, sms));
     return GDN_OK;
 }
 
@@ -879,7 +890,9 @@ gdn_status_t gdn_ssm_prefill(const gdn_ssm_dims_t *dims, const void *x, const vo
     a.tail = conv_tail;
     a.stream = reinterpret_cast<cudaStream_t>(stream);
     if ((st = ssm_pointers(a)) != GDN_OK) return st;
-    const size_t ws_bytes = gdn::ssm_workspace_bytes(a);
+    int sms = 0;
+    if (gdn::sm_count(&sms) != cudaSuccess) return GDN_ERR_CUDA;
+    const size_t ws_bytes = gdn::ssm_workspace_bytes(a, sms);
     char *ws = nullptr;
     if (ws_bytes > 0) {
         cudaMemPool_t pool;
@@ -888,7 +901,7 @@ gdn_status_t gdn_ssm_prefill(const gdn_ssm_dims_t *dims, const void *x, const vo
             return GDN_ERR_CUDA;
     }
     cudaError_t e = record(g_ev_begin, a.stream);
-    if (e == cudaSuccess) e = gdn::launch_ssm_prefill(a, ws);
+    if (e == cudaSuccess) e = gdn::launch_ssm_prefill(a, ws, sms);
     if (e == cudaSuccess) e = record(g_ev_end, a.stream);
     if (ws) {
         const cudaError_t ef = cudaFreeAsync(ws, a.stream);

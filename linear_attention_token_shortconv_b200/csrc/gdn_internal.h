@@ -156,8 +156,14 @@ struct SsmArgs {
     void *tail;
     cudaStream_t stream;
 };
-size_t ssm_workspace_bytes(const SsmArgs &a);
-cudaError_t launch_ssm_prefill(const SsmArgs &a, void *ws);
+size_t ssm_workspace_bytes(const SsmArgs &a, int sms);
+cudaError_t launch_ssm_prefill(const SsmArgs &a, void *ws, int sms);
+// the chunked tensor-core prefill (bf16 tensors)
+bool ssm_tc_supported(const SsmArgs &a);
+size_t ssm_tc_workspace_bytes(const SsmArgs &a, int sms);
+cudaError_t launch_ssm_tc(const SsmArgs &a, void *ws, int sms);
+cudaError_t ssm_error_word(unsigned *v, bool clear, cudaStream_t s);
+cudaError_t ssm_wait_selftest(uint32_t max_polls, cudaStream_t s);
 cudaError_t launch_ssm_decode(const SsmArgs &a);
 
 // K9: e4m3 values with one fp32 scale per 1 x 128 (block_rows = 1) or 128 x 128

@@ -233,17 +233,17 @@ cudaError_t launch_fp32(const SsmArgs &a, char *ws) {
 
 }  // namespace
 
-size_t ssm_workspace_bytes(const SsmArgs &a) {
+size_t ssm_workspace_bytes(const SsmArgs &a, int sms) {
+    if (ssm_tc_supported(a)) return ssm_tc_workspace_bytes(a, sms);
     const size_t chans = (size_t)a.H * a.P + 2 * (size_t)a.G * a.N;
     return round256((size_t)a.n_tok * chans * 4) + round256((size_t)a.n_tok * a.H * 8);
 }
 
-cudaError_t launch_ssm_prefill(const SsmArgs &a, void *ws) {
+cudaError_t launch_ssm_prefill(const SsmArgs &a, void *ws, int sms) {
     cudaError_t e;
-    if (a.in_bf16) {
-        e = a.out_bf16 ? launch_fp32<bf16, bf16>(a, static_cast<char *>(ws))
-                       : launch_fp32<bf16, float>(a, static_cast<char *>(ws));
-    } else {
+    if (ssm_tc_supported(a)) e = launch_ssm_tc(a, ws, sms);
+    else if (a.in_bf16) e = launch_fp32<bf16, float>(a, static_cast<char *>(ws));
+    else {
         e = a.out_bf16 ? launch_fp32<float, bf16>(a, static_cast<char *>(ws))
                        : launch_fp32<float, float>(a, static_cast<char *>(ws));
     }

@@ -30,7 +30,7 @@ EXPORTS = ("gdn_prefill", "gdn_prefill_workspace_size", "gdn_decode_step", "gdn_
            "gdn_layer_forward", "gdn_layer_workspace_size", "gdn_prefill_ws", "gdn_prefill_conv_tail",
            "gdn_gemm_bf16", "gdn_ssm_prefill", "gdn_ssm_prefill_workspace_size", "gdn_ssm_decode_step",
            "gdn_quant_fp8", "gdn_gemm_fp8")
-ERRF_PREP, ERRF_CHAIN, ERRF_DECODE, ERRF_QSA, ERRF_GEMM, ERRF_FP8 = 1, 2, 4, 8, 16, 64
+ERRF_PREP, ERRF_CHAIN, ERRF_DECODE, ERRF_QSA, ERRF_GEMM, ERRF_FP8, ERRF_SSM = 1, 2, 4, 8, 16, 64, 128
 
 
 class GdnError(RuntimeError):
