@@ -820,6 +820,7 @@ gdn_status_t ssm_dims(const gdn_ssm_dims_t *d, bool step, gdn::SsmArgs *a) {
     const int64_t vec = a->in_bf16 ? 8 : 4;   // elements of 16 bytes
     for (int i = 0; i < 5; ++i) {
         if (given[i] < 0 || (given[i] > 0 && given[i] < packed[i])) return GDN_ERR_INVALID_ARG;
+        if (given[i] > (int64_t)1 << 30) return GDN_ERR_UNSUPPORTED;   // strides of the tensor maps
         *ld[i] = given[i] ? given[i] : packed[i];
         if (i < 4 && *ld[i] % vec != 0) return GDN_ERR_ALIGNMENT;
     }

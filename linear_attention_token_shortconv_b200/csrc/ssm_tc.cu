@@ -33,6 +33,7 @@ using ssm::seq_range;
 
 namespace stc {
 constexpr int Q = 64;             // tokens per chunk
+constexpr int PREP_THREADS = 512;
 constexpr int REC = 336;          // floats of one (chunk, head) record
 // record: L log2 e [64] | u [64] | u e^R [64] | 2^ec e^L [64] | 2^ec umax [64] | e^L_end, umax
 constexpr int R_L = 0, R_U = 64, R_W = 128, R_YI = 192, R_YW = 256, R_DEC = 320, R_UMAX = 321;
@@ -62,7 +63,39 @@ __device__ __forceinline__ void scale_pow2(uint32_t max_bits, int top, float &sc
     inv = __uint_as_float((uint32_t)(254 - s) << 23);
 }
 
-__device__ __forceinline__ float silu_fast(float x) { return __fdividef(x, 1.0f + __expf(-x)); }
+// 2^x and 1 / x on the special-function unit, 2 units in the last place each;
+// subnormal results and arguments are flushed (decays below 2^-126 are nothing).
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// x / (1 + e^-x): x = -inf gives -inf * 0 = NaN as the formula does
+__device__ __forceinline__ float silu_fast(float x) { return x * rcp(1.0f + ex2(-stc::kLog2e * x)); }
+
+__device__ __forceinline__ float2 half2_float2(uint32_t h) {
+    __half2 p;
+    *reinterpret_cast<uint32_t *>(&p) = h;
+    return __half22float2(p);
+}
+__device__ __forceinline__ uint32_t pack(float2 v) { return umma::pack_half2(v.x, v.y); }
+__device__ __forceinline__ float amax2(float m, float2 v) { return fmaxf(m, fmaxf(fabsf(v.x), fabsf(v.y))); }
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
+
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(umma::smem_u32(bar)) : "memory");
+}
 
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
@@ -85,7 +118,7 @@ struct PrepArgs {
 
 // One CTA per (slot, group).
 template <int N>
-__global__ void __launch_bounds__(256) ssm_prep_kernel(const PrepArgs a) {
+__global__ void __launch_bounds__(stc::PREP_THREADS) ssm_prep_kernel(const PrepArgs a) {
     using namespace stc;
     __shared__ float eb[Q], ec[Q];        // inverse scales of the rows of B and C
     __shared__ float dts[Q][33];
@@ -108,7 +141,7 @@ __global__ void __launch_bounds__(256) ssm_prep_kernel(const PrepArgs a) {
     // in N / 8 neighbouring lanes
     constexpr int VEC = N / 8;                    // lanes of a row
     constexpr int LANES = 2 * VEC;                // threads across B | C
-    constexpr int RUN = Q / (256 / LANES);        // tokens of a thread
+    constexpr int RUN = Q / (PREP_THREADS / LANES);        // tokens of a thread
     {
         const int v = tid % LANES, isC = v / VEC, c = (v % VEC) * 8;
         const int r0 = (tid / LANES) * RUN;
@@ -145,7 +178,7 @@ __global__ void __launch_bounds__(256) ssm_prep_kernel(const PrepArgs a) {
                 float s = bias[e];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) s = fmaf(w[e][j], win[(i + j) & 3][e], s);
-                x[e] = r < len ? ssm::silu(s) : 0.f;
+                x[e] = r < len ? silu_fast(s) : 0.f;
                 m = max(m, __float_as_uint(x[e]) & 0x7fffffffu);
             }
 #pragma unroll
@@ -172,12 +205,12 @@ __global__ void __launch_bounds__(256) ssm_prep_kernel(const PrepArgs a) {
     for (int h0 = 0; h0 < heads; h0 += 32) {
         __syncthreads();
         const int hn = min(32, heads - h0);
-        for (int i = tid; i < len * 32; i += 256) {
+        for (int i = tid; i < len * 32; i += PREP_THREADS) {
             const int r = i >> 5, k = i & 31;
             if (k < hn) dts[r][k] = to_f32(a.dt[(t0 + r) * a.ld_dt + g * heads + h0 + k]);
         }
         __syncthreads();
-        for (int k = warp; k < hn; k += 8) {
+        for (int k = warp; k < hn; k += PREP_THREADS / 32) {
             const int h = g * heads + h0 + k;
             const float rate = expf(__ldg(a.A + h)), bias = __ldg(a.b_dt + h);
             float d[2], la[2];
@@ -246,6 +279,9 @@ struct ChainArgs {
     float *s0_copy;     // [n_seq][H][N][P] when S_final may be S0
     int n_seq, n_tok, H, G, P, blocks_per_group, seg_chunks, n_seg;
 };
+struct ChainMaps {
+    CUtensorMap z, out;   // [N_tok][H P], boxes of 64 columns x 64 tokens
+};
 }  // namespace
 
 namespace stc {
@@ -254,12 +290,12 @@ template <int N> struct Smem {
     static constexpr int OFF_X = 2 * TILE;             // x'' fp16, token rows x 128 columns (two 64-column blocks)
     static constexpr int OFF_XH = OFF_X + 16384;       // weighted x, hi and lo
     static constexpr int OFF_XL = OFF_XH + 16384;
-    static constexpr int OFF_W = OFF_XL + 16384;       // decayed scores, 128 rows (two halves) x 64
-    static constexpr int OFF_S = OFF_W + 16384;        // state fp16, N rows x 128 columns
-    static constexpr int OFF_REC = OFF_S + 2 * N * 128;   // [2 stages][2 halves][REC]
+    static constexpr int OFF_S = OFF_XL + 16384;       // state fp16, N rows x 128 columns
+    static constexpr int OFF_Z = OFF_S + 2 * N * 128;  // [2 stages]: z, then out in its place, 64 rows x 128 columns
+    static constexpr int OFF_REC = OFF_Z + 2 * 16384;  // [2 stages][2 halves][REC]
     static constexpr int OFF_CW = OFF_REC + 4 * REC * 4;  // conv weights [5][128]
-    static constexpr int OFF_MAX = OFF_CW + 5 * 128 * 4;  // maxima: x [16 warps][2], state [16 warps]
-    static constexpr int OFF_BAR = OFF_MAX + 48 * 4;
+    static constexpr int OFF_MAX = OFF_CW + 5 * 128 * 4;  // bits of the largest |.|, [2 chunks][x, x, state, state]
+    static constexpr int OFF_BAR = OFF_MAX + 8 * 4;
     static constexpr int SIZE = OFF_BAR + 128 + 1024;     // barriers, TMEM slot, abort flag; alignment slack
 };
 static_assert(Smem<128>::SIZE <= 232448, "227 KB per block");
@@ -268,17 +304,18 @@ static_assert(Smem<128>::SIZE <= 232448, "227 KB per block");
 // STATE_ONLY: segment k of a split sequence, from zero (segment 0: from S0) to its
 // final state in seg_state.  Otherwise the whole mixer over the segment.
 template <int N, bool STATE_ONLY>
-__global__ void __launch_bounds__(stc::THREADS, 1) ssm_chain_kernel(const ChainArgs a) {
+__global__ void __launch_bounds__(stc::THREADS, 1)
+ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
     using namespace stc;
     using Sm = Smem<N>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = umma::align_smem<1024>(smem_raw);
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + Sm::OFF_BAR);
-    uint64_t *bar_sc = full + 2, *bar_u = full + 3, *bar_y = full + 4;
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(full + 5);
+    uint64_t *bar_sc = full + 2, *bar_u = full + 3, *bar_y = full + 4, *full_z = full + 5, *bar_w = full + 7;
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(full + 8);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tslot + 1);
     float *cw = reinterpret_cast<float *>(sm + Sm::OFF_CW);
-    uint32_t *xmax = reinterpret_cast<uint32_t *>(sm + Sm::OFF_MAX), *smax = xmax + 32;
+    uint32_t *mx = reinterpret_cast<uint32_t *>(sm + Sm::OFF_MAX);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int q = warp & 3, cg = warp >> 2;
     const int blk = blockIdx.x, n = blockIdx.y, seg = blockIdx.z;
@@ -305,20 +342,21 @@ __global__ void __launch_bounds__(stc::THREADS, 1) ssm_chain_kernel(const ChainA
     const int shead = cg < 2 ? head0 : head1;
     const int spc = a.P == 64 ? sc0 & 63 : sc0;                       // column within the head
     const size_t sbase = (((size_t)n * a.H + shead) * N + srow) * a.P + spc;
-    float S[32];
+    float2 S[16];
 #pragma unroll
-    for (int j = 0; j < 32; ++j) S[j] = 0.f;
+    for (int j = 0; j < 16; ++j) S[j] = make_float2(0.f, 0.f);
     auto load_state = [&](const float *p) {
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-            const float4 v = *reinterpret_cast<const float4 *>(p + j);
-            S[j] = v.x; S[j + 1] = v.y; S[j + 2] = v.z; S[j + 3] = v.w;
+        for (int j = 0; j < 16; j += 2) {
+            const float4 v = *reinterpret_cast<const float4 *>(p + 2 * j);
+            S[j] = make_float2(v.x, v.y);
+            S[j + 1] = make_float2(v.z, v.w);
         }
     };
     auto store_state = [&](float *p) {
 #pragma unroll
-        for (int j = 0; j < 32; j += 4)
-            *reinterpret_cast<float4 *>(p + j) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+        for (int j = 0; j < 16; j += 2)
+            *reinterpret_cast<float4 *>(p + 2 * j) = make_float4(S[j].x, S[j].y, S[j + 1].x, S[j + 1].y);
     };
     const size_t seg_base = ((size_t)n * gridDim.x + blk) * (a.n_seg - 1);   // of this chain's segments
     auto seg_ptr = [&](int k) { return a.seg_state + ((seg_base + k) * N + srow) * 128 + sc0; };
@@ -336,10 +374,10 @@ __global__ void __launch_bounds__(stc::THREADS, 1) ssm_chain_kernel(const ChainA
                 const float d = __ldg(a.seg_decay + (seg_base + k) * 2 + (cg >> 1));
                 const float *p = seg_ptr(k);
 #pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                    const float4 v = *reinterpret_cast<const float4 *>(p + j);
-                    S[j] = fmaf(d, S[j], v.x); S[j + 1] = fmaf(d, S[j + 1], v.y);
-                    S[j + 2] = fmaf(d, S[j + 2], v.z); S[j + 3] = fmaf(d, S[j + 3], v.w);
+                for (int j = 0; j < 16; j += 2) {
+                    const float4 v = *reinterpret_cast<const float4 *>(p + 2 * j);
+                    S[j] = ffma2(make_float2(d, d), S[j], make_float2(v.x, v.y));
+                    S[j + 1] = ffma2(make_float2(d, d), S[j + 1], make_float2(v.z, v.w));
                 }
             }
         }
@@ -348,10 +386,12 @@ __global__ void __launch_bounds__(stc::THREADS, 1) ssm_chain_kernel(const ChainA
 
     if (warp == 0) umma::tmem_alloc(tslot, 512);
     if (tid == 0) {
-        for (int i = 0; i < 5; ++i) umma::mbar_init(full + i, 1);
+        for (int i = 0; i < 7; ++i) umma::mbar_init(full + i, 1);
+        umma::mbar_init(bar_w, THREADS / 32);
         *abort_flag = 0;
         umma::fence_mbar_init();
     }
+    if (tid < 8) mx[tid] = 0;
     for (int i = tid; i < 5 * 128; i += THREADS) {
         const int j = i >> 7, c = i & 127;
         const bool in = c < 64 || live1;
@@ -383,8 +423,18 @@ __global__ void __launch_bounds__(stc::THREADS, 1) ssm_chain_kernel(const ChainA
         bulk_load(sm + Sm::OFF_REC + b * 2 * REC * 4, a.rec + (slot * a.H + head0) * REC, REC * 4, full + b);
         bulk_load(sm + Sm::OFF_REC + (b * 2 + 1) * REC * 4, a.rec + (slot * a.H + head1) * REC, REC * 4, full + b);
     };
+    auto issue_z = [&](int c) {
+        uint8_t *p = sm + Sm::OFF_Z + (c & 1) * 16384;
+        const int t = begin + (c_lo + c) * Q;
+        umma::mbar_expect_tx(full_z + (c & 1), live1 ? 16384 : 8192);
+        umma::tma_load_3d(p, &maps.z, (int)xcol, 0, t, full_z + (c & 1));
+        if (live1) umma::tma_load_3d(p + 8192, &maps.z, (int)xcol + 64, 0, t, full_z + (c & 1));
+    };
     if (tid == 0)
-        for (int c = 0; c < 2 && c < chunks; ++c) issue(c);
+        for (int c = 0; c < 2 && c < chunks; ++c) {
+            issue(c);
+            if (!STATE_ONLY && a.z && c == 0) issue_z(c);
+        }
 
     // ---- raw x of this thread: tokens 4 warp .. + 3 and the three before, columns 4 lane .. + 3
     const int xc = 4 * lane, half = lane >> 4;
@@ -392,212 +442,256 @@ __global__ void __launch_bounds__(stc::THREADS, 1) ssm_chain_kernel(const ChainA
     uint2 raw[7];
     auto fetch = [&](int c) {
         const int t = begin + (c_lo + c) * Q + 4 * warp - 3;
+        const bf16 *p = a.x + t * a.ld_x + xcol + xc;
+        if (t >= begin && t + 7 <= end && live1) {
+#pragma unroll
+            for (int j = 0; j < 7; ++j) raw[j] = __ldg(reinterpret_cast<const uint2 *>(p + j * a.ld_x));
+            return;
+        }
 #pragma unroll
         for (int j = 0; j < 7; ++j) {
             raw[j] = make_uint2(0, 0);
             if (!xlive) continue;
             if (t + j >= begin) {
-                if (t + j < end) raw[j] = __ldg(reinterpret_cast<const uint2 *>(a.x + (t + j) * a.ld_x + xcol + xc));
+                if (t + j < end) raw[j] = __ldg(reinterpret_cast<const uint2 *>(p + j * a.ld_x));
             } else if (a.hist) {
                 raw[j] = __ldg(reinterpret_cast<const uint2 *>(a.hist + ((size_t)n * 3 + (t + j - begin + 3)) * chans +
                                                                xcol + xc));
             }
         }
     };
-    if (chunks > 0) fetch(0);
+    // convolution and activation of the fetched tokens of chunk c, and the largest |x| of
+    // each half into mx[c & 1][half]
+    float2 xh[4][2];
+    auto convolve = [&](int c) {
+        const int len = min(Q, end - (begin + (c_lo + c) * Q));
+        float2 w[5][2], f[7][2];
+#pragma unroll
+        for (int j = 0; j < 5; ++j) {
+            const float4 v = *reinterpret_cast<const float4 *>(cw + 128 * j + xc);
+            w[j][0] = make_float2(v.x, v.y);
+            w[j][1] = make_float2(v.z, v.w);
+        }
+#pragma unroll
+        for (int j = 0; j < 7; ++j) {
+            f[j][0] = make_float2(bf16lo(raw[j].x), bf16hi(raw[j].x));
+            f[j][1] = make_float2(bf16lo(raw[j].y), bf16hi(raw[j].y));
+        }
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool in = 4 * warp + i < len;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float2 v = w[4][e];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v = ffma2(w[j][e], f[i + j][e], v);
+                xh[i][e] = in ? make_float2(silu_fast(v.x), silu_fast(v.y)) : make_float2(0.f, 0.f);
+                m = amax2(m, xh[i][e]);
+            }
+        }
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if ((lane & 15) == 0) atomicMax(mx + (c & 1) * 4 + half, __float_as_uint(m));
+    };
 
-    const float dskip0 = !STATE_ONLY && a.D ? __ldg(a.D + head0) : 0.f;
-    const float dskip1 = !STATE_ONLY && a.D ? __ldg(a.D + head1) : 0.f;
+    const float dskip = !STATE_ONLY && a.D ? __ldg(a.D + (q < 2 ? head0 : head1)) : 0.f;
     float decay0 = 1.f, decay1 = 1.f;   // of the whole segment (state pass)
-    const uint32_t sX = umma::smem_u32(sm + Sm::OFF_X), sXH = umma::smem_u32(sm + Sm::OFF_XH);
-    const uint32_t sXL = umma::smem_u32(sm + Sm::OFF_XL), sW = umma::smem_u32(sm + Sm::OFF_W);
-    const uint32_t sS = umma::smem_u32(sm + Sm::OFF_S), sT = umma::smem_u32(sm);
+    // operand addresses of this thread: a row's 16-byte chunks k, k ^ 1, ... differ by an
+    // exclusive or with the chunk's bits
+    uint8_t *const p_x = sm + Sm::OFF_X + half * 8192 + umma::sw128_offset(4 * warp, (lane & 15) >> 1) + 8 * (lane & 1);
+    uint8_t *const p_s = sm + Sm::OFF_S + (cg >> 1) * (N * 128) + umma::sw128_offset(srow, (cg & 1) * 4);
+    const int hv = q >> 1, t = 32 * (q & 1) + lane;      // rows of y: half and token of this thread
+    const int oc = 64 * hv + 16 * cg;                    // and its 16 columns
+    uint8_t *const p_o = sm + Sm::OFF_X + hv * 8192 + umma::sw128_offset(t, 2 * cg);
+    auto flip = [](auto *p, int bytes) {   // p with bits of the chunk index flipped (every tile is 1024-byte aligned)
+        return p + ((int)((umma::smem_u32(p) ^ (uint32_t)bytes) - umma::smem_u32(p)));
+    };
+    // matrix descriptors; the start address field counts 16 bytes
+    const uint32_t sT = umma::smem_u32(sm);
+    const uint64_t d_tile = umma::sw128_desc(sT, 16, 1024);
+    const uint64_t d_tile_mn = umma::sw128_desc(sT, N == 128 ? KB : 0, 1024);   // N = 64: rows 64.. repeat rows 0..
+    const uint64_t d_x = umma::sw128_desc(sT + Sm::OFF_X, 8192, 1024);
+    const uint64_t d_s = umma::sw128_desc(sT + Sm::OFF_S, 16, 1024);
 
+    if (chunks > 0) {
+        fetch(0);
+        convolve(0);
+        if (chunks > 1) fetch(1);
+    }
     for (int c = 0; c < chunks; ++c) {
         const int b = c & 1;
         const uint32_t ph = (uint32_t)c & 1u, ph_full = (uint32_t)(c >> 1) & 1u;
         const int t0 = begin + (c_lo + c) * Q, len = min(Q, end - t0);
         const float *rec0 = reinterpret_cast<const float *>(sm + Sm::OFF_REC) + b * 2 * REC, *rec1 = rec0 + REC;
-
-        // ---- convolution and activation of x
-        float xh[4][4];
-        uint32_t m = 0;
-        {
-            float4 w[5];
-#pragma unroll
-            for (int j = 0; j < 5; ++j) w[j] = *reinterpret_cast<const float4 *>(cw + 128 * j + xc);
-            float f[7][4];
-#pragma unroll
-            for (int j = 0; j < 7; ++j) {
-                f[j][0] = bf16lo(raw[j].x); f[j][1] = bf16hi(raw[j].x);
-                f[j][2] = bf16lo(raw[j].y); f[j][3] = bf16hi(raw[j].y);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const bool in = 4 * warp + i < len;
-                const float s0 = fmaf(w[3].x, f[i + 3][0], fmaf(w[2].x, f[i + 2][0], fmaf(w[1].x, f[i + 1][0], fmaf(w[0].x, f[i][0], w[4].x))));
-                const float s1 = fmaf(w[3].y, f[i + 3][1], fmaf(w[2].y, f[i + 2][1], fmaf(w[1].y, f[i + 1][1], fmaf(w[0].y, f[i][1], w[4].y))));
-                const float s2 = fmaf(w[3].z, f[i + 3][2], fmaf(w[2].z, f[i + 2][2], fmaf(w[1].z, f[i + 1][2], fmaf(w[0].z, f[i][2], w[4].z))));
-                const float s3 = fmaf(w[3].w, f[i + 3][3], fmaf(w[2].w, f[i + 2][3], fmaf(w[1].w, f[i + 1][3], fmaf(w[0].w, f[i][3], w[4].w))));
-                xh[i][0] = in ? silu_fast(s0) : 0.f;
-                xh[i][1] = in ? silu_fast(s1) : 0.f;
-                xh[i][2] = in ? silu_fast(s2) : 0.f;
-                xh[i][3] = in ? silu_fast(s3) : 0.f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) m = max(m, __float_as_uint(xh[i][e]) & 0x7fffffffu);
-            }
-        }
-        if (c + 1 < chunks) fetch(c + 1);
-#pragma unroll
-        for (int o = 1; o < 16; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if ((lane & 15) == 0) xmax[half * 16 + warp] = m;
         if (!STATE_ONLY) {
-            uint32_t ms = 0;
+            float ms = 0.f;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) ms = max(ms, __float_as_uint(S[j]) & 0x7fffffffu);
-            ms = __reduce_max_sync(0xffffffffu, ms);
-            if (lane == 0) smax[warp] = ms;       // columns of half cg / 2: warps 8 (cg / 2) .. + 7
+            for (int j = 0; j < 16; ++j) ms = amax2(ms, S[j]);
+            const uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(ms));
+            if (lane == 0) atomicMax(mx + b * 4 + 2 + (cg >> 1), mb);
         }
         __syncthreads();   // the previous chunk is done with the tiles, the stage of chunk c - 1 and x
-        if (tid == 0 && c >= 1 && c + 1 < chunks) issue(c + 1);
+        if (tid < 4) mx[(b ^ 1) * 4 + tid] = 0;   // chunk c - 1's, for chunk c + 1, whose x is added after the next barrier
 
         // ---- scales; operands into shared memory
-        float xs, xinv, xinv0, xinv1, ss = 0.f, sinv0 = 0.f, sinv1 = 0.f;
-        {
-            uint32_t m0 = 0, m1 = 0;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) { m0 = max(m0, xmax[i]); m1 = max(m1, xmax[16 + i]); }
-            float s0, s1;
-            scale_pow2(m0, 13, s0, xinv0);
-            scale_pow2(m1, 13, s1, xinv1);
-            xs = half ? s1 : s0;
-            xinv = cg < 2 ? xinv0 : xinv1;        // of the state columns of this thread
-            if (!STATE_ONLY) {
-                m0 = m1 = 0;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) { m0 = max(m0, smax[i]); m1 = max(m1, smax[8 + i]); }
-                scale_pow2(m0, 13, s0, sinv0);
-                scale_pow2(m1, 13, s1, sinv1);
-                ss = cg < 2 ? s0 : s1;
-            }
-        }
+        const uint4 mxv = *reinterpret_cast<const uint4 *>(mx + b * 4);
+        float xs0, xs1, xinv0, xinv1;
+        scale_pow2(mxv.x, 13, xs0, xinv0);
+        scale_pow2(mxv.y, 13, xs1, xinv1);
+        float sinv = 0.f;                    // of the rows of y of this thread
         wait(full + b, ph_full);
         {
-            const float *rw = (half ? rec1 : rec0) + R_W;
-            const uint32_t off = half * 8192 + 8 * (lane & 1);
-            const int chunk = (lane & 15) >> 1;
+            const float4 wr4 = *reinterpret_cast<const float4 *>((half ? rec1 : rec0) + R_W + 4 * warp);
+            const float wr[4] = {wr4.x, wr4.y, wr4.z, wr4.w};
+            const float xs = half ? xs1 : xs0;
+            const float2 xs2 = make_float2(xs, xs);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int r = 4 * warp + i;
-                const uint32_t at = off + umma::sw128_offset(r, chunk);
-                const float wr = rw[r];
-                uint32_t hi2[2], lo2[2], x2[2];
+                uint8_t *p = flip(p_x, 16 * i) + 128 * i;
+                uint32_t x2[2], hi2[2], lo2[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float u0 = xh[i][2 * e] * xs, u1 = xh[i][2 * e + 1] * xs;
-                    x2[e] = umma::pack_half2(u0, u1);
-                    const float v0 = u0 * wr, v1 = u1 * wr;
-                    const __half2 p = __floats2half2_rn(v0, v1);
-                    const float2 pf = __half22float2(p);
-                    hi2[e] = *reinterpret_cast<const uint32_t *>(&p);
-                    lo2[e] = umma::pack_half2(v0 - pf.x, v1 - pf.y);
+                    const float2 u = fmul2(xh[i][e], xs2), v = fmul2(u, make_float2(wr[i], wr[i]));
+                    x2[e] = pack(u);
+                    hi2[e] = pack(v);
+                    const float2 h = half2_float2(hi2[e]);
+                    lo2[e] = umma::pack_half2(v.x - h.x, v.y - h.y);
                 }
-                if (!STATE_ONLY) *reinterpret_cast<uint2 *>(sm + Sm::OFF_X + at) = make_uint2(x2[0], x2[1]);
-                *reinterpret_cast<uint2 *>(sm + Sm::OFF_XH + at) = make_uint2(hi2[0], hi2[1]);
-                *reinterpret_cast<uint2 *>(sm + Sm::OFF_XL + at) = make_uint2(lo2[0], lo2[1]);
+                if (!STATE_ONLY) *reinterpret_cast<uint2 *>(p) = make_uint2(x2[0], x2[1]);
+                *reinterpret_cast<uint2 *>(p + (Sm::OFF_XH - Sm::OFF_X)) = make_uint2(hi2[0], hi2[1]);
+                *reinterpret_cast<uint2 *>(p + (Sm::OFF_XL - Sm::OFF_X)) = make_uint2(lo2[0], lo2[1]);
             }
-            if (!STATE_ONLY && srow < N) {
-                uint8_t *p = sm + Sm::OFF_S + (cg >> 1) * (N * 128);
+        }
+        if (!STATE_ONLY) {
+            float s0, s1, i0, i1;
+            scale_pow2(mxv.z, 13, s0, i0);
+            scale_pow2(mxv.w, 13, s1, i1);
+            sinv = hv ? i1 : i0;
+            const float ss = cg < 2 ? s0 : s1;
+            const float2 ss2 = make_float2(ss, ss);
+            if (srow < N) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    umma::st_chunk(p, srow, (cg & 1) * 4 + j,
-                                   make_uint4(umma::pack_half2(S[8 * j] * ss, S[8 * j + 1] * ss),
-                                              umma::pack_half2(S[8 * j + 2] * ss, S[8 * j + 3] * ss),
-                                              umma::pack_half2(S[8 * j + 4] * ss, S[8 * j + 5] * ss),
-                                              umma::pack_half2(S[8 * j + 6] * ss, S[8 * j + 7] * ss)));
+                    *reinterpret_cast<uint4 *>(flip(p_s, 16 * j)) =
+                        make_uint4(pack(fmul2(S[4 * j], ss2)), pack(fmul2(S[4 * j + 1], ss2)),
+                                   pack(fmul2(S[4 * j + 2], ss2)), pack(fmul2(S[4 * j + 3], ss2)));
             }
         }
         umma::fence_proxy_async_smem();
         umma::tc_fence_before();
         __syncthreads();
-        if (tid == 0) {
-            umma::tc_fence_after();
-            const uint32_t tile = sT + b * Sm::TILE;
-            constexpr int KS = N / 16;   // K steps over the state dim
-            if (!STATE_ONLY) {
+        // The tensor pipe takes MMAs about as fast as it runs them, so their issuer waits
+        // along: three warps share the work, and the two whose results are needed later
+        // do theirs after their part of the convolution.
+        const uint64_t dt = d_tile + (uint32_t)(b * (Sm::TILE >> 4));
+        constexpr int KS = N / 16;   // K steps over the state dim
+        if (!STATE_ONLY && warp == 0) {
+            if (elect_one()) {
+                umma::tc_fence_after();
                 const uint32_t id = umma::idesc_f16(128, 64, false, false);
 #pragma unroll
                 for (int j = 0; j < 2; ++j)   // scores: C in rows 64 j .. 64 j + 63
 #pragma unroll
                     for (int k = 0; k < KS; ++k) {
-                        const uint32_t kb = tile + (k / 4) * KB + (k % 4) * 32;
-                        umma::mma_f16(T_SC + 64 * j, umma::sw128_desc(kb + (j ? 0 : OFF_C), 16, 1024),
-                                      umma::sw128_desc(kb, 16, 1024), id, k > 0);
+                        const uint32_t kb = ((k / 4) * KB + (k % 4) * 32) >> 4;
+                        umma::mma_f16(T_SC + 64 * j, dt + (kb + (j ? 0 : OFF_C >> 4)), dt + kb, id, k > 0);
                     }
                 umma::mma_commit(bar_sc);
             }
-            {
+            __syncwarp();
+        }
+        if (warp == 12) {
+            if (elect_one()) {
+                if (c >= 1 && c + 1 < chunks) issue(c + 1);
+                if (!STATE_ONLY) {
+                    // out of chunk c - 1 (written before the barrier) leaves; its tile takes z of chunk c + 1
+                    if (c >= 1) {
+                        const uint8_t *p = sm + Sm::OFF_Z + (b ^ 1) * 16384;
+                        umma::tma_store_3d(&maps.out, (int)xcol, 0, t0 - Q, p);
+                        if (live1) umma::tma_store_3d(&maps.out, (int)xcol + 64, 0, t0 - Q, p + 8192);
+                        umma::bulk_commit();
+                        umma::bulk_wait_read<0>();
+                    }
+                    if (a.z && c + 1 < chunks) issue_z(c + 1);
+                }
+            }
+            __syncwarp();
+        }
+        // ---- while they run: x of the next chunk
+        const float *recv = hv ? rec1 : rec0;
+        if (c + 1 < chunks) {
+            convolve(c + 1);
+            if (c + 2 < chunks) fetch(c + 2);
+        }
+        if (warp == 1) {
+            if (elect_one()) {
+                umma::tc_fence_after();
                 const uint32_t id = umma::idesc_f16(128, 128, true, true);
-                constexpr uint32_t LBO = N == 128 ? KB : 0;   // N = 64: rows 64.. repeat rows 0..
-                const uint32_t as[3] = {tile, tile, tile + OFF_LO}, bs[3] = {sXH, sXL, sXH};
+                const uint64_t da = d_tile_mn + (uint32_t)(b * (Sm::TILE >> 4));
+                const uint64_t dxh = d_x + ((Sm::OFF_XH - Sm::OFF_X) >> 4), dxl = d_x + ((Sm::OFF_XL - Sm::OFF_X) >> 4);
 #pragma unroll
-                for (int p = 0; p < 3; ++p)
+                for (int p = 0; p < 3; ++p)   // hi hi, hi lo, lo hi
 #pragma unroll
                     for (int k = 0; k < Q / 16; ++k)
-                        umma::mma_f16(T_U, umma::sw128_desc(as[p] + k * 2048, LBO, 1024),
-                                      umma::sw128_desc(bs[p] + k * 2048, 8192, 1024), id, p > 0 || k > 0);
+                        umma::mma_f16(T_U, da + (((p == 2 ? OFF_LO : 0) + k * 2048) >> 4),
+                                      (p == 1 ? dxl : dxh) + ((k * 2048) >> 4), id, p > 0 || k > 0);
                 umma::mma_commit(bar_u);
             }
-            if (!STATE_ONLY) {
-                const uint32_t id = umma::idesc_f16(128, 64, false, true);
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int k = 0; k < KS; ++k) {
-                        const uint32_t kb = tile + (k / 4) * KB + (k % 4) * 32;
-                        umma::mma_f16(T_YI + 64 * j, umma::sw128_desc(kb + (j ? 0 : OFF_C), 16, 1024),
-                                      umma::sw128_desc(sS + j * (N * 128) + k * 2048, 16, 1024), id, k > 0);
-                    }
-            }
+            __syncwarp();
         }
-        const int hv = q >> 1, t = 32 * (q & 1) + lane;      // rows of y: half and token of this thread
-        const float *recv = hv ? rec1 : rec0;
         if (!STATE_ONLY) {
-            // ---- decayed scores: 16 of them per thread
+            // ---- decayed scores: 16 of them per thread, as the A operand in tensor memory.
+            // Half 0 (lanes 0..63) writes columns 64 .. 95 and half 1 columns 0 .. 31, where
+            // the other half's scores lie in lanes that nobody reads.
             wait(bar_sc, ph);
             umma::tc_fence_after();
-            uint32_t sc[16];
+            uint32_t sc[16], p[8];
             umma::tmem_ld16_nowait(T_SC + lane_off + 64 * hv + 16 * cg, sc);
             umma::tmem_ld_wait();
             const float Lt = recv[R_L + t];
-            float wv[16];
 #pragma unroll
             for (int s4 = 0; s4 < 4; ++s4) {
-                const float4 l4 = *reinterpret_cast<const float4 *>(recv + R_L + 16 * cg + 4 * s4);
-                const float4 u4 = *reinterpret_cast<const float4 *>(recv + R_U + 16 * cg + 4 * s4);
-                const float ls[4] = {l4.x, l4.y, l4.z, l4.w}, us[4] = {u4.x, u4.y, u4.z, u4.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int s = 16 * cg + 4 * s4 + e;
-                    wv[4 * s4 + e] = s <= t ? __uint_as_float(sc[4 * s4 + e]) * us[e] * exp2f(Lt - ls[e]) : 0.f;
-                }
+                const int s = 16 * cg + 4 * s4;
+                const float4 l4 = *reinterpret_cast<const float4 *>(recv + R_L + s);
+                const float4 u4 = *reinterpret_cast<const float4 *>(recv + R_U + s);
+                float w0 = __uint_as_float(sc[4 * s4]) * u4.x * ex2(Lt - l4.x);
+                float w1 = __uint_as_float(sc[4 * s4 + 1]) * u4.y * ex2(Lt - l4.y);
+                float w2 = __uint_as_float(sc[4 * s4 + 2]) * u4.z * ex2(Lt - l4.z);
+                float w3 = __uint_as_float(sc[4 * s4 + 3]) * u4.w * ex2(Lt - l4.w);
+                if (s > t) w0 = 0.f;
+                if (s + 1 > t) w1 = 0.f;
+                if (s + 2 > t) w2 = 0.f;
+                if (s + 3 > t) w3 = 0.f;
+                p[2 * s4] = umma::pack_half2(w0, w1);
+                p[2 * s4 + 1] = umma::pack_half2(w2, w3);
             }
-            uint32_t p[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) p[e] = umma::pack_half2(wv[2 * e], wv[2 * e + 1]);
-            umma::st_chunk(sm + Sm::OFF_W, srow, 2 * cg, make_uint4(p[0], p[1], p[2], p[3]));
-            umma::st_chunk(sm + Sm::OFF_W, srow, 2 * cg + 1, make_uint4(p[4], p[5], p[6], p[7]));
-            umma::fence_proxy_async_smem();
+            umma::tmem_st8(T_SC + lane_off + (hv ? 0 : 64) + 8 * cg, p);
+            umma::tmem_st_wait();
             umma::tc_fence_before();
-            __syncthreads();
-            if (tid == 0) {
-                umma::tc_fence_after();
-                const uint32_t id = umma::idesc_f16(128, 128, false, true);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_w);
+            if (warp == 2) {
+                wait(bar_w, ph);
+                if (elect_one()) {
+                    umma::tc_fence_after();
+                    const uint32_t idi = umma::idesc_f16(128, 64, false, true);
 #pragma unroll
-                for (int k = 0; k < Q / 16; ++k)
-                    umma::mma_f16(T_YW, umma::sw128_desc(sW + k * 32, 16, 1024),
-                                  umma::sw128_desc(sX + k * 2048, 8192, 1024), id, k > 0);
-                umma::mma_commit(bar_y);
+                    for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                        for (int k = 0; k < Q / 16; ++k)   // rows 64 j .. of the decayed scores, columns of half j
+                            umma::mma_f16_ts(T_YW + 64 * j, T_SC + (j ? 0 : 64) + 8 * k,
+                                             d_x + ((j * 8192 + k * 2048) >> 4), idi, k > 0);
+#pragma unroll
+                        for (int k = 0; k < KS; ++k) {
+                            const uint32_t kb = ((k / 4) * KB + (k % 4) * 32) >> 4;
+                            umma::mma_f16(T_YI + 64 * j, dt + (kb + (j ? 0 : OFF_C >> 4)),
+                                          d_s + ((j * (N * 128) + k * 2048) >> 4), idi, k > 0);
+                        }
+                    }
+                    umma::mma_commit(bar_y);
+                }
+                __syncwarp();
             }
         }
         // ---- state
@@ -605,57 +699,67 @@ __global__ void __launch_bounds__(stc::THREADS, 1) ssm_chain_kernel(const ChainA
         umma::tc_fence_after();
         {
             const float *rs = cg < 2 ? rec0 : rec1;
-            const float dec = rs[R_DEC], add = rs[R_UMAX] * xinv;
-            float v[32];
-            umma::tmem_ld32(T_U + lane_off + sc0, v);
+            const float dec = rs[R_DEC], add = rs[R_UMAX] * (cg < 2 ? xinv0 : xinv1);
+            const float2 dec2 = make_float2(dec, dec), add2 = make_float2(add, add);
+            uint32_t v[32];
+            umma::tmem_ld32_nowait(T_U + lane_off + sc0, v);
+            umma::tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) S[j] = fmaf(dec, S[j], add * v[j]);
+            for (int j = 0; j < 16; ++j)
+                S[j] = ffma2(dec2, S[j],
+                             fmul2(add2, make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]))));
             if (STATE_ONLY) { decay0 *= rec0[R_DEC]; decay1 *= rec1[R_DEC]; }
         }
         if (!STATE_ONLY) {
-            // ---- output: token t of half hv, columns 64 hv + 16 cg .. + 15
-            const bool store = t < len && (hv == 0 || live1);
-            const long long tok = t0 + t;
-            const int oc = 64 * hv + 16 * cg;
-            float zf[2][8];
-            if (a.z && store) {
-                load8(a.z + tok * a.ld_z + xcol + oc, zf[0]);
-                load8(a.z + tok * a.ld_z + xcol + oc + 8, zf[1]);
-            }
+            // ---- output: token t of half hv, columns oc .. + 15; a whole chunk leaves by TMA
+            // from the z tile, a ragged one directly
+            if (a.z) wait(full_z + b, ph_full);
             wait(bar_y, ph);
             umma::tc_fence_after();
             uint32_t yi[16], yw[16];
             umma::tmem_ld16_nowait(T_YI + lane_off + oc, yi);
             umma::tmem_ld16_nowait(T_YW + lane_off + oc, yw);
             umma::tmem_ld_wait();
-            if (store) {
-                const float fi = recv[R_YI + t] * (hv ? sinv1 : sinv0), fx = hv ? xinv1 : xinv0;
-                const float fw = recv[R_YW + t] * fx, fd = (hv ? dskip1 : dskip0) * fx;
-                bf16 *o = a.out + tok * (long long)(a.H * a.P) + xcol + oc;
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint4 xx = *reinterpret_cast<const uint4 *>(sm + Sm::OFF_X + hv * 8192 +
-                                                                      umma::sw128_offset(t, 2 * cg + k));
-                    const __half2 *x2 = reinterpret_cast<const __half2 *>(&xx);
-                    uint32_t w[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 xf = __half22float2(x2[e]);
-                        float y0 = fmaf(__uint_as_float(yi[8 * k + 2 * e]), fi,
-                                        fmaf(__uint_as_float(yw[8 * k + 2 * e]), fw, xf.x * fd));
-                        float y1 = fmaf(__uint_as_float(yi[8 * k + 2 * e + 1]), fi,
-                                        fmaf(__uint_as_float(yw[8 * k + 2 * e + 1]), fw, xf.y * fd));
-                        if (a.z) {
-                            y0 *= silu_fast(zf[k][2 * e]);
-                            y1 *= silu_fast(zf[k][2 * e + 1]);
-                        }
-                        const __nv_bfloat162 p = __floats2bfloat162_rn(y0, y1);
-                        w[e] = *reinterpret_cast<const uint32_t *>(&p);
-                    }
-                    reinterpret_cast<uint4 *>(o)[k] = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-            }
             umma::tc_fence_before();
+            const float fx = hv ? xinv1 : xinv0;
+            const float fi = recv[R_YI + t] * sinv, fw = recv[R_YW + t] * fx, fd = dskip * fx;
+            const float2 fi2 = make_float2(fi, fi), fw2 = make_float2(fw, fw), fd2 = make_float2(fd, fd);
+            bf16 *const o = a.out + (long long)(t0 + t) * (a.H * a.P) + xcol + oc;
+            uint8_t *const p_z = p_o + (Sm::OFF_Z - Sm::OFF_X) + b * 16384;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint4 xx = *reinterpret_cast<const uint4 *>(flip(p_o, 16 * k));
+                const uint4 zz = a.z ? *reinterpret_cast<const uint4 *>(flip(p_z, 16 * k)) : make_uint4(0, 0, 0, 0);
+                const uint32_t xw[4] = {xx.x, xx.y, xx.z, xx.w}, zw[4] = {zz.x, zz.y, zz.z, zz.w};
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = 8 * k + 2 * e;
+                    float2 y = fmul2(half2_float2(xw[e]), fd2);
+                    y = ffma2(make_float2(__uint_as_float(yw[i]), __uint_as_float(yw[i + 1])), fw2, y);
+                    y = ffma2(make_float2(__uint_as_float(yi[i]), __uint_as_float(yi[i + 1])), fi2, y);
+                    if (a.z) y = fmul2(y, make_float2(silu_fast(bf16lo(zw[e])), silu_fast(bf16hi(zw[e]))));
+                    const __nv_bfloat162 pb = __floats2bfloat162_rn(y.x, y.y);
+                    w[e] = *reinterpret_cast<const uint32_t *>(&pb);
+                }
+                const uint4 w4 = make_uint4(w[0], w[1], w[2], w[3]);
+                if (len == Q) *reinterpret_cast<uint4 *>(flip(p_z, 16 * k)) = w4;
+                else if (t < len && (hv == 0 || live1)) reinterpret_cast<uint4 *>(o)[k] = w4;
+            }
+            umma::fence_proxy_async_smem();
+        }
+    }
+    if (!STATE_ONLY && chunks > 0) {
+        __syncthreads();
+        const int t = begin + (c_lo + chunks - 1) * Q;
+        if (warp == 12 && elect_one()) {   // the last chunk's tile; the copies end before the CTA does
+            if (t + Q <= end) {
+                const uint8_t *p = sm + Sm::OFF_Z + ((chunks - 1) & 1) * 16384;
+                umma::tma_store_3d(&maps.out, (int)xcol, 0, t, p);
+                if (live1) umma::tma_store_3d(&maps.out, (int)xcol + 64, 0, t, p + 8192);
+                umma::bulk_commit();
+            }
+            umma::bulk_wait_all();
         }
     }
     if (owner && !*abort_flag) {
@@ -670,8 +774,10 @@ __global__ void __launch_bounds__(stc::THREADS, 1) ssm_chain_kernel(const ChainA
     umma::tc_fence_before();
     __syncthreads();
     if (*abort_flag && tid == 0)   // copies in flight land before the CTA leaves (bounded)
-        for (int b = 0; b < 2 && b < chunks; ++b)
-            umma::mbar_wait_bounded(full + b, (uint32_t)(((chunks - 1 - b) / 2)) & 1u, 1u << 16);
+        for (int b = 0; b < 2 && b < chunks; ++b) {
+            umma::mbar_wait_bounded(full + b, (uint32_t)((chunks - 1 - b) / 2) & 1u, 1u << 16);
+            if (!STATE_ONLY && a.z) umma::mbar_wait_bounded(full_z + b, (uint32_t)((chunks - 1 - b) / 2) & 1u, 1u << 16);
+        }
     if (warp == 0) umma::tmem_dealloc(tb, 512);
 }
 
@@ -749,10 +855,19 @@ cudaError_t launch_tc(const SsmArgs &a, char *ws, int sms) {
     ca.n_seg = p.n_seg;
     cudaError_t e;
     if (a.n_tok > 0) {
-        ssm_prep_kernel<N><<<dim3(p.slots, a.G), 256, 0, a.stream>>>(pa);
+        ssm_prep_kernel<N><<<dim3(p.slots, a.G), stc::PREP_THREADS, 0, a.stream>>>(pa);
         if ((e = launched()) != cudaSuccess) return e;
     }
     constexpr int SMEM = stc::Smem<N>::SIZE;
+    ChainMaps maps = {};
+    if (a.n_tok > 0) {
+        if ((e = make_tma_mat_bf16(reinterpret_cast<TmaMap *>(&maps.out), a.out, a.H * a.P, a.n_tok, a.H * a.P, 64,
+                                   stc::Q)) != cudaSuccess)
+            return e;
+        if (a.z && (e = make_tma_mat_bf16(reinterpret_cast<TmaMap *>(&maps.z), a.z, a.H * a.P, a.n_tok, (int)a.ld_z,
+                                          64, stc::Q)) != cudaSuccess)
+            return e;
+    }
     if ((e = cudaFuncSetAttribute(ssm_chain_kernel<N, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM)) !=
         cudaSuccess)
         return e;
@@ -760,10 +875,10 @@ cudaError_t launch_tc(const SsmArgs &a, char *ws, int sms) {
         if ((e = cudaFuncSetAttribute(ssm_chain_kernel<N, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM)) !=
             cudaSuccess)
             return e;
-        ssm_chain_kernel<N, true><<<dim3(p.blocks, a.n_seq, p.n_seg - 1), stc::THREADS, SMEM, a.stream>>>(ca);
+        ssm_chain_kernel<N, true><<<dim3(p.blocks, a.n_seq, p.n_seg - 1), stc::THREADS, SMEM, a.stream>>>(ca, maps);
         if ((e = launched()) != cudaSuccess) return e;
     }
-    ssm_chain_kernel<N, false><<<dim3(p.blocks, a.n_seq, p.n_seg), stc::THREADS, SMEM, a.stream>>>(ca);
+    ssm_chain_kernel<N, false><<<dim3(p.blocks, a.n_seq, p.n_seg), stc::THREADS, SMEM, a.stream>>>(ca, maps);
     return launched();
 }
 
