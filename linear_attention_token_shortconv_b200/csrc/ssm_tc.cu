@@ -34,9 +34,10 @@ using ssm::seq_range;
 namespace stc {
 constexpr int Q = 64;             // tokens per chunk
 constexpr int PREP_THREADS = 512;
-constexpr int REC = 336;          // floats of one (chunk, head) record
-// record: L log2 e [64] | u [64] | u e^R [64] | 2^ec e^L [64] | 2^ec umax [64] | e^L_end, umax
-constexpr int R_L = 0, R_U = 64, R_W = 128, R_YI = 192, R_YW = 256, R_DEC = 320, R_UMAX = 321;
+constexpr int REC = 368;          // floats of one (chunk, head) record
+// record: L log2 e [64] | u [64] | u e^R [64] | 2^ec e^L [64] | 2^ec umax [64] |
+// u e^{L_31 - L} of the first 32 tokens | e^L_end, umax
+constexpr int R_L = 0, R_U = 64, R_W = 128, R_YI = 192, R_YW = 256, R_UH = 320, R_DEC = 352, R_UMAX = 353;
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr uint32_t MAX_POLLS = 1u << 24;
 constexpr int THREADS = 512;
@@ -75,13 +76,23 @@ __device__ __forceinline__ float rcp(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-// x / (1 + e^-x): x = -inf gives -inf * 0 = NaN as the formula does
-__device__ __forceinline__ float silu_fast(float x) { return x * rcp(1.0f + ex2(-stc::kLog2e * x)); }
+// x / (1 + e^-x) of a pair with one reciprocal, 1 / a = b / (a b): the special-function
+// unit (16 results a clock) is what the chain has least of.  The exponent is kept below
+// 60 so that the product is finite; there x 2^-60 stands for x e^x.
+__device__ __forceinline__ float2 silu2(float2 x) {
+    const float2 e = fmul2(x, make_float2(-stc::kLog2e, -stc::kLog2e));
+    const float2 d = fadd2(make_float2(ex2(fminf(e.x, 60.f)), ex2(fminf(e.y, 60.f))), make_float2(1.f, 1.f));
+    const float r = rcp(d.x * d.y);
+    return fmul2(fmul2(x, make_float2(r, r)), make_float2(d.y, d.x));
+}
 
 __device__ __forceinline__ float2 half2_float2(uint32_t h) {
     __half2 p;
     *reinterpret_cast<uint32_t *>(&p) = h;
     return __half22float2(p);
+}
+__device__ __forceinline__ float2 as_float2(uint32_t a, uint32_t b) {
+    return make_float2(__uint_as_float(a), __uint_as_float(b));
 }
 __device__ __forceinline__ uint32_t pack(float2 v) { return umma::pack_half2(v.x, v.y); }
 __device__ __forceinline__ float amax2(float m, float2 v) { return fmaxf(m, fmaxf(fabsf(v.x), fabsf(v.y))); }
@@ -91,6 +102,19 @@ __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
     return p != 0;
+}
+
+// Shared memory by 32-bit address: a row's chunks are one exclusive or apart.
+__device__ __forceinline__ void sts64(uint32_t p, uint32_t a, uint32_t b) {
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(p), "r"(a), "r"(b) : "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t p, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t p) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p) : "memory");
+    return v;
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
@@ -174,12 +198,17 @@ __global__ void __launch_bounds__(stc::PREP_THREADS) ssm_prep_kernel(const PrepA
             float x[8];
             uint32_t m = 0;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float s = bias[e];
+            for (int e = 0; e < 8; e += 2) {
+                float s[2] = {bias[e], bias[e + 1]};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) s = fmaf(w[e][j], win[(i + j) & 3][e], s);
-                x[e] = r < len ? silu_fast(s) : 0.f;
-                m = max(m, __float_as_uint(x[e]) & 0x7fffffffu);
+                for (int j = 0; j < 4; ++j) {
+                    s[0] = fmaf(w[e][j], win[(i + j) & 3][e], s[0]);
+                    s[1] = fmaf(w[e + 1][j], win[(i + j) & 3][e + 1], s[1]);
+                }
+                const float2 v = silu2(make_float2(s[0], s[1]));
+                x[e] = r < len ? v.x : 0.f;
+                x[e + 1] = r < len ? v.y : 0.f;
+                m = max(m, max(__float_as_uint(x[e]) & 0x7fffffffu, __float_as_uint(x[e + 1]) & 0x7fffffffu));
             }
 #pragma unroll
             for (int o = 1; o < VEC; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -234,6 +263,7 @@ __global__ void __launch_bounds__(stc::PREP_THREADS) ssm_prep_kernel(const PrepA
                 }
             }
             const float half0 = __shfl_sync(0xffffffffu, pre[0], 31), half1 = __shfl_sync(0xffffffffu, suf[1], 0);
+            const float suf0 = suf[0];   // from the token to the end of the first half
             pre[1] += half0;
             suf[0] += half1;
             // sums after the token: the next token's inclusive suffix
@@ -256,6 +286,9 @@ __global__ void __launch_bounds__(stc::PREP_THREADS) ssm_prep_kernel(const PrepA
                 rec[R_YI + r] = ec[r] * expf(pre[i]);
                 rec[R_YW + r] = ec[r] * inv;
             }
+            // e^{L_31 - L_s}, the sum after s inside the first half
+            const float in_half = __shfl_down_sync(0xffffffffu, suf0, 1);
+            rec[R_UH + lane] = u[0] * expf(lane == 31 ? 0.f : in_half);
             if (lane == 0) {
                 rec[R_DEC] = expf(total);
                 rec[R_UMAX] = inv;
@@ -386,7 +419,7 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
 
     if (warp == 0) umma::tmem_alloc(tslot, 512);
     if (tid == 0) {
-        for (int i = 0; i < 7; ++i) umma::mbar_init(full + i, 1);
+        for (int i = 0; i < 7; ++i) umma::mbar_init(full + i, i == 4 ? 2 : 1);   // y: two products
         umma::mbar_init(bar_w, THREADS / 32);
         *abort_flag = 0;
         umma::fence_mbar_init();
@@ -486,7 +519,8 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
                 float2 v = w[4][e];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) v = ffma2(w[j][e], f[i + j][e], v);
-                xh[i][e] = in ? make_float2(silu_fast(v.x), silu_fast(v.y)) : make_float2(0.f, 0.f);
+                v = silu2(v);
+                xh[i][e] = in ? v : make_float2(0.f, 0.f);
                 m = amax2(m, xh[i][e]);
             }
         }
@@ -499,16 +533,13 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
     float decay0 = 1.f, decay1 = 1.f;   // of the whole segment (state pass)
     // operand addresses of this thread: a row's 16-byte chunks k, k ^ 1, ... differ by an
     // exclusive or with the chunk's bits
-    uint8_t *const p_x = sm + Sm::OFF_X + half * 8192 + umma::sw128_offset(4 * warp, (lane & 15) >> 1) + 8 * (lane & 1);
-    uint8_t *const p_s = sm + Sm::OFF_S + (cg >> 1) * (N * 128) + umma::sw128_offset(srow, (cg & 1) * 4);
+    const uint32_t sT = umma::smem_u32(sm);
+    const uint32_t p_x = sT + Sm::OFF_X + half * 8192 + umma::sw128_offset(4 * warp, (lane & 15) >> 1) + 8 * (lane & 1);
+    const uint32_t p_s = sT + Sm::OFF_S + (cg >> 1) * (N * 128) + umma::sw128_offset(srow, (cg & 1) * 4);
     const int hv = q >> 1, t = 32 * (q & 1) + lane;      // rows of y: half and token of this thread
     const int oc = 64 * hv + 16 * cg;                    // and its 16 columns
-    uint8_t *const p_o = sm + Sm::OFF_X + hv * 8192 + umma::sw128_offset(t, 2 * cg);
-    auto flip = [](auto *p, int bytes) {   // p with bits of the chunk index flipped (every tile is 1024-byte aligned)
-        return p + ((int)((umma::smem_u32(p) ^ (uint32_t)bytes) - umma::smem_u32(p)));
-    };
+    const uint32_t p_o = sT + Sm::OFF_X + hv * 8192 + umma::sw128_offset(t, 2 * cg);
     // matrix descriptors; the start address field counts 16 bytes
-    const uint32_t sT = umma::smem_u32(sm);
     const uint64_t d_tile = umma::sw128_desc(sT, 16, 1024);
     const uint64_t d_tile_mn = umma::sw128_desc(sT, N == 128 ? KB : 0, 1024);   // N = 64: rows 64.. repeat rows 0..
     const uint64_t d_x = umma::sw128_desc(sT + Sm::OFF_X, 8192, 1024);
@@ -548,7 +579,7 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
             const float2 xs2 = make_float2(xs, xs);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                uint8_t *p = flip(p_x, 16 * i) + 128 * i;
+                const uint32_t p = (p_x ^ (16 * i)) + 128 * i;
                 uint32_t x2[2], hi2[2], lo2[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -558,9 +589,9 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
                     const float2 h = half2_float2(hi2[e]);
                     lo2[e] = umma::pack_half2(v.x - h.x, v.y - h.y);
                 }
-                if (!STATE_ONLY) *reinterpret_cast<uint2 *>(p) = make_uint2(x2[0], x2[1]);
-                *reinterpret_cast<uint2 *>(p + (Sm::OFF_XH - Sm::OFF_X)) = make_uint2(hi2[0], hi2[1]);
-                *reinterpret_cast<uint2 *>(p + (Sm::OFF_XL - Sm::OFF_X)) = make_uint2(lo2[0], lo2[1]);
+                if (!STATE_ONLY) sts64(p, x2[0], x2[1]);
+                sts64(p + (Sm::OFF_XH - Sm::OFF_X), hi2[0], hi2[1]);
+                sts64(p + (Sm::OFF_XL - Sm::OFF_X), lo2[0], lo2[1]);
             }
         }
         if (!STATE_ONLY) {
@@ -573,20 +604,19 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
             if (srow < N) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    *reinterpret_cast<uint4 *>(flip(p_s, 16 * j)) =
-                        make_uint4(pack(fmul2(S[4 * j], ss2)), pack(fmul2(S[4 * j + 1], ss2)),
-                                   pack(fmul2(S[4 * j + 2], ss2)), pack(fmul2(S[4 * j + 3], ss2)));
+                    sts128(p_s ^ (16 * j), make_uint4(pack(fmul2(S[4 * j], ss2)), pack(fmul2(S[4 * j + 1], ss2)),
+                                                      pack(fmul2(S[4 * j + 2], ss2)), pack(fmul2(S[4 * j + 3], ss2))));
             }
         }
         umma::fence_proxy_async_smem();
         umma::tc_fence_before();
         __syncthreads();
         // The tensor pipe takes MMAs about as fast as it runs them, so their issuer waits
-        // along: three warps share the work, and the two whose results are needed later
-        // do theirs after their part of the convolution.
+        // along.  The four warps with no scores of their own to decay (tokens 0 .. 31
+        // against 32 .. 63) share that work and the copies.
         const uint64_t dt = d_tile + (uint32_t)(b * (Sm::TILE >> 4));
         constexpr int KS = N / 16;   // K steps over the state dim
-        if (!STATE_ONLY && warp == 0) {
+        if (!STATE_ONLY && warp == 8) {
             if (elect_one()) {
                 umma::tc_fence_after();
                 const uint32_t id = umma::idesc_f16(128, 64, false, false);
@@ -601,30 +631,7 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
             }
             __syncwarp();
         }
-        if (warp == 12) {
-            if (elect_one()) {
-                if (c >= 1 && c + 1 < chunks) issue(c + 1);
-                if (!STATE_ONLY) {
-                    // out of chunk c - 1 (written before the barrier) leaves; its tile takes z of chunk c + 1
-                    if (c >= 1) {
-                        const uint8_t *p = sm + Sm::OFF_Z + (b ^ 1) * 16384;
-                        umma::tma_store_3d(&maps.out, (int)xcol, 0, t0 - Q, p);
-                        if (live1) umma::tma_store_3d(&maps.out, (int)xcol + 64, 0, t0 - Q, p + 8192);
-                        umma::bulk_commit();
-                        umma::bulk_wait_read<0>();
-                    }
-                    if (a.z && c + 1 < chunks) issue_z(c + 1);
-                }
-            }
-            __syncwarp();
-        }
-        // ---- while they run: x of the next chunk
-        const float *recv = hv ? rec1 : rec0;
-        if (c + 1 < chunks) {
-            convolve(c + 1);
-            if (c + 2 < chunks) fetch(c + 2);
-        }
-        if (warp == 1) {
+        if (warp == 10) {
             if (elect_one()) {
                 umma::tc_fence_after();
                 const uint32_t id = umma::idesc_f16(128, 128, true, true);
@@ -640,55 +647,100 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
             }
             __syncwarp();
         }
+        if (warp == 14) {
+            if (elect_one() && c >= 1 && c + 1 < chunks) issue(c + 1);
+            __syncwarp();
+        }
+        if (!STATE_ONLY && warp == 12) {
+            if (elect_one() && c >= 1) {   // out of chunk c - 1, written before the barrier
+                const uint8_t *p = sm + Sm::OFF_Z + (b ^ 1) * 16384;
+                umma::tma_store_3d(&maps.out, (int)xcol, 0, t0 - Q, p);
+                if (live1) umma::tma_store_3d(&maps.out, (int)xcol + 64, 0, t0 - Q, p + 8192);
+                umma::bulk_commit();
+            }
+            __syncwarp();
+        }
+        // ---- while they run: x of the next chunk
+        const float *recv = hv ? rec1 : rec0;
+        if (c + 1 < chunks) {
+            convolve(c + 1);
+            if (c + 2 < chunks) fetch(c + 2);
+        }
+        if (!STATE_ONLY && warp == 12) {
+            if (elect_one() && a.z && c + 1 < chunks) {   // its tile takes z of chunk c + 1
+                umma::bulk_wait_read<0>();
+                issue_z(c + 1);
+            }
+            __syncwarp();
+        }
+        if (!STATE_ONLY && warp == 8) {
+            if (elect_one()) {
+                const uint32_t id = umma::idesc_f16(128, 64, false, true);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int k = 0; k < KS; ++k) {
+                        const uint32_t kb = ((k / 4) * KB + (k % 4) * 32) >> 4;
+                        umma::mma_f16(T_YI + 64 * j, dt + (kb + (j ? 0 : OFF_C >> 4)),
+                                      d_s + ((j * (N * 128) + k * 2048) >> 4), id, k > 0);
+                    }
+                umma::mma_commit(bar_y);
+            }
+            __syncwarp();
+        }
         if (!STATE_ONLY) {
             // ---- decayed scores: 16 of them per thread, as the A operand in tensor memory.
             // Half 0 (lanes 0..63) writes columns 64 .. 95 and half 1 columns 0 .. 31, where
             // the other half's scores lie in lanes that nobody reads.
             wait(bar_sc, ph);
             umma::tc_fence_after();
-            uint32_t sc[16], p[8];
-            umma::tmem_ld16_nowait(T_SC + lane_off + 64 * hv + 16 * cg, sc);
-            umma::tmem_ld_wait();
-            const float Lt = recv[R_L + t];
+            uint32_t p[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            if ((q & 1) || cg < 2) {   // tokens 0 .. 31 see nothing of 32 .. 63
+                uint32_t sc[16];
+                umma::tmem_ld16_nowait(T_SC + lane_off + 64 * hv + 16 * cg, sc);
+                umma::tmem_ld_wait();
+                const float Lt = recv[R_L + t];
+                if ((q & 1) && cg < 2) {
+                    // t > 31 >= s: e^{L_t - L_s} = e^{L_t - L_31} e^{L_31 - L_s}, both at most 1
+                    const float et = ex2(Lt - recv[R_L + 31]);
+                    const float2 et2 = make_float2(et, et);
 #pragma unroll
-            for (int s4 = 0; s4 < 4; ++s4) {
-                const int s = 16 * cg + 4 * s4;
-                const float4 l4 = *reinterpret_cast<const float4 *>(recv + R_L + s);
-                const float4 u4 = *reinterpret_cast<const float4 *>(recv + R_U + s);
-                float w0 = __uint_as_float(sc[4 * s4]) * u4.x * ex2(Lt - l4.x);
-                float w1 = __uint_as_float(sc[4 * s4 + 1]) * u4.y * ex2(Lt - l4.y);
-                float w2 = __uint_as_float(sc[4 * s4 + 2]) * u4.z * ex2(Lt - l4.z);
-                float w3 = __uint_as_float(sc[4 * s4 + 3]) * u4.w * ex2(Lt - l4.w);
-                if (s > t) w0 = 0.f;
-                if (s + 1 > t) w1 = 0.f;
-                if (s + 2 > t) w2 = 0.f;
-                if (s + 3 > t) w3 = 0.f;
-                p[2 * s4] = umma::pack_half2(w0, w1);
-                p[2 * s4 + 1] = umma::pack_half2(w2, w3);
+                    for (int s4 = 0; s4 < 4; ++s4) {
+                        const float4 u4 = *reinterpret_cast<const float4 *>(recv + R_UH + 16 * cg + 4 * s4);
+                        p[2 * s4] = pack(fmul2(fmul2(make_float2(u4.x, u4.y), et2), as_float2(sc[4 * s4], sc[4 * s4 + 1])));
+                        p[2 * s4 + 1] = pack(fmul2(fmul2(make_float2(u4.z, u4.w), et2), as_float2(sc[4 * s4 + 2], sc[4 * s4 + 3])));
+                    }
+                } else {
+#pragma unroll
+                    for (int s4 = 0; s4 < 4; ++s4) {
+                        const int s = 16 * cg + 4 * s4;
+                        const float4 l4 = *reinterpret_cast<const float4 *>(recv + R_L + s);
+                        const float4 u4 = *reinterpret_cast<const float4 *>(recv + R_U + s);
+                        float2 w0 = fmul2(as_float2(sc[4 * s4], sc[4 * s4 + 1]), make_float2(u4.x, u4.y));
+                        float2 w1 = fmul2(as_float2(sc[4 * s4 + 2], sc[4 * s4 + 3]), make_float2(u4.z, u4.w));
+                        w0 = fmul2(w0, make_float2(ex2(Lt - l4.x), ex2(Lt - l4.y)));
+                        w1 = fmul2(w1, make_float2(ex2(Lt - l4.z), ex2(Lt - l4.w)));
+                        p[2 * s4] = pack(make_float2(s > t ? 0.f : w0.x, s + 1 > t ? 0.f : w0.y));
+                        p[2 * s4 + 1] = pack(make_float2(s + 2 > t ? 0.f : w1.x, s + 3 > t ? 0.f : w1.y));
+                    }
+                }
             }
             umma::tmem_st8(T_SC + lane_off + (hv ? 0 : 64) + 8 * cg, p);
             umma::tmem_st_wait();
             umma::tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_w);
-            if (warp == 2) {
+            if (warp == 14) {
                 wait(bar_w, ph);
                 if (elect_one()) {
                     umma::tc_fence_after();
-                    const uint32_t idi = umma::idesc_f16(128, 64, false, true);
+                    const uint32_t id = umma::idesc_f16(128, 64, false, true);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
+                    for (int j = 0; j < 2; ++j)   // rows 64 j .. of the decayed scores, columns of half j
 #pragma unroll
-                        for (int k = 0; k < Q / 16; ++k)   // rows 64 j .. of the decayed scores, columns of half j
+                        for (int k = 0; k < Q / 16; ++k)
                             umma::mma_f16_ts(T_YW + 64 * j, T_SC + (j ? 0 : 64) + 8 * k,
-                                             d_x + ((j * 8192 + k * 2048) >> 4), idi, k > 0);
-#pragma unroll
-                        for (int k = 0; k < KS; ++k) {
-                            const uint32_t kb = ((k / 4) * KB + (k % 4) * 32) >> 4;
-                            umma::mma_f16(T_YI + 64 * j, dt + (kb + (j ? 0 : OFF_C >> 4)),
-                                          d_s + ((j * (N * 128) + k * 2048) >> 4), idi, k > 0);
-                        }
-                    }
+                                             d_x + ((j * 8192 + k * 2048) >> 4), id, k > 0);
                     umma::mma_commit(bar_y);
                 }
                 __syncwarp();
@@ -725,11 +777,11 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
             const float fi = recv[R_YI + t] * sinv, fw = recv[R_YW + t] * fx, fd = dskip * fx;
             const float2 fi2 = make_float2(fi, fi), fw2 = make_float2(fw, fw), fd2 = make_float2(fd, fd);
             bf16 *const o = a.out + (long long)(t0 + t) * (a.H * a.P) + xcol + oc;
-            uint8_t *const p_z = p_o + (Sm::OFF_Z - Sm::OFF_X) + b * 16384;
+            const uint32_t p_z = p_o + (Sm::OFF_Z - Sm::OFF_X) + b * 16384;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const uint4 xx = *reinterpret_cast<const uint4 *>(flip(p_o, 16 * k));
-                const uint4 zz = a.z ? *reinterpret_cast<const uint4 *>(flip(p_z, 16 * k)) : make_uint4(0, 0, 0, 0);
+                const uint4 xx = lds128(p_o ^ (16 * k));
+                const uint4 zz = a.z ? lds128(p_z ^ (16 * k)) : make_uint4(0, 0, 0, 0);
                 const uint32_t xw[4] = {xx.x, xx.y, xx.z, xx.w}, zw[4] = {zz.x, zz.y, zz.z, zz.w};
                 uint32_t w[4];
 #pragma unroll
@@ -738,12 +790,12 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
                     float2 y = fmul2(half2_float2(xw[e]), fd2);
                     y = ffma2(make_float2(__uint_as_float(yw[i]), __uint_as_float(yw[i + 1])), fw2, y);
                     y = ffma2(make_float2(__uint_as_float(yi[i]), __uint_as_float(yi[i + 1])), fi2, y);
-                    if (a.z) y = fmul2(y, make_float2(silu_fast(bf16lo(zw[e])), silu_fast(bf16hi(zw[e]))));
+                    if (a.z) y = fmul2(y, silu2(make_float2(bf16lo(zw[e]), bf16hi(zw[e]))));
                     const __nv_bfloat162 pb = __floats2bfloat162_rn(y.x, y.y);
                     w[e] = *reinterpret_cast<const uint32_t *>(&pb);
                 }
                 const uint4 w4 = make_uint4(w[0], w[1], w[2], w[3]);
-                if (len == Q) *reinterpret_cast<uint4 *>(flip(p_z, 16 * k)) = w4;
+                if (len == Q) sts128(p_z ^ (16 * k), w4);
                 else if (t < len && (hv == 0 || live1)) reinterpret_cast<uint4 *>(o)[k] = w4;
             }
             umma::fence_proxy_async_smem();
