@@ -945,8 +945,8 @@ gdn_status_t gdn_quant_fp8(int rows, int cols, const void *x, int64_t ld_x, gdn_
     if (!aligned16(x) || !aligned16(q) || !aligned_to(scale, 4) || ld_q % 16 != 0 ||
         ld_x % (in_dtype == GDN_BF16 ? 8 : 4) != 0)
         return GDN_ERR_ALIGNMENT;
-    // grid limits: 64 row blocks, or one row of 128 x 128 blocks, per CTA row
-    if ((int64_t)rows * ((cols + 127) / 128) > (int64_t)1 << 36 || (block_rows == 128 && rows > 65535 * 128))
+    // row blocks are counted in 32 bits; one grid row per 128 rows of 128 x 128 blocks
+    if ((int64_t)rows * ((cols + 127) / 128) >= (int64_t)1 << 31 || (block_rows == 128 && rows > 65535 * 128))
         return GDN_ERR_UNSUPPORTED;
     const cudaError_t e = gdn::launch_quant_fp8(rows, cols, x, ld_x, in_dtype == GDN_BF16, block_rows, q, ld_q, scale,
                                                 reinterpret_cast<cudaStream_t>(stream));

@@ -46,16 +46,25 @@ constexpr int QB = 4;   // row blocks per half warp
 
 template <typename T>
 __global__ void __launch_bounds__(256)
-quant_rows_kernel(const T *__restrict__ x, long long ld_x, long long n_blocks, int cols, int cb,
+quant_rows_kernel(const T *__restrict__ x, long long ld_x, uint32_t n_blocks, int cols, uint32_t cb,
                   uint8_t *__restrict__ q, long long ld_q, float *__restrict__ scale) {
     const int sub = threadIdx.x & 15;
-    const long long first = ((long long)blockIdx.x * 16 + (threadIdx.x >> 4)) * QB;
+    const uint32_t first = (blockIdx.x * 16 + (threadIdx.x >> 4)) * QB;
+    // row and column of this half warp's row blocks, which follow one another
+    uint32_t r[QB], c[QB];
+    r[0] = first / cb;
+    c[0] = first - r[0] * cb;
+#pragma unroll
+    for (int i = 1; i < QB; ++i) {
+        const bool wrap = c[i - 1] + 1 == cb;
+        r[i] = r[i - 1] + wrap;
+        c[i] = wrap ? 0 : c[i - 1] + 1;
+    }
     float v[QB][8];
 #pragma unroll
     for (int i = 0; i < QB; ++i) {
-        const long long b = first + i, r = b / cb;
-        const int c = (int)(b - r * cb) * 128 + 8 * sub;
-        if (b < n_blocks && c < cols) load8(x + r * ld_x + c, v[i]);
+        const int col = (int)c[i] * 128 + 8 * sub;
+        if (first + i < n_blocks && col < cols) load8(x + r[i] * ld_x + col, v[i]);
         else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
@@ -67,11 +76,10 @@ quant_rows_kernel(const T *__restrict__ x, long long ld_x, long long n_blocks, i
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
         const float amax = block_amax(m);
-        const long long b = first + i, r = b / cb;
-        const int c = (int)(b - r * cb) * 128 + 8 * sub;
-        if (b < n_blocks) {
-            if (sub == 0) scale[b] = __fdiv_rn(amax, kFp8Max);
-            if (c < cols) *reinterpret_cast<uint2 *>(q + r * ld_q + c) = to_e4m3x8(v[i], __fdiv_rn(kFp8Max, amax));
+        const int col = (int)c[i] * 128 + 8 * sub;
+        if (first + i < n_blocks) {
+            if (sub == 0) scale[first + i] = __fdiv_rn(amax, kFp8Max);
+            if (col < cols) *reinterpret_cast<uint2 *>(q + r[i] * ld_q + col) = to_e4m3x8(v[i], __fdiv_rn(kFp8Max, amax));
         }
     }
 }
@@ -115,7 +123,7 @@ cudaError_t launch_quant(int rows, int cols, const void *x, long long ld_x, int 
     if (block_rows == 1) {
         const long long n = (long long)rows * cb, per_cta = 16 * QB;
         quant_rows_kernel<T><<<(unsigned)((n + per_cta - 1) / per_cta), 256, 0, stream>>>(
-            static_cast<const T *>(x), ld_x, n, cols, cb, static_cast<uint8_t *>(q), ld_q, scale);
+            static_cast<const T *>(x), ld_x, (uint32_t)n, cols, (uint32_t)cb, static_cast<uint8_t *>(q), ld_q, scale);
     } else {
         quant_tiles_kernel<T><<<dim3(cb, (rows + 127) / 128), 256, 0, stream>>>(
             static_cast<const T *>(x), ld_x, rows, cols, static_cast<uint8_t *>(q), ld_q, scale);

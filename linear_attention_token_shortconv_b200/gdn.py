@@ -521,47 +521,99 @@ def decode_multi(q, k, v, conv_w, conv_hist, a_logit, b_logit, A, b_alpha, z, no
     return out
 
 
+def _bad(name, t, shape, dtype):
+    """Raises the error that _expect gives for this tensor (or a shape's)."""
+    _expect(name, t, shape, dtype)
+    raise ValueError(f"{name}: expected {tuple(shape)} {dtype}")
+
+
+def _packed(name, t, shape, dtype):
+    """_expect for a tensor that must also be contiguous (None: absent, accepted)."""
+    if t is not None:
+        if t.dtype is not dtype or t.shape != shape:
+            _bad(name, t, shape, dtype)
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: must be contiguous")
+
+
 def _token_ld(name, t, shape, dtype):
     """Elements from one token of `t` to the next, after checking its shape and dtype.
     Tokens may lie apart (a column block of a projection result); within a token the
     elements must be packed."""
-    _expect(name, t, shape, dtype)
+    if t.dtype is not dtype or t.shape != shape:
+        _bad(name, t, shape, dtype)
+    st = t.stride()
     want = 1
-    for n, st in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if n != 1 and st != want:
-            raise ValueError(f"{name}: the elements of a token must be packed (strides {t.stride()})")
-        want *= n
-    if t.shape[0] <= 1:
+    for i in range(len(shape) - 1, 0, -1):
+        if st[i] != want and shape[i] != 1:
+            raise ValueError(f"{name}: the elements of a token must be packed (strides {st})")
+        want *= shape[i]
+    if shape[0] <= 1:
         return 0
-    if t.stride(0) < want:
-        raise ValueError(f"{name}: tokens overlap (strides {t.stride()})")
-    return t.stride(0)
+    if st[0] < want:
+        raise ValueError(f"{name}: tokens overlap (strides {st})")
+    return st[0]
 
 
-def _raw(t):
-    """Address of a strided tensor whose layout has been checked (None: absent)."""
-    return None if t is None or not t.numel() else t.data_ptr()
+def _addresses(*ts):
+    """(device index, addresses) of tensors whose layout has been checked; None or an
+    empty tensor gives 0.  All must be on one CUDA device."""
+    dev, ptrs = -1, []
+    for t in ts:
+        if t is None:
+            ptrs.append(None)
+            continue
+        d = t.get_device()
+        if d < 0:
+            raise ValueError("all tensors must live on a CUDA device")
+        if dev < 0:
+            dev = d
+        elif d != dev:
+            raise ValueError(f"tensors on cuda:{dev} and cuda:{d}: all must be on one device")
+        ptrs.append(t.data_ptr() or None)
+    return dev, ptrs
+
+
+def _call(fn, where, dev, stream, *args):
+    """Runs a library call on device `dev`, on `stream` or that device's current one."""
+    if dev == torch.cuda.current_device():
+        s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+        rc = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+            rc = fn(*args, s)
+    if rc != 0:
+        raise GdnError(rc, where)
 
 
 def _ssm_dims(x, B, C, dt_logit, conv_w, conv_b, A, b_dt, D, z, out, n_seq):
-    if x.dim() != 3 or B.dim() != 3:
-        raise ValueError("x [N_tok, H, P] and B, C [N_tok, G, N] expected")
-    n_tok, H, P = x.shape
-    G, N = B.shape[1:]
-    if x.dtype not in (BF16, F32):
-        raise TypeError(f"x: dtype {x.dtype}, expected {BF16} or {F32}")
+    if x.dim() != 3 or B.dim() != 3 or conv_w.dim() != 2:
+        raise ValueError("x [N_tok, H, P], B, C [N_tok, G, N] and conv_w [channels, K] expected")
+    tok, group = x.shape, B.shape
+    n_tok, H, P = tok
+    G, N = group[1:]
+    io = x.dtype
+    if io is not BF16 and io is not F32:
+        raise TypeError(f"x: dtype {io}, expected {BF16} or {F32}")
+    if group[0] != n_tok:
+        _bad("B", B, (n_tok, G, N), io)
     chans = H * P + 2 * G * N
-    lds = [_token_ld("x", x, (n_tok, H, P), x.dtype), _token_ld("B", B, (n_tok, G, N), x.dtype),
-           _token_ld("C", C, (n_tok, G, N), x.dtype),
-           0 if z is None else _token_ld("z", z, (n_tok, H, P), x.dtype),
-           _token_ld("dt_logit", dt_logit, (n_tok, H), x.dtype)]
-    _expect("conv_w", conv_w, (chans, None), F32)
-    _expect("conv_b", conv_b, (chans,), F32)
-    _expect("A", A, (H,), F32)
-    _expect("b_dt", b_dt, (H,), F32)
-    _expect("D", D, (H,), F32)
-    _expect("out", out, (n_tok, H, P), (F32, BF16))
-    return SsmDims(n_seq, n_tok, H, G, P, N, conv_w.shape[1], _dt(x), _dt(out), *lds), chans
+    heads = (H,)
+    ld_x, ld_B = _token_ld("x", x, tok, io), _token_ld("B", B, group, io)
+    ld_C, ld_dt = _token_ld("C", C, group, io), _token_ld("dt_logit", dt_logit, (n_tok, H), io)
+    ld_z = 0 if z is None else _token_ld("z", z, tok, io)
+    _packed("conv_w", conv_w, (chans, conv_w.shape[1]), F32)
+    _packed("conv_b", conv_b, (chans,), F32)
+    _packed("A", A, heads, F32)
+    _packed("b_dt", b_dt, heads, F32)
+    _packed("D", D, heads, F32)
+    if out.dtype is not F32 and out.dtype is not BF16:
+        raise TypeError(f"out: dtype {out.dtype}, expected {F32} or {BF16}")
+    _packed("out", out, tok, out.dtype)
+    dims = SsmDims(n_seq, n_tok, H, G, P, N, conv_w.shape[1], GDN_BF16 if io is BF16 else GDN_F32,
+                   GDN_BF16 if out.dtype is BF16 else GDN_F32, ld_x, ld_B, ld_C, ld_z, ld_dt)
+    return dims, (n_seq, 3, chans), (n_seq, H, N, P)
 
 
 def ssm_prefill(x, B, C, dt_logit, conv_w, A, b_dt, *, conv_b=None, D=None, z=None, S0=None, conv_hist=None,
@@ -579,24 +631,20 @@ def ssm_prefill(x, B, C, dt_logit, conv_w, A, b_dt, *, conv_b=None, D=None, z=No
         n_seq = num_seqs if num_seqs is not None else (S0.shape[0] if S0 is not None else 1)
     if out is None:
         out = torch.empty(x.shape, dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
-    dims, chans = _ssm_dims(x, B, C, dt_logit, conv_w, conv_b, A, b_dt, D, z, out, n_seq)
-    state, hist = (n_seq, dims.H, dims.N, dims.P), (n_seq, 3, chans)
+    dims, hist, state = _ssm_dims(x, B, C, dt_logit, conv_w, conv_b, A, b_dt, D, z, out, n_seq)
     if want_state:
         if S_final is None:
             S_final = torch.empty(state, dtype=F32, device=x.device)
         if conv_tail is None:
             conv_tail = torch.empty(hist, dtype=x.dtype, device=x.device)
-    _expect("S0", S0, state, F32)
-    _expect("S_final", S_final, state, F32)
-    _expect("conv_hist", conv_hist, hist, x.dtype)
-    _expect("conv_tail", conv_tail, hist, x.dtype)
-    _expect("cu_seqlens", cu_seqlens, (n_seq + 1,), I32)
-    with torch.cuda.device(_device(x, B, C, dt_logit, conv_w, conv_b, A, b_dt, D, z, S0, conv_hist, cu_seqlens, out,
-                                   S_final, conv_tail)):
-        rc = load().gdn_ssm_prefill(ctypes.byref(dims), _raw(x), _raw(B), _raw(C), _raw(dt_logit), _ptr(conv_w),
-                                    _ptr(conv_b), _ptr(A), _ptr(b_dt), _ptr(D), _raw(z), _ptr(S0), _ptr(conv_hist),
-                                    _ptr(cu_seqlens), _ptr(out), _ptr(S_final), _ptr(conv_tail), _stream(stream))
-    _check(rc, "gdn_ssm_prefill")
+    _packed("S0", S0, state, F32)
+    _packed("S_final", S_final, state, F32)
+    _packed("conv_hist", conv_hist, hist, x.dtype)
+    _packed("conv_tail", conv_tail, hist, x.dtype)
+    _packed("cu_seqlens", cu_seqlens, (n_seq + 1,), I32)
+    dev, ptrs = _addresses(x, B, C, dt_logit, conv_w, conv_b, A, b_dt, D, z, S0, conv_hist, cu_seqlens, out, S_final,
+                           conv_tail)
+    _call(load().gdn_ssm_prefill, "gdn_ssm_prefill", dev, stream, ctypes.byref(dims), *ptrs)
     return out, S_final, conv_tail
 
 
@@ -616,28 +664,27 @@ def ssm_decode_step(x, B, C, dt_logit, conv_w, conv_hist, A, b_dt, S, *, conv_b=
     in place.  out_dtype defaults to x.dtype.  Returns out [B, H, P]."""
     if out is None:
         out = torch.empty(x.shape, dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
-    dims, chans = _ssm_dims(x, B, C, dt_logit, conv_w, conv_b, A, b_dt, D, z, out, x.shape[0])
-    _expect("conv_hist", conv_hist, (dims.num_seqs, 3, chans), x.dtype)
-    _expect("S", S, (dims.num_seqs, dims.H, dims.N, dims.P), F32)
-    with torch.cuda.device(_device(x, B, C, dt_logit, conv_w, conv_b, conv_hist, A, b_dt, D, z, S, out)):
-        rc = load().gdn_ssm_decode_step(ctypes.byref(dims), _raw(x), _raw(B), _raw(C), _raw(dt_logit), _ptr(conv_w),
-                                        _ptr(conv_b), _ptr(conv_hist), _ptr(A), _ptr(b_dt), _ptr(D), _raw(z),
-                                        _ptr(S), _ptr(out), _stream(stream))
-    _check(rc, "gdn_ssm_decode_step")
+    dims, hist, state = _ssm_dims(x, B, C, dt_logit, conv_w, conv_b, A, b_dt, D, z, out, x.shape[0])
+    if conv_hist is None or S is None:
+        raise ValueError("conv_hist and S are required")
+    _packed("conv_hist", conv_hist, hist, x.dtype)
+    _packed("S", S, state, F32)
+    dev, ptrs = _addresses(x, B, C, dt_logit, conv_w, conv_b, conv_hist, A, b_dt, D, z, S, out)
+    _call(load().gdn_ssm_decode_step, "gdn_ssm_decode_step", dev, stream, ctypes.byref(dims), *ptrs)
     return out
 
 
 E4M3 = torch.float8_e4m3fn
 
 
-def _matrix_ld(name, t, shape, dtypes):
-    """Row stride of a matrix with packed rows, after checking its shape and dtype."""
-    _expect(name, t, shape, dtypes)
-    if t.shape[1] > 1 and t.stride(1) != 1:
+def _matrix_ld(name, t):
+    """Row stride of a matrix with packed rows."""
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
         raise ValueError(f"{name}: rows must be contiguous (strides {t.stride()})")
-    if t.shape[0] <= 1:
-        return -(-t.shape[1] // 16) * 16   # one row: any pitch will do
-    if t.stride(0) < t.shape[1]:
+    if rows <= 1:
+        return -(-cols // 16) * 16   # one row: any pitch will do
+    if t.stride(0) < cols:
         raise ValueError(f"{name}: rows overlap (strides {t.stride()})")
     return t.stride(0)
 
@@ -656,14 +703,17 @@ def quant_fp8(x, block_rows=1, *, q=None, scale=None, stream=None):
     shape = (-(-rows // block_rows), -(-cols // 128))
     if q is None:
         q = torch.empty((rows, cols), dtype=E4M3, device=x.device)
+    elif q.dtype is not E4M3 or q.shape != (rows, cols):
+        _bad("q", q, (rows, cols), E4M3)
     if scale is None:
         scale = torch.empty(shape, dtype=F32, device=x.device)
-    ld_x, ld_q = _matrix_ld("x", x, (rows, cols), (BF16, F32)), _matrix_ld("q", q, (rows, cols), E4M3)
-    _expect("scale", scale, shape, F32)
-    with torch.cuda.device(_device(x, q, scale)):
-        rc = load().gdn_quant_fp8(rows, cols, _raw(x), ld_x, _dt(x), block_rows, _raw(q), ld_q, _ptr(scale),
-                                  _stream(stream))
-    _check(rc, "gdn_quant_fp8")
+    if x.dtype is not BF16 and x.dtype is not F32:
+        raise TypeError(f"x: dtype {x.dtype}, expected {BF16} or {F32}")
+    _packed("scale", scale, shape, F32)
+    ld_x, ld_q = _matrix_ld("x", x), _matrix_ld("q", q)
+    dev, (px, pq, ps) = _addresses(x, q, scale)
+    _call(load().gdn_quant_fp8, "gdn_quant_fp8", dev, stream, rows, cols, px, ld_x,
+          GDN_BF16 if x.dtype is BF16 else GDN_F32, block_rows, pq, ld_q, ps)
     return q, scale
 
 
@@ -675,17 +725,23 @@ def gemm_fp8(a, a_scale, b, b_scale, *, out=None, out_dtype=torch.bfloat16, stre
         raise ValueError("a [M, K] and b [N, K] expected")
     M, K = a.shape
     N = b.shape[0]
+    if a.dtype is not E4M3:
+        raise TypeError(f"a: dtype {a.dtype}, expected {E4M3}")
+    if b.dtype is not E4M3 or b.shape[1] != K:
+        _bad("b", b, (N, K), E4M3)
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype, device=a.device)
-    lda, ldb = _matrix_ld("a", a, (M, K), E4M3), _matrix_ld("b", b, (N, K), E4M3)
-    ldc = _matrix_ld("out", out, (M, N), (BF16, F32))
+    if out.dtype is not BF16 and out.dtype is not F32:
+        raise TypeError(f"out: dtype {out.dtype}, expected {F32} or {BF16}")
+    if out.shape != (M, N):
+        _bad("out", out, (M, N), out.dtype)
     kb = -(-K // 128)
-    _expect("a_scale", a_scale, (M, kb), F32)
-    _expect("b_scale", b_scale, (-(-N // 128), kb), F32)
-    with torch.cuda.device(_device(a, a_scale, b, b_scale, out)):
-        rc = load().gdn_gemm_fp8(M, N, K, _raw(a), lda, _ptr(a_scale), _raw(b), ldb, _ptr(b_scale), _raw(out), ldc,
-                                 _dt(out), _stream(stream))
-    _check(rc, "gdn_gemm_fp8")
+    _packed("a_scale", a_scale, (M, kb), F32)
+    _packed("b_scale", b_scale, (-(-N // 128), kb), F32)
+    lda, ldb, ldc = _matrix_ld("a", a), _matrix_ld("b", b), _matrix_ld("out", out)
+    dev, (pa, psa, pb, psb, pc) = _addresses(a, a_scale, b, b_scale, out)
+    _call(load().gdn_gemm_fp8, "gdn_gemm_fp8", dev, stream, M, N, K, pa, lda, psa, pb, ldb, psb, pc, ldc,
+          GDN_BF16 if out.dtype is BF16 else GDN_F32)
     return out
 
 
