@@ -70,6 +70,7 @@ cudaError_t make_tma_rows_f32(TmaMap *out, const void *base, int cols, int rows,
 cudaError_t make_tma_mat_bf16(TmaMap *out, const void *base, int inner, int rows, int ld, int box_inner,
                               int box_rows);
 cudaError_t make_tma_mat_u8(TmaMap *out, const void *base, int inner, int rows, long long ld, int box_rows);
+cudaError_t make_tma_mat_out(TmaMap *out, const void *base, bool bf16, int inner, int rows, long long ld);
 cudaError_t make_tma_plain_bf16(TmaMap *out, const void *base, int rank, const long long *dims,
                                 const long long *strides, const int *box);
 // K7: C [M, N] = A [M, K] B [K, N], bf16 row-major with leading dimensions lda,

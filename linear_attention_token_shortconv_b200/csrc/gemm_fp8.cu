@@ -12,8 +12,8 @@
 // read it, multiply by the block's scale and add it into fp32 registers while the
 // next block's MMAs fill another buffer.
 //
-// Roles: warp 0 lane 0 loads by TMA, warp 1 lane 0 issues the MMAs (and owns the
-// TMEM), the others are the epilogue.  Every wait is bounded; one that expires raises
+// Roles: warp 0 loads by TMA, warp 1 issues the MMAs (and owns the
+// TMEM), warp 2 fetches the scales, warps 4 and up are the epilogue.  Every wait is bounded; one that expires raises
 // the error word and an abort flag that the other roles check.
 //
 // Two operand orders.  Many tokens: tokens are the MMA's 128 rows and features its BN
@@ -39,26 +39,33 @@ __device__ unsigned int g_fp8_err;
 namespace fp8 {
 constexpr int BM = 128, BK = 128;
 constexpr uint32_t MAX_POLLS = 1u << 24;
+constexpr int NSC = 8, SC_SLOT = 132;   // ring of scales: 128 of A's rows, two of B's blocks
 
 template <int BN_, bool SWAP_> struct Shape {
     static constexpr int BN = BN_;
     static constexpr bool SWAP = SWAP_;
     static constexpr int A_ST = BM * BK, B_ST = BN * BK, ST = A_ST + B_ST;
-    static constexpr int NS = 196608 / ST < 8 ? 196608 / ST : 8;
+    static constexpr int EPI_WARPS = BN >= 128 ? 8 : 4;
+    static constexpr int OUT_WARP = SWAP ? 0 : 32 * (EPI_WARPS == 8 ? BN / 2 : BN) * 2;   // result rows of a warp, bf16
+    static constexpr int OUT = OUT_WARP * EPI_WARPS;
+    static constexpr int NS = (226304 - OUT) / ST < 8 ? (226304 - OUT) / ST : 8;
     static constexpr int NT = 512 / BN < 4 ? 512 / BN : 4;            // TMEM buffers
     static constexpr uint32_t TMEM_COLS = NT * BN;                      // 64 .. 512, a power of two
-    static constexpr int EPI_WARPS = BN >= 128 ? 8 : 4;
     static constexpr int EPC = EPI_WARPS == 8 ? BN / 2 : BN;            // columns of an epilogue thread
-    static constexpr int THREADS = 64 + 32 * EPI_WARPS;
-    static constexpr int OFF_BAR = NS * ST;
-    static constexpr int SMEM = OFF_BAR + 256 + 1024;                   // barriers; alignment slack
+    static constexpr int THREADS = 128 + 32 * EPI_WARPS;                // warp 3 idle: registers are split by groups of 4
+    static constexpr int OFF_OUT = NS * ST;
+    static constexpr int OFF_SC = OFF_OUT + OUT;
+    static constexpr int OFF_BAR = OFF_SC + NSC * SC_SLOT * 4;
+    static constexpr int SMEM = OFF_BAR + 384 + 1024;                   // barriers; alignment slack
     static constexpr int PART_LD = SWAP ? BM : BN + 4;                  // split: row length of the fp32 part
-    static_assert((SWAP ? BN * BM : BM * (BN + 4)) * 4 <= OFF_BAR, "the split's part fits in the stages");
+    static_assert((SWAP ? BN * BM : BM * (BN + 4)) * 4 <= OFF_OUT, "the split's part fits in the stages");
+    static_assert(SMEM <= 232448, "227 KB per block");
 };
 }  // namespace fp8
 
 struct Fp8Maps {
     CUtensorMap a, b;   // MMA rows (box 128 x 128 bytes) and columns (box 128 bytes x BN)
+    CUtensorMap c;      // the result, boxes of 128 bytes x 32 rows (where its rows are 16-byte aligned)
 };
 
 namespace {
@@ -73,9 +80,31 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint6
         : "memory");
 }
 
+// True in one lane of a converged warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
+
 __device__ __forceinline__ void arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(umma::smem_u32(bar)) : "memory");
 }
+
+// Registers move from the loading warps to the epilogue: 4 warps x 56 + 8 x 224 is what
+// 12 warps x 168 were launched with.
+template <int R> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R> __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
+
+// A 4-byte asynchronous copy to shared memory, zero where `in` is false (src is then any
+// valid address); an arrival on `bar` once this thread's earlier copies have landed.
+__device__ __forceinline__ void copy4(uint32_t dst, const float *src, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(umma::smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -89,19 +118,19 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr, int rank) {
     return v;
 }
 
-__device__ __forceinline__ void store8v(__nv_bfloat16 *p, const float *x) {
-    uint4 u;
-    uint32_t *w = reinterpret_cast<uint32_t *>(&u);
+// One 16-byte chunk of a result row.
+template <typename T> __device__ __forceinline__ void store_chunk(uint8_t *p, const float *x);
+template <> __device__ __forceinline__ void store_chunk<__nv_bfloat16>(uint8_t *p, const float *x) {
+    uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
         memcpy(w + e, &b, 4);
     }
-    *reinterpret_cast<uint4 *>(p) = u;
+    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ void store8v(float *p, const float *x) {
-    reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+template <> __device__ __forceinline__ void store_chunk<float>(uint8_t *p, const float *x) {
+    *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
 }
 
 }  // namespace
@@ -109,14 +138,15 @@ __device__ __forceinline__ void store8v(float *p, const float *x) {
 template <class Sh, typename Tout>
 __global__ void __launch_bounds__(Sh::THREADS, 1)
 gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const float *__restrict__ a_scale,
-                const float *__restrict__ b_scale, Tout *__restrict__ C, long long ldc, int split) {
+                const float *__restrict__ b_scale, Tout *__restrict__ C, long long ldc, int split, int tma_out) {
     using namespace fp8;
     constexpr int BN = Sh::BN, NS = Sh::NS, NT = Sh::NT, EPC = Sh::EPC;
     constexpr bool SWAP = Sh::SWAP;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = umma::align_smem<1024>(smem_raw);
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + Sh::OFF_BAR), *empty = full + NS;
-    uint64_t *tfull = empty + NS, *tempty = tfull + NT, *mma_done = tempty + NT;
+    uint64_t *tfull = empty + NS, *tempty = tfull + NT, *sfull = tempty + NT, *sempty = sfull + NSC;
+    uint64_t *mma_done = sempty + NSC;
     uint32_t *tslot = reinterpret_cast<uint32_t *>(mma_done + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tslot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -138,6 +168,10 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
             umma::mbar_init(tfull + i, 1);
             umma::mbar_init(tempty + i, Sh::EPI_WARPS);
         }
+        for (int i = 0; i < NSC; ++i) {
+            umma::mbar_init(sfull + i, 32);
+            umma::mbar_init(sempty + i, Sh::EPI_WARPS);
+        }
         umma::mbar_init(mma_done, 1);
         *abort_flag = 0;
         umma::fence_mbar_init();
@@ -149,28 +183,37 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
     const uint32_t tbase = *tslot;
 
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-        if (*abort_flag) return false;
-        if (umma::mbar_wait_bounded(bar, parity, MAX_POLLS)) return true;
+        for (uint32_t i = 0; i < MAX_POLLS; ++i) {
+            if (umma::mbar_try_wait(bar, parity)) return true;
+            if ((i & 63u) == 63u && *abort_flag) return false;
+        }
         atomicOr(&g_fp8_err, 1u);
         *abort_flag = 1;
         return false;
     };
 
-    if (warp == 0 && lane == 0) {
+    constexpr bool MOVE_REGS = Sh::EPI_WARPS == 8;
+    if (warp < 4) {
+    if constexpr (MOVE_REGS) regs_dec<56>();
+    // Loading and issuing warps walk their loops with all lanes and elect one for the
+    // instruction itself: loops of a lone lane lose the uniform registers that descriptors
+    // and barriers are addressed with.
+    if (warp == 0) {
         // ---------------------------------------------------------------- producer
-        umma::prefetch_tensormap(&maps.a);
-        umma::prefetch_tensormap(&maps.b);
         int st = 0, issued = 0;
         uint32_t ph = 1;
         bool ok = true;
         for (long long t = first; ok && t < n_tiles; t += step) {
             const int tr = (int)(t % tiles_r), tc = (int)(t / tiles_r);
             for (int kb = k_lo; kb < k_hi; ++kb) {
-                if (!(ok = wait(empty + st, ph))) break;
-                uint8_t *buf = sm + st * Sh::ST;
-                umma::mbar_expect_tx(full + st, Sh::ST);
-                umma::tma_load_3d(buf, &maps.a, BK * kb, 0, BM * tr, full + st);
-                umma::tma_load_3d(buf + Sh::A_ST, &maps.b, BK * kb, 0, BN * tc, full + st);
+                if (!(ok = __all_sync(0xffffffffu, wait(empty + st, ph)))) break;
+                if (elect_one()) {
+                    uint8_t *buf = sm + st * Sh::ST;
+                    umma::mbar_expect_tx(full + st, Sh::ST);
+                    umma::tma_load_3d(buf, &maps.a, BK * kb, 0, BM * tr, full + st);
+                    umma::tma_load_3d(buf + Sh::A_ST, &maps.b, BK * kb, 0, BN * tc, full + st);
+                }
+                __syncwarp();
                 if (issued < NS) ++issued;
                 if (++st == NS) { st = 0; ph ^= 1; }
             }
@@ -181,24 +224,27 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
                 if (--st < 0) { st = NS - 1; ph ^= 1; }
                 umma::mbar_wait_bounded(full + st, ph ^ 1, MAX_POLLS);
             }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
         // --------------------------------------------------------------- MMA issuer
-        const uint32_t idesc = umma::idesc_f16(BM, BN, false, false);   // format 0 is e4m3 in this kind
-        const uint32_t base = umma::smem_u32(sm);
+        constexpr uint32_t idesc = umma::idesc_f16(BM, BN, false, false);   // format 0 is e4m3 in this kind
+        const uint64_t d0 = umma::sw128_desc(umma::smem_u32(sm), 16, 1024);
         int st = 0, ts = 0;
         uint32_t ph = 0, tph = 1;
         bool ok = true, any = false;
         for (long long t = first; ok && t < n_tiles; t += step) {
             for (int kb = k_lo; kb < k_hi; ++kb) {
-                if (!(ok = wait(tempty + ts, tph)) || !(ok = wait(full + st, ph))) break;
+                ok = wait(tempty + ts, tph) && wait(full + st, ph);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 umma::tc_fence_after();
-                const uint64_t ad = umma::sw128_desc(base + st * Sh::ST, 16, 1024);
-                const uint64_t bd = umma::sw128_desc(base + st * Sh::ST + Sh::A_ST, 16, 1024);
+                if (elect_one()) {
+                    const uint64_t ad = d0 + (uint32_t)st * (Sh::ST >> 4), bd = ad + (Sh::A_ST >> 4);
 #pragma unroll
-                for (int ks = 0; ks < BK / 32; ++ks)   // 32 bytes of K: start address + 2 (units of 16)
-                    mma_e4m3(tbase + ts * BN, ad + 2 * ks, bd + 2 * ks, idesc, ks > 0);
-                umma::mma_commit(empty + st);
-                umma::mma_commit(tfull + ts);
+                    for (int ks = 0; ks < BK / 32; ++ks)   // 32 bytes of K: start address + 2 (units of 16)
+                        mma_e4m3(tbase + ts * BN, ad + 2 * ks, bd + 2 * ks, idesc, ks > 0);
+                    umma::mma_commit(empty + st);
+                    umma::mma_commit(tfull + ts);
+                }
+                __syncwarp();
                 any = true;
                 if (++st == NS) { st = 0; ph ^= 1; }
                 if (++ts == NT) { ts = 0; tph ^= 1; }
@@ -206,50 +252,66 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
         }
         // after an abort the epilogue may not have waited for the last MMAs: they
         // complete before the tensor memory is released
-        if (any && *abort_flag) {
+        if (any && *abort_flag && elect_one()) {
             umma::mma_commit(mma_done);
             umma::mbar_wait_bounded(mma_done, 0, MAX_POLLS);
         }
-    } else if (warp >= 2) {
+    } else if (warp == 2) {
+        // ------------------------------------------------------------------- scales
+        // They come from L2, whose latency is several K blocks' MMAs: 4-byte asynchronous
+        // copies into a ring, in flight for many blocks at once.
+        int ss = 0;
+        uint32_t sph = 1;
+        bool ok = true;
+        for (long long t = first; ok && t < n_tiles; t += step) {
+            const int tr = (int)(t % tiles_r), tc = (int)(t / tiles_r);
+            // tokens of the tile (rows, or columns in the swapped order) and blocks of features
+            constexpr int TOK = SWAP ? BN : BM, PER = TOK < 32 ? 1 : TOK / 32;
+            const int m0 = SWAP ? BN * tc : BM * tr, nb0 = SWAP ? tr : (BN * tc) >> 7;
+            const int nb = nb0 + lane;   // lanes 0, 1: the tile's one or two blocks of 128 features
+            const bool has_b = lane < (SWAP || BN <= 128 ? 1 : 2) && (long long)nb * 128 < N;
+            for (int kb = k_lo; kb < k_hi; ++kb) {
+                if (!(ok = __all_sync(0xffffffffu, wait(sempty + ss, sph)))) break;
+                const uint32_t dst = umma::smem_u32(sm + Sh::OFF_SC) + ss * SC_SLOT * 4;
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    const int j = 32 * i + lane, m = m0 + j;
+                    if (j < TOK) copy4(dst + 4 * j, a_scale + (m < M ? (size_t)m * kbs + kb : 0), m < M);
+                }
+                if (lane < 2) copy4(dst + 512 + 4 * lane, b_scale + (has_b ? (size_t)nb * kbs + kb : 0), has_b);
+                copies_arrive(sfull + ss);
+                if (++ss == NSC) { ss = 0; sph ^= 1; }
+            }
+        }
+        copies_wait();
+    }
+    } else {
+        if constexpr (MOVE_REGS) regs_inc<224>();
         // ----------------------------------------------------------------- epilogue
         // TMEM lane quadrant warp % 4: one row of the tile per lane; with 8 warps the
         // second four take the upper half of the columns
-        const int qd = warp & 3, c0 = Sh::EPI_WARPS == 8 ? EPC * ((warp - 2) >> 2) : 0;
+        const int qd = warp & 3, c0 = Sh::EPI_WARPS == 8 ? EPC * ((warp - 4) >> 2) : 0;
         const uint32_t trow = tbase + ((uint32_t)(32 * qd) << 16) + c0;
         int ts = 0;
         uint32_t tph = 0;
         bool ok = true;
+        float acc[EPC];
+        const float *scales = reinterpret_cast<const float *>(sm + Sh::OFF_SC);
+        int ss = 0;
+        uint32_t sph = 0;
         for (long long t = first; ok && t < n_tiles; t += step) {
             const int tr = (int)(t % tiles_r), tc = (int)(t / tiles_r);
             const int row = BM * tr + 32 * qd + lane, col0 = BN * tc + c0;
-            // scales of this thread: its row's, and its columns' (one block of 128, or
-            // in the swapped order one per column: lane j holds column j's and j + 32's)
-            const float *srow = nullptr, *scol = nullptr, *scol2 = nullptr;
-            if constexpr (!SWAP) {
-                if (row < M) srow = a_scale + (size_t)row * kbs;
-                if (col0 < N) scol = b_scale + (size_t)(col0 >> 7) * kbs;
-            } else {
-                srow = b_scale + (size_t)tr * kbs;
-                if (lane < BN && col0 + lane < M) scol = a_scale + (size_t)(col0 + lane) * kbs;
-                if (BN > 32 && col0 + 32 + lane < M) scol2 = a_scale + (size_t)(col0 + 32 + lane) * kbs;
-            }
-            float acc[EPC];
 #pragma unroll
             for (int j = 0; j < EPC; ++j) acc[j] = 0.f;
-            auto fetch = [&](int kb, float &r, float &c, float &c2) {
-                const bool in = kb < k_hi;
-                r = in && srow ? __ldg(srow + kb) : 0.f;
-                c = in && scol ? __ldg(scol + kb) : 0.f;
-                c2 = in && scol2 ? __ldg(scol2 + kb) : 0.f;
-            };
-            float r, c, c2;
-            fetch(k_lo, r, c, c2);
             for (int kb = k_lo; kb < k_hi; ++kb) {
-                const float s = r * c, s2 = r * c2;
-                ok = __all_sync(0xffffffffu, wait(tfull + ts, tph));
-                if (!ok) break;
+                if (!(ok = __all_sync(0xffffffffu, wait(sfull + ss, sph)))) break;
+                const float *sc = scales + ss * SC_SLOT;
+                // this row's scale times its columns' (one block of 128), or in the swapped
+                // order the rows' one scale, to be multiplied by each column's
+                const float s = SWAP ? sc[128] : sc[32 * qd + lane] * sc[128 + (c0 >> 7)];
+                if (!(ok = __all_sync(0xffffffffu, wait(tfull + ts, tph)))) break;
                 umma::tc_fence_after();
-                fetch(kb + 1, r, c, c2);
                 constexpr int W = EPC < 32 ? EPC : 32;
 #pragma unroll
                 for (int j0 = 0; j0 < EPC; j0 += W) {
@@ -258,15 +320,26 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
                     else umma::tmem_ld16_nowait(trow + ts * BN + j0, v);
                     umma::tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < W; ++j) {
-                        const float f = SWAP ? __shfl_sync(0xffffffffu, j0 ? s2 : s, j) : s;
-                        acc[j0 + j] = fmaf(__uint_as_float(v[j]), f, acc[j0 + j]);
+                    for (int j = 0; j < W; j += 4) {
+                        float4 f = make_float4(s, s, s, s);
+                        if constexpr (SWAP) {
+                            f = *reinterpret_cast<const float4 *>(sc + j0 + j);
+                            f.x *= s; f.y *= s; f.z *= s; f.w *= s;
+                        }
+                        acc[j0 + j] = fmaf(__uint_as_float(v[j]), f.x, acc[j0 + j]);
+                        acc[j0 + j + 1] = fmaf(__uint_as_float(v[j + 1]), f.y, acc[j0 + j + 1]);
+                        acc[j0 + j + 2] = fmaf(__uint_as_float(v[j + 2]), f.z, acc[j0 + j + 2]);
+                        acc[j0 + j + 3] = fmaf(__uint_as_float(v[j + 3]), f.w, acc[j0 + j + 3]);
                     }
                 }
                 umma::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) arrive(tempty + ts);
+                if (lane == 0) {
+                    arrive(tempty + ts);
+                    arrive(sempty + ss);
+                }
                 if (++ts == NT) { ts = 0; tph ^= 1; }
+                if (++ss == NSC) { ss = 0; sph ^= 1; }
             }
             if (!ok) break;
             if (split > 1) {
@@ -287,18 +360,39 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
                     for (int j = 0; j < EPC; ++j)
                         if (col0 + j < M) C[(col0 + j) * ldc + row] = from_f32<Tout>(acc[j]);
                 }
+            } else if (tma_out) {
+                // rows of this warp through shared memory (128-byte rows, swizzled), then one
+                // bulk store per 128 bytes of columns; rows and columns outside C are not written
+                constexpr int SC = 128 / (int)sizeof(Tout);        // columns of a 128-byte row
+                constexpr int GROUPS = Sh::OUT_WARP / 4096;        // of them in the buffer
+                uint8_t *buf = sm + Sh::OFF_OUT + (warp - 4) * Sh::OUT_WARP;
+#pragma unroll
+                for (int j0 = 0; j0 < EPC; j0 += SC * GROUPS) {
+                    if (lane == 0) umma::bulk_wait_read<0>();      // the last store has read the buffer
+                    __syncwarp();
+#pragma unroll
+                    for (int gq = 0; gq < GROUPS && j0 + gq * SC < EPC; ++gq)
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            store_chunk<Tout>(buf + gq * 4096 + umma::sw128_offset(lane, k), acc + j0 + gq * SC + k * (SC / 8));
+                    umma::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+#pragma unroll
+                        for (int gq = 0; gq < GROUPS && j0 + gq * SC < EPC; ++gq)
+                            if (col0 + j0 + gq * SC < N && BM * tr + 32 * qd < M)
+                                umma::tma_store_3d(&maps.c, col0 + j0 + gq * SC, 0, BM * tr + 32 * qd, buf + gq * 4096);
+                        umma::bulk_commit();
+                    }
+                }
             } else if (row < M) {
                 Tout *crow = C + row * ldc + col0;
-                if ((reinterpret_cast<uintptr_t>(crow) & 15) == 0 && col0 + EPC <= N) {
 #pragma unroll
-                    for (int j = 0; j < EPC; j += 8) store8v(crow + j, acc + j);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < EPC; ++j)
-                        if (col0 + j < N) crow[j] = from_f32<Tout>(acc[j]);
-                }
+                for (int j = 0; j < EPC; ++j)
+                    if (col0 + j < N) crow[j] = from_f32<Tout>(acc[j]);
             }
         }
+        if (tma_out && lane == 0) umma::bulk_wait_all();
     }
     umma::tc_fence_before();
     __syncwarp();
@@ -343,6 +437,10 @@ cudaError_t launch_shape(int M, int N, int K, const void *A, long long lda, cons
     e = make_tma_mat_u8(reinterpret_cast<TmaMap *>(&m.b), Sh::SWAP ? A : B, K, Sh::SWAP ? M : N, Sh::SWAP ? lda : ldb,
                         Sh::BN);
     if (e != cudaSuccess) return e;
+    const bool tma_out = !Sh::SWAP && (reinterpret_cast<uintptr_t>(C) & 15) == 0 && ldc * sizeof(Tout) % 16 == 0;
+    if (tma_out && (e = make_tma_mat_out(reinterpret_cast<TmaMap *>(&m.c), C, sizeof(Tout) == 2, N, M, ldc)) !=
+                       cudaSuccess)
+        return e;
     auto *kernel = gemm_fp8_kernel<Sh, Tout>;
     if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM)) != cudaSuccess)
         return e;
@@ -362,7 +460,7 @@ cudaError_t launch_shape(int M, int N, int K, const void *A, long long lda, cons
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if ((e = cudaLaunchKernelEx(&cfg, kernel, m, M, N, K, a_scale, b_scale, static_cast<Tout *>(C), ldc, split)) !=
+    if ((e = cudaLaunchKernelEx(&cfg, kernel, m, M, N, K, a_scale, b_scale, static_cast<Tout *>(C), ldc, split, (int)tma_out)) !=
         cudaSuccess)
         return e;
     return launched();

@@ -126,4 +126,23 @@ cudaError_t make_tma_mat_u8(TmaMap *out, const void *base, int inner, int rows, 
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// A row-major result [rows][inner] of bf16 or fp32 (leading dimension ld elements, rows
+// 16-byte aligned) as a 3-D map {inner, 1, rows}, boxes of 128 bytes x 32 rows, 128-byte
+// swizzle.
+cudaError_t make_tma_mat_out(TmaMap *out, const void *base, bool bf16, int inner, int rows, long long ld) {
+    EncodeTiledFn fn;
+    cudaError_t e = encoder(&fn);
+    if (e != cudaSuccess) return e;
+    const int esz = bf16 ? 2 : 4;
+    const cuuint64_t dims[3] = {(cuuint64_t)inner, 1, (cuuint64_t)rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld * esz, (cuuint64_t)ld * esz};
+    const cuuint32_t box[3] = {(cuuint32_t)(128 / esz), 1, 32};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(reinterpret_cast<CUtensorMap *>(out->bytes),
+                    bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
+                    const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 }  // namespace gdn
