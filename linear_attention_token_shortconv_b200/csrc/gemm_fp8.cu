@@ -12,8 +12,8 @@
 // read it, multiply by the block's scale and add it into fp32 registers while the
 // next block's MMAs fill another buffer.
 //
-// Roles: warp 0 loads by TMA, warp 1 issues the MMAs (and owns the
-// TMEM), warp 2 fetches the scales, warps 4 and up are the epilogue.  Every wait is bounded; one that expires raises
+// Roles: warp 0 loads by TMA, warps 1 and 3 issue the MMAs (1 owns the TMEM), warp 2
+// fetches the scales, warps 4 and up are the epilogue.  Every wait is bounded; one that expires raises
 // the error word and an abort flag that the other roles check.
 //
 // Two operand orders.  Many tokens: tokens are the MMA's 128 rows and features its BN
@@ -52,7 +52,7 @@ template <int BN_, bool SWAP_> struct Shape {
     static constexpr int NT = 512 / BN < 4 ? 512 / BN : 4;            // TMEM buffers
     static constexpr uint32_t TMEM_COLS = NT * BN;                      // 64 .. 512, a power of two
     static constexpr int EPC = EPI_WARPS == 8 ? BN / 2 : BN;            // columns of an epilogue thread
-    static constexpr int THREADS = 128 + 32 * EPI_WARPS;                // warp 3 idle: registers are split by groups of 4
+    static constexpr int THREADS = 128 + 32 * EPI_WARPS;                
     static constexpr int OFF_OUT = NS * ST;
     static constexpr int OFF_SC = OFF_OUT + OUT;
     static constexpr int OFF_BAR = OFF_SC + NSC * SC_SLOT * 4;
@@ -133,6 +133,17 @@ template <> __device__ __forceinline__ void store_chunk<float>(uint8_t *p, const
     *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
 }
 
+// The tiles of a CTA: i, its row of tiles r (fastest) and column c.
+struct Tile {
+    int i, r, c;
+    __device__ __forceinline__ Tile(int first, int rows) : i(first), r(first % rows), c(first / rows) {}
+    __device__ __forceinline__ void next(int step, int rows) {
+        i += step;
+        r += step;
+        while (r >= rows) { r -= rows; ++c; }
+    }
+};
+
 }  // namespace
 
 template <class Sh, typename Tout>
@@ -147,16 +158,16 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + Sh::OFF_BAR), *empty = full + NS;
     uint64_t *tfull = empty + NS, *tempty = tfull + NT, *sfull = tempty + NT, *sempty = sfull + NSC;
     uint64_t *mma_done = sempty + NSC;
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(mma_done + 1);
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(mma_done + 2);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tslot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rows = SWAP ? N : M, cols = SWAP ? M : N;              // of the MMA's operands
     const int tiles_r = (rows + BM - 1) / BM, tiles_c = (cols + BN - 1) / BN;
     const int kbs = (K + BK - 1) / BK;
-    const long long n_tiles = (long long)tiles_r * tiles_c;
+    const int n_tiles = tiles_r * tiles_c;
     // split > 1: one tile per cluster, rank `part` takes K blocks [k_lo, k_hi)
     const int part = split > 1 ? (int)(blockIdx.x % split) : 0;
-    const long long first = blockIdx.x / split, step = gridDim.x / split;
+    const int first = blockIdx.x / split, step = gridDim.x / split;
     const int k_lo = (int)((long long)kbs * part / split), k_hi = (int)((long long)kbs * (part + 1) / split);
 
     if (tid == 0) {
@@ -173,6 +184,7 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
             umma::mbar_init(sempty + i, Sh::EPI_WARPS);
         }
         umma::mbar_init(mma_done, 1);
+        umma::mbar_init(mma_done + 1, 1);
         *abort_flag = 0;
         umma::fence_mbar_init();
     }
@@ -203,8 +215,8 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
         int st = 0, issued = 0;
         uint32_t ph = 1;
         bool ok = true;
-        for (long long t = first; ok && t < n_tiles; t += step) {
-            const int tr = (int)(t % tiles_r), tc = (int)(t / tiles_r);
+        for (Tile t(first, tiles_r); ok && t.i < n_tiles; t.next(step, tiles_r)) {
+            const int tr = t.r, tc = t.c;
             for (int kb = k_lo; kb < k_hi; ++kb) {
                 if (!(ok = __all_sync(0xffffffffu, wait(empty + st, ph)))) break;
                 if (elect_one()) {
@@ -224,15 +236,19 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
                 if (--st < 0) { st = NS - 1; ph ^= 1; }
                 umma::mbar_wait_bounded(full + st, ph ^ 1, MAX_POLLS);
             }
-    } else if (warp == 1) {
-        // --------------------------------------------------------------- MMA issuer
+    } else if (warp == 1 || warp == 3) {
+        // -------------------------------------------------------------- MMA issuers
+        // Two warps take the K blocks in turn: one waits for its operands and its buffer
+        // while the other's MMAs are issued.  Every K block has a product of its own, so
+        // their order does not matter.
         constexpr uint32_t idesc = umma::idesc_f16(BM, BN, false, false);   // format 0 is e4m3 in this kind
         const uint64_t d0 = umma::sw128_desc(umma::smem_u32(sm), 16, 1024);
-        int st = 0, ts = 0;
+        int skip = warp == 3, st = skip, ts = skip;
         uint32_t ph = 0, tph = 1;
         bool ok = true, any = false;
-        for (long long t = first; ok && t < n_tiles; t += step) {
-            for (int kb = k_lo; kb < k_hi; ++kb) {
+        for (int t = first; ok && t < n_tiles; t += step) {
+            int kb = k_lo + skip;
+            for (; kb < k_hi; kb += 2) {
                 ok = wait(tempty + ts, tph) && wait(full + st, ph);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 umma::tc_fence_after();
@@ -246,15 +262,16 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
                 }
                 __syncwarp();
                 any = true;
-                if (++st == NS) { st = 0; ph ^= 1; }
-                if (++ts == NT) { ts = 0; tph ^= 1; }
+                if ((st += 2) >= NS) { st -= NS; ph ^= 1; }
+                if ((ts += 2) >= NT) { ts -= NT; tph ^= 1; }
             }
+            skip = kb - k_hi;   // an odd number of K blocks: the other warp begins the next tile
         }
         // after an abort the epilogue may not have waited for the last MMAs: they
         // complete before the tensor memory is released
         if (any && *abort_flag && elect_one()) {
-            umma::mma_commit(mma_done);
-            umma::mbar_wait_bounded(mma_done, 0, MAX_POLLS);
+            umma::mma_commit(mma_done + (warp == 3));
+            umma::mbar_wait_bounded(mma_done + (warp == 3), 0, MAX_POLLS);
         }
     } else if (warp == 2) {
         // ------------------------------------------------------------------- scales
@@ -263,8 +280,8 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
         int ss = 0;
         uint32_t sph = 1;
         bool ok = true;
-        for (long long t = first; ok && t < n_tiles; t += step) {
-            const int tr = (int)(t % tiles_r), tc = (int)(t / tiles_r);
+        for (Tile t(first, tiles_r); ok && t.i < n_tiles; t.next(step, tiles_r)) {
+            const int tr = t.r, tc = t.c;
             // tokens of the tile (rows, or columns in the swapped order) and blocks of features
             constexpr int TOK = SWAP ? BN : BM, PER = TOK < 32 ? 1 : TOK / 32;
             const int m0 = SWAP ? BN * tc : BM * tr, nb0 = SWAP ? tr : (BN * tc) >> 7;
@@ -299,8 +316,8 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
         const float *scales = reinterpret_cast<const float *>(sm + Sh::OFF_SC);
         int ss = 0;
         uint32_t sph = 0;
-        for (long long t = first; ok && t < n_tiles; t += step) {
-            const int tr = (int)(t % tiles_r), tc = (int)(t / tiles_r);
+        for (Tile t(first, tiles_r); ok && t.i < n_tiles; t.next(step, tiles_r)) {
+            const int tr = t.r, tc = t.c;
             const int row = BM * tr + 32 * qd + lane, col0 = BN * tc + c0;
 #pragma unroll
             for (int j = 0; j < EPC; ++j) acc[j] = 0.f;
@@ -398,7 +415,7 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
     __syncwarp();
     if (split > 1) {
         cluster_sync();
-        const int tr = (int)(first % tiles_r), tc = (int)(first / tiles_r);
+        const int tr = first % tiles_r, tc = first / tiles_r;
         const uint32_t base = umma::smem_u32(sm);
         // elements of the tile in the order of C's rows; rank `part` adds its share
         constexpr int INNER = SWAP ? BM : BN, OUTER = SWAP ? BN : BM;
@@ -447,7 +464,7 @@ cudaError_t launch_shape(int M, int N, int K, const void *A, long long lda, cons
     const long long rows = Sh::SWAP ? N : M, cols = Sh::SWAP ? M : N;
     const long long tiles = ((rows + fp8::BM - 1) / fp8::BM) * ((cols + Sh::BN - 1) / Sh::BN);
     const long long grid = split > 1 ? tiles * split : tiles < sms ? tiles : sms;
-    if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+    if (tiles * split > 0x7fffffff) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(Sh::THREADS);
