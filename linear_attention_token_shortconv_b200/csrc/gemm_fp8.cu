@@ -26,6 +26,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include <atomic>
 #include <cstring>
 
 #include "gdn_device.cuh"
@@ -41,10 +42,13 @@ constexpr int BM = 128, BK = 128;
 constexpr uint32_t MAX_POLLS = 1u << 24;
 constexpr int NSC = 8, SC_SLOT = 132;   // ring of scales: 128 of A's rows, two of B's blocks
 
-template <int BN_, bool SWAP_> struct Shape {
+template <int BN_, bool SWAP_, bool PAIR_ = false> struct Shape {
     static constexpr int BN = BN_;
     static constexpr bool SWAP = SWAP_;
-    static constexpr int A_ST = BM * BK, B_ST = BN * BK, ST = A_ST + B_ST;
+    static constexpr bool PAIR = PAIR_;                                 // two CTAs on one tile of 256 rows
+    static constexpr int ROWS = PAIR ? 2 * BM : BM;                     // of a tile
+    static constexpr int B_ROWS = PAIR ? BN / 2 : BN;                   // rows of B that one CTA loads
+    static constexpr int A_ST = BM * BK, B_ST = B_ROWS * BK, ST = A_ST + B_ST;
     static constexpr int EPI_WARPS = BN >= 128 ? 8 : 4;
     static constexpr int OUT_WARP = SWAP ? 0 : 32 * (EPI_WARPS == 8 ? BN / 2 : BN) * 2;   // result rows of a warp, bf16
     static constexpr int OUT = OUT_WARP * EPI_WARPS;
@@ -52,31 +56,88 @@ template <int BN_, bool SWAP_> struct Shape {
     static constexpr int NT = 512 / BN < 4 ? 512 / BN : 4;            // TMEM buffers
     static constexpr uint32_t TMEM_COLS = NT * BN;                      // 64 .. 512, a power of two
     static constexpr int EPC = EPI_WARPS == 8 ? BN / 2 : BN;            // columns of an epilogue thread
-    static constexpr int THREADS = 128 + 32 * EPI_WARPS;                
+    static constexpr int THREADS = 128 + 32 * EPI_WARPS;
     static constexpr int OFF_OUT = NS * ST;
     static constexpr int OFF_SC = OFF_OUT + OUT;
     static constexpr int OFF_BAR = OFF_SC + NSC * SC_SLOT * 4;
     static constexpr int SMEM = OFF_BAR + 384 + 1024;                   // barriers; alignment slack
     static constexpr int PART_LD = SWAP ? BM : BN + 4;                  // split: row length of the fp32 part
-    static_assert((SWAP ? BN * BM : BM * (BN + 4)) * 4 <= OFF_OUT, "the split's part fits in the stages");
+    static_assert(PAIR || (SWAP ? BN * BM : BM * (BN + 4)) * 4 <= OFF_OUT, "the split's part fits in the stages");
     static_assert(SMEM <= 232448, "227 KB per block");
 };
 }  // namespace fp8
 
 struct Fp8Maps {
-    CUtensorMap a, b;   // MMA rows (box 128 x 128 bytes) and columns (box 128 bytes x BN)
+    CUtensorMap a, b;   // MMA rows (box 128 x 128 bytes) and columns (box 128 bytes x B_ROWS)
     CUtensorMap c;      // the result, boxes of 128 bytes x 32 rows (where its rows are 16-byte aligned)
 };
 
 namespace {
 
 // kind::f8f6f4, e4m3 operands (format 0), fp32 result; both operands K-major.
+// With PAIR the MMA's rows and its B operand are spread over two CTAs at the same
+// shared-memory offsets.
+template <bool PAIR>
 __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                          uint32_t accumulate) {
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+            " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+            " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+            : "memory");
+}
+
+// An arrival on `bar` (of both CTAs of a pair) when this thread's MMAs so far are done.
+template <bool PAIR> __device__ __forceinline__ void commit(uint64_t *bar) {
+    if constexpr (PAIR)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                umma::smem_u32(bar)),
+            "h"((uint16_t)3)
+            : "memory");
+    else
+        umma::mma_commit(bar);
+}
+
+template <bool PAIR> __device__ __forceinline__ void tmem_alloc(uint32_t *dst, uint32_t cols) {
+    if constexpr (PAIR) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(umma::smem_u32(dst)),
+                     "r"(cols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+        umma::tmem_alloc(dst, cols);
+    }
+}
+template <bool PAIR> __device__ __forceinline__ void tmem_dealloc(uint32_t addr, uint32_t cols) {
+    if constexpr (PAIR)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+    else
+        umma::tmem_dealloc(addr, cols);
+}
+
+// Address of the cluster's CTA `rank`'s copy of a shared variable.
+__device__ __forceinline__ uint32_t at_rank(const void *p, int rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(umma::smem_u32(p)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// A tile into this CTA's shared memory whose bytes are counted on the barrier at cluster
+// address `bar`, which may be the other CTA's of the pair.
+__device__ __forceinline__ void tma_load_pair(void *dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(umma::smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
 
@@ -152,7 +213,7 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
                 const float *__restrict__ b_scale, Tout *__restrict__ C, long long ldc, int split, int tma_out) {
     using namespace fp8;
     constexpr int BN = Sh::BN, NS = Sh::NS, NT = Sh::NT, EPC = Sh::EPC;
-    constexpr bool SWAP = Sh::SWAP;
+    constexpr bool SWAP = Sh::SWAP, PAIR = Sh::PAIR;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = umma::align_smem<1024>(smem_raw);
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + Sh::OFF_BAR), *empty = full + NS;
@@ -162,12 +223,14 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tslot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rows = SWAP ? N : M, cols = SWAP ? M : N;              // of the MMA's operands
-    const int tiles_r = (rows + BM - 1) / BM, tiles_c = (cols + BN - 1) / BN;
+    const int tiles_r = (rows + Sh::ROWS - 1) / Sh::ROWS, tiles_c = (cols + BN - 1) / BN;
     const int kbs = (K + BK - 1) / BK;
     const int n_tiles = tiles_r * tiles_c;
     // split > 1: one tile per cluster, rank `part` takes K blocks [k_lo, k_hi)
     const int part = split > 1 ? (int)(blockIdx.x % split) : 0;
-    const int first = blockIdx.x / split, step = gridDim.x / split;
+    const int rank = PAIR ? (int)(blockIdx.x & 1) : 0;   // of the pair; 0 leads
+    const int per_tile = PAIR ? 2 : split;
+    const int first = blockIdx.x / per_tile, step = gridDim.x / per_tile;
     const int k_lo = (int)((long long)kbs * part / split), k_hi = (int)((long long)kbs * (part + 1) / split);
 
     if (tid == 0) {
@@ -177,7 +240,7 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
         }
         for (int i = 0; i < NT; ++i) {
             umma::mbar_init(tfull + i, 1);
-            umma::mbar_init(tempty + i, Sh::EPI_WARPS);
+            umma::mbar_init(tempty + i, (PAIR ? 2 : 1) * Sh::EPI_WARPS);
         }
         for (int i = 0; i < NSC; ++i) {
             umma::mbar_init(sfull + i, 32);
@@ -188,9 +251,10 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
         *abort_flag = 0;
         umma::fence_mbar_init();
     }
-    if (warp == 1) umma::tmem_alloc(tslot, Sh::TMEM_COLS);
+    if (warp == 1) tmem_alloc<PAIR>(tslot, Sh::TMEM_COLS);
     umma::tc_fence_before();
     __syncthreads();
+    if constexpr (PAIR) cluster_sync();   // the other CTA's barriers are ready
     umma::tc_fence_after();
     const uint32_t tbase = *tslot;
 
@@ -221,9 +285,17 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
                 if (!(ok = __all_sync(0xffffffffu, wait(empty + st, ph)))) break;
                 if (elect_one()) {
                     uint8_t *buf = sm + st * Sh::ST;
-                    umma::mbar_expect_tx(full + st, Sh::ST);
-                    umma::tma_load_3d(buf, &maps.a, BK * kb, 0, BM * tr, full + st);
-                    umma::tma_load_3d(buf + Sh::A_ST, &maps.b, BK * kb, 0, BN * tc, full + st);
+                    if constexpr (PAIR) {
+                        // both halves are counted on the leader's barrier
+                        const uint32_t bar = at_rank(full + st, 0);
+                        if (rank == 0) umma::mbar_expect_tx(full + st, 2 * Sh::ST);
+                        tma_load_pair(buf, &maps.a, BK * kb, 0, Sh::ROWS * tr + BM * rank, bar);
+                        tma_load_pair(buf + Sh::A_ST, &maps.b, BK * kb, 0, BN * tc + Sh::B_ROWS * rank, bar);
+                    } else {
+                        umma::mbar_expect_tx(full + st, Sh::ST);
+                        umma::tma_load_3d(buf, &maps.a, BK * kb, 0, BM * tr, full + st);
+                        umma::tma_load_3d(buf + Sh::A_ST, &maps.b, BK * kb, 0, BN * tc, full + st);
+                    }
                 }
                 __syncwarp();
                 if (issued < NS) ++issued;
@@ -231,17 +303,17 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
             }
         }
         // after an abort, loads still in flight land before the CTA leaves
-        if (*abort_flag)
+        if (*abort_flag && rank == 0)
             for (int i = 0; i < issued; ++i) {
                 if (--st < 0) { st = NS - 1; ph ^= 1; }
                 umma::mbar_wait_bounded(full + st, ph ^ 1, MAX_POLLS);
             }
-    } else if (warp == 1 || warp == 3) {
+    } else if ((warp == 1 || warp == 3) && rank == 0) {
         // -------------------------------------------------------------- MMA issuers
         // Two warps take the K blocks in turn: one waits for its operands and its buffer
         // while the other's MMAs are issued.  Every K block has a product of its own, so
         // their order does not matter.
-        constexpr uint32_t idesc = umma::idesc_f16(BM, BN, false, false);   // format 0 is e4m3 in this kind
+        constexpr uint32_t idesc = umma::idesc_f16(Sh::ROWS, BN, false, false);   // format 0 is e4m3 in this kind
         const uint64_t d0 = umma::sw128_desc(umma::smem_u32(sm), 16, 1024);
         int skip = warp == 3, st = skip, ts = skip;
         uint32_t ph = 0, tph = 1;
@@ -256,9 +328,9 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
                     const uint64_t ad = d0 + (uint32_t)st * (Sh::ST >> 4), bd = ad + (Sh::A_ST >> 4);
 #pragma unroll
                     for (int ks = 0; ks < BK / 32; ++ks)   // 32 bytes of K: start address + 2 (units of 16)
-                        mma_e4m3(tbase + ts * BN, ad + 2 * ks, bd + 2 * ks, idesc, ks > 0);
-                    umma::mma_commit(empty + st);
-                    umma::mma_commit(tfull + ts);
+                        mma_e4m3<PAIR>(tbase + ts * BN, ad + 2 * ks, bd + 2 * ks, idesc, ks > 0);
+                    commit<PAIR>(empty + st);
+                    commit<PAIR>(tfull + ts);
                 }
                 __syncwarp();
                 any = true;
@@ -270,7 +342,7 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
         // after an abort the epilogue may not have waited for the last MMAs: they
         // complete before the tensor memory is released
         if (any && *abort_flag && elect_one()) {
-            umma::mma_commit(mma_done + (warp == 3));
+            commit<PAIR>(mma_done + (warp == 3));
             umma::mbar_wait_bounded(mma_done + (warp == 3), 0, MAX_POLLS);
         }
     } else if (warp == 2) {
@@ -284,7 +356,7 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
             const int tr = t.r, tc = t.c;
             // tokens of the tile (rows, or columns in the swapped order) and blocks of features
             constexpr int TOK = SWAP ? BN : BM, PER = TOK < 32 ? 1 : TOK / 32;
-            const int m0 = SWAP ? BN * tc : BM * tr, nb0 = SWAP ? tr : (BN * tc) >> 7;
+            const int m0 = SWAP ? BN * tc : Sh::ROWS * tr + BM * rank, nb0 = SWAP ? tr : (BN * tc) >> 7;
             const int nb = nb0 + lane;   // lanes 0, 1: the tile's one or two blocks of 128 features
             const bool has_b = lane < (SWAP || BN <= 128 ? 1 : 2) && (long long)nb * 128 < N;
             for (int kb = k_lo; kb < k_hi; ++kb) {
@@ -318,7 +390,7 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
         uint32_t sph = 0;
         for (Tile t(first, tiles_r); ok && t.i < n_tiles; t.next(step, tiles_r)) {
             const int tr = t.r, tc = t.c;
-            const int row = BM * tr + 32 * qd + lane, col0 = BN * tc + c0;
+            const int row0 = Sh::ROWS * tr + BM * rank + 32 * qd, row = row0 + lane, col0 = BN * tc + c0;
 #pragma unroll
             for (int j = 0; j < EPC; ++j) acc[j] = 0.f;
             for (int kb = k_lo; kb < k_hi; ++kb) {
@@ -352,7 +424,8 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
                 umma::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    arrive(tempty + ts);
+                    if constexpr (PAIR) arrive_at(at_rank(tempty + ts, 0));
+                    else arrive(tempty + ts);
                     arrive(sempty + ss);
                 }
                 if (++ts == NT) { ts = 0; tph ^= 1; }
@@ -397,8 +470,8 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
                     if (lane == 0) {
 #pragma unroll
                         for (int gq = 0; gq < GROUPS && j0 + gq * SC < EPC; ++gq)
-                            if (col0 + j0 + gq * SC < N && BM * tr + 32 * qd < M)
-                                umma::tma_store_3d(&maps.c, col0 + j0 + gq * SC, 0, BM * tr + 32 * qd, buf + gq * 4096);
+                            if (col0 + j0 + gq * SC < N && row0 < M)
+                                umma::tma_store_3d(&maps.c, col0 + j0 + gq * SC, 0, row0, buf + gq * 4096);
                         umma::bulk_commit();
                     }
                 }
@@ -433,13 +506,35 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
         }
         __syncwarp();
         cluster_sync();   // no CTA leaves while another still reads its part
+    } else if constexpr (PAIR) {
+        cluster_sync();   // the leader's MMAs read both CTAs' memory
     } else {
         __syncthreads();
     }
-    if (warp == 1) umma::tmem_dealloc(tbase, Sh::TMEM_COLS);
+    if (warp == 1) tmem_dealloc<PAIR>(tbase, Sh::TMEM_COLS);
 }
 
 namespace {
+
+// Clusters of two CTAs of this kernel that the current device runs at once (asked once
+// per device and kernel).
+template <typename Kernel>
+cudaError_t resident_pairs(Kernel *kernel, cudaLaunchConfig_t cfg, int sms, int *pairs) {
+    static std::atomic<int> cache[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!cache[dev]) {
+        int n = 0;
+        cfg.gridDim = dim3(2 * (sms / 2));
+        if ((e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg)) != cudaSuccess) return e;
+        if (n < 1) return cudaErrorInvalidConfiguration;
+        cache[dev] = n;
+    }
+    *pairs = cache[dev];
+    return cudaSuccess;
+}
 
 template <class Sh, typename Tout>
 cudaError_t launch_shape(int M, int N, int K, const void *A, long long lda, const float *a_scale, const void *B,
@@ -452,7 +547,7 @@ cudaError_t launch_shape(int M, int N, int K, const void *A, long long lda, cons
                         fp8::BM);
     if (e != cudaSuccess) return e;
     e = make_tma_mat_u8(reinterpret_cast<TmaMap *>(&m.b), Sh::SWAP ? A : B, K, Sh::SWAP ? M : N, Sh::SWAP ? lda : ldb,
-                        Sh::BN);
+                        Sh::B_ROWS);
     if (e != cudaSuccess) return e;
     const bool tma_out = !Sh::SWAP && (reinterpret_cast<uintptr_t>(C) & 15) == 0 && ldc * sizeof(Tout) % 16 == 0;
     if (tma_out && (e = make_tma_mat_out(reinterpret_cast<TmaMap *>(&m.c), C, sizeof(Tout) == 2, N, M, ldc)) !=
@@ -462,21 +557,27 @@ cudaError_t launch_shape(int M, int N, int K, const void *A, long long lda, cons
     if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM)) != cudaSuccess)
         return e;
     const long long rows = Sh::SWAP ? N : M, cols = Sh::SWAP ? M : N;
-    const long long tiles = ((rows + fp8::BM - 1) / fp8::BM) * ((cols + Sh::BN - 1) / Sh::BN);
-    const long long grid = split > 1 ? tiles * split : tiles < sms ? tiles : sms;
+    const long long tiles = ((rows + Sh::ROWS - 1) / Sh::ROWS) * ((cols + Sh::BN - 1) / Sh::BN);
+    const int cluster = Sh::PAIR ? 2 : split;
     if (tiles * split > 0x7fffffff) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
+    cfg.gridDim = dim3((unsigned)(split > 1 ? tiles * split : tiles < sms ? tiles : sms));
     cfg.blockDim = dim3(Sh::THREADS);
     cfg.dynamicSmemBytes = Sh::SMEM;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)split;
+    attr[0].val.clusterDim.x = (unsigned)cluster;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    if constexpr (Sh::PAIR) {
+        // as many pairs as run at once: not every SM has a partner
+        int pairs = 0;
+        if ((e = resident_pairs(kernel, cfg, sms, &pairs)) != cudaSuccess) return e;
+        cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
+    }
     if ((e = cudaLaunchKernelEx(&cfg, kernel, m, M, N, K, a_scale, b_scale, static_cast<Tout *>(C), ldc, split, (int)tma_out)) !=
         cudaSuccess)
         return e;
@@ -505,7 +606,9 @@ cudaError_t launch_typed(int M, int N, int K, const void *A, long long lda, cons
         if (M <= 32) return GDN_FP8(32, true, s);
         return GDN_FP8(64, true, s);
     }
-    if (tiles(M, N, 256) >= sms) return GDN_FP8(256, false, 1);
+    if (tiles(M, N, 256) >= sms)
+        return launch_shape<fp8::Shape<256, false, true>, Tout>(M, N, K, A, lda, a_scale, B, ldb, b_scale, C, ldc, 1,
+                                                                sms, stream);
     if (tiles(M, N, 128) >= sms) return GDN_FP8(128, false, 1);
     return GDN_FP8(64, false, split_for(tiles(M, N, 64)));
 #undef GDN_FP8
