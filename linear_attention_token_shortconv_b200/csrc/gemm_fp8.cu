@@ -40,7 +40,9 @@ __device__ unsigned int g_fp8_err;
 namespace fp8 {
 constexpr int BM = 128, BK = 128;
 constexpr uint32_t MAX_POLLS = 1u << 24;
-constexpr int NSC = 8, SC_SLOT = 132;   // ring of scales: 128 of A's rows, two of B's blocks
+// ring of scales: SG K blocks of the 128 rows (or columns) of tokens and of two blocks of
+// features, a token's SG scales side by side
+constexpr int NSC = 3, SG = 4, SC_SLOT = 130 * SG;
 
 template <int BN_, bool SWAP_, bool PAIR_ = false> struct Shape {
     static constexpr int BN = BN_;
@@ -49,13 +51,16 @@ template <int BN_, bool SWAP_, bool PAIR_ = false> struct Shape {
     static constexpr int ROWS = PAIR ? 2 * BM : BM;                     // of a tile
     static constexpr int B_ROWS = PAIR ? BN / 2 : BN;                   // rows of B that one CTA loads
     static constexpr int A_ST = BM * BK, B_ST = B_ROWS * BK, ST = A_ST + B_ST;
-    static constexpr int EPI_WARPS = BN >= 128 ? 8 : 4;
-    static constexpr int OUT_WARP = SWAP ? 0 : 32 * (EPI_WARPS == 8 ? BN / 2 : BN) * 2;   // result rows of a warp, bf16
+    // Epilogue: 64 columns a thread (32 or 16 in the swapped order), 32 rows a warp.  A K
+    // block costs a warp two waits and its TMEM reads in sequence, several hundred clocks
+    // at two warps a scheduler; four of them hide it from one another.
+    static constexpr int EPC = SWAP ? (BN < 32 ? BN : 32) : 64;
+    static constexpr int EPI_WARPS = 4 * BN / EPC;
+    static constexpr int OUT_WARP = SWAP ? 0 : 4096;                    // result rows of a warp, 128 bytes each
     static constexpr int OUT = OUT_WARP * EPI_WARPS;
     static constexpr int NS = (226304 - OUT) / ST < 8 ? (226304 - OUT) / ST : 8;
     static constexpr int NT = 512 / BN < 4 ? 512 / BN : 4;            // TMEM buffers
     static constexpr uint32_t TMEM_COLS = NT * BN;                      // 64 .. 512, a power of two
-    static constexpr int EPC = EPI_WARPS == 8 ? BN / 2 : BN;            // columns of an epilogue thread
     static constexpr int THREADS = 128 + 32 * EPI_WARPS;
     static constexpr int OFF_OUT = NS * ST;
     static constexpr int OFF_SC = OFF_OUT + OUT;
@@ -128,8 +133,9 @@ __device__ __forceinline__ uint32_t at_rank(const void *p, int rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(umma::smem_u32(p)), "r"(rank));
     return a;
 }
-__device__ __forceinline__ void arrive_at(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+template <bool PAIR> __device__ __forceinline__ void arrive_at(uint32_t bar) {
+    if constexpr (PAIR) asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    else asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // A tile into this CTA's shared memory whose bytes are counted on the barrier at cluster
 // address `bar`, which may be the other CTA's of the pair.
@@ -152,8 +158,8 @@ __device__ __forceinline__ void arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(umma::smem_u32(bar)) : "memory");
 }
 
-// Registers move from the loading warps to the epilogue: 4 warps x 56 + 8 x 224 is what
-// 12 warps x 168 were launched with.
+// Registers move from the loading warps to the epilogue: 4 warps x 64 + 16 x 104 is what
+// 20 warps x 96 were launched with.
 template <int R> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R> __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 
@@ -180,18 +186,18 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr, int rank) {
 }
 
 // One 16-byte chunk of a result row.
-template <typename T> __device__ __forceinline__ void store_chunk(uint8_t *p, const float *x);
-template <> __device__ __forceinline__ void store_chunk<__nv_bfloat16>(uint8_t *p, const float *x) {
+template <typename T> __device__ __forceinline__ void store_chunk(uint8_t *p, const float2 *x);
+template <> __device__ __forceinline__ void store_chunk<__nv_bfloat16>(uint8_t *p, const float2 *x) {
     uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
+        const __nv_bfloat162 b = __floats2bfloat162_rn(x[e].x, x[e].y);
         memcpy(w + e, &b, 4);
     }
     *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
-template <> __device__ __forceinline__ void store_chunk<float>(uint8_t *p, const float *x) {
-    *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+template <> __device__ __forceinline__ void store_chunk<float>(uint8_t *p, const float2 *x) {
+    *reinterpret_cast<float4 *>(p) = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
 }
 
 // The tiles of a CTA: i, its row of tiles r (fastest) and column c.
@@ -258,8 +264,12 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
     umma::tc_fence_after();
     const uint32_t tbase = *tslot;
 
+    // A wait that expires raises the abort flag, and every later one gives up soon after:
+    // the loads stop, the other roles run through their loops on whatever there is, and
+    // nothing is stored.
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-        for (uint32_t i = 0; i < MAX_POLLS; ++i) {
+        if (umma::mbar_try_wait(bar, parity)) return true;
+        for (uint32_t i = 1; i < MAX_POLLS; ++i) {
             if (umma::mbar_try_wait(bar, parity)) return true;
             if ((i & 63u) == 63u && *abort_flag) return false;
         }
@@ -268,9 +278,9 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
         return false;
     };
 
-    constexpr bool MOVE_REGS = Sh::EPI_WARPS == 8;
+    constexpr bool MOVE_REGS = Sh::EPI_WARPS == 16;
     if (warp < 4) {
-    if constexpr (MOVE_REGS) regs_dec<56>();
+    if constexpr (MOVE_REGS) regs_dec<64>();
     // Loading and issuing warps walk their loops with all lanes and elect one for the
     // instruction itself: loops of a lone lane lose the uniform registers that descriptors
     // and barriers are addressed with.
@@ -317,12 +327,13 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
         const uint64_t d0 = umma::sw128_desc(umma::smem_u32(sm), 16, 1024);
         int skip = warp == 3, st = skip, ts = skip;
         uint32_t ph = 0, tph = 1;
-        bool ok = true, any = false;
-        for (int t = first; ok && t < n_tiles; t += step) {
+        bool any = false;
+        for (int t = first; t < n_tiles; t += step) {
             int kb = k_lo + skip;
             for (; kb < k_hi; kb += 2) {
-                ok = wait(tempty + ts, tph) && wait(full + st, ph);
-                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                wait(tempty + ts, tph);
+                wait(full + st, ph);
+                __syncwarp();
                 umma::tc_fence_after();
                 if (elect_one()) {
                     const uint64_t ad = d0 + (uint32_t)st * (Sh::ST >> 4), bd = ad + (Sh::A_ST >> 4);
@@ -351,23 +362,28 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
         // copies into a ring, in flight for many blocks at once.
         int ss = 0;
         uint32_t sph = 1;
-        bool ok = true;
-        for (Tile t(first, tiles_r); ok && t.i < n_tiles; t.next(step, tiles_r)) {
+        for (Tile t(first, tiles_r); t.i < n_tiles; t.next(step, tiles_r)) {
             const int tr = t.r, tc = t.c;
             // tokens of the tile (rows, or columns in the swapped order) and blocks of features
             constexpr int TOK = SWAP ? BN : BM, PER = TOK < 32 ? 1 : TOK / 32;
             const int m0 = SWAP ? BN * tc : Sh::ROWS * tr + BM * rank, nb0 = SWAP ? tr : (BN * tc) >> 7;
             const int nb = nb0 + lane;   // lanes 0, 1: the tile's one or two blocks of 128 features
             const bool has_b = lane < (SWAP || BN <= 128 ? 1 : 2) && (long long)nb * 128 < N;
-            for (int kb = k_lo; kb < k_hi; ++kb) {
-                if (!(ok = __all_sync(0xffffffffu, wait(sempty + ss, sph)))) break;
+            for (int kb = k_lo; kb < k_hi; kb += SG) {
+                wait(sempty + ss, sph);
                 const uint32_t dst = umma::smem_u32(sm + Sh::OFF_SC) + ss * SC_SLOT * 4;
 #pragma unroll
                 for (int i = 0; i < PER; ++i) {
                     const int j = 32 * i + lane, m = m0 + j;
-                    if (j < TOK) copy4(dst + 4 * j, a_scale + (m < M ? (size_t)m * kbs + kb : 0), m < M);
+                    const float *src = a_scale + (m < M ? (size_t)m * kbs + kb : 0);
+#pragma unroll
+                    for (int g = 0; g < SG; ++g)
+                        if (j < TOK) copy4(dst + 4 * (SG * j + g), src + (m < M && kb + g < k_hi ? g : 0), m < M && kb + g < k_hi);
                 }
-                if (lane < 2) copy4(dst + 512 + 4 * lane, b_scale + (has_b ? (size_t)nb * kbs + kb : 0), has_b);
+                const float *src = b_scale + (has_b ? (size_t)nb * kbs + kb : 0);
+#pragma unroll
+                for (int g = 0; g < SG; ++g)
+                    if (lane < 2) copy4(dst + 4 * (SG * (128 + lane) + g), src + (has_b && kb + g < k_hi ? g : 0), has_b && kb + g < k_hi);
                 copies_arrive(sfull + ss);
                 if (++ss == NSC) { ss = 0; sph ^= 1; }
             }
@@ -375,31 +391,40 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
         copies_wait();
     }
     } else {
-        if constexpr (MOVE_REGS) regs_inc<224>();
+        if constexpr (MOVE_REGS) regs_inc<104>();
         // ----------------------------------------------------------------- epilogue
-        // TMEM lane quadrant warp % 4: one row of the tile per lane; with 8 warps the
-        // second four take the upper half of the columns
-        const int qd = warp & 3, c0 = Sh::EPI_WARPS == 8 ? EPC * ((warp - 4) >> 2) : 0;
+        // TMEM lane quadrant warp % 4: one row of the tile per lane; each four warps take
+        // the next EPC columns
+        const int qd = warp & 3, c0 = EPC * ((warp - 4) >> 2);
         const uint32_t trow = tbase + ((uint32_t)(32 * qd) << 16) + c0;
-        int ts = 0;
-        uint32_t tph = 0;
-        bool ok = true;
-        float acc[EPC];
+        int ts = 0, ss = 0;
+        uint32_t tph = 0, sph = 0;
+        const uint32_t tempty0 = PAIR ? at_rank(tempty, 0) : umma::smem_u32(tempty);   // the issuers' copy
+        float2 acc[EPC / 2];
         const float *scales = reinterpret_cast<const float *>(sm + Sh::OFF_SC);
-        int ss = 0;
-        uint32_t sph = 0;
-        for (Tile t(first, tiles_r); ok && t.i < n_tiles; t.next(step, tiles_r)) {
+        for (Tile t(first, tiles_r); t.i < n_tiles; t.next(step, tiles_r)) {
             const int tr = t.r, tc = t.c;
             const int row0 = Sh::ROWS * tr + BM * rank + 32 * qd, row = row0 + lane, col0 = BN * tc + c0;
 #pragma unroll
-            for (int j = 0; j < EPC; ++j) acc[j] = 0.f;
+            for (int j = 0; j < EPC / 2; ++j) acc[j] = make_float2(0.f, 0.f);
+            float4 s4 = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int kb = k_lo; kb < k_hi; ++kb) {
-                if (!(ok = __all_sync(0xffffffffu, wait(sfull + ss, sph)))) break;
+                const int sg = (kb - k_lo) & (SG - 1);
                 const float *sc = scales + ss * SC_SLOT;
-                // this row's scale times its columns' (one block of 128), or in the swapped
-                // order the rows' one scale, to be multiplied by each column's
-                const float s = SWAP ? sc[128] : sc[32 * qd + lane] * sc[128 + (c0 >> 7)];
-                if (!(ok = __all_sync(0xffffffffu, wait(tfull + ts, tph)))) break;
+                if (sg == 0) {
+                    // SG K blocks' scales of this row times its columns' (one block of 128), or
+                    // in the swapped order of the rows, to be multiplied by each column's
+                    wait(sfull + ss, sph);
+                    s4 = *reinterpret_cast<const float4 *>(sc + SG * (SWAP ? 128 : 128 + (c0 >> 7)));
+                    if constexpr (!SWAP) {
+                        const float4 r4 = *reinterpret_cast<const float4 *>(sc + SG * (32 * qd + lane));
+                        s4.x *= r4.x; s4.y *= r4.y; s4.z *= r4.z; s4.w *= r4.w;
+                    }
+                }
+                const float s = s4.x;
+                s4 = make_float4(s4.y, s4.z, s4.w, 0.f);
+                wait(tfull + ts, tph);
+                __syncwarp();
                 umma::tc_fence_after();
                 constexpr int W = EPC < 32 ? EPC : 32;
 #pragma unroll
@@ -408,47 +433,46 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
                     if constexpr (W == 32) umma::tmem_ld32_nowait(trow + ts * BN + j0, v);
                     else umma::tmem_ld16_nowait(trow + ts * BN + j0, v);
                     umma::tmem_ld_wait();
+                    if (j0 + W == EPC) {   // the buffer is read: the next product may take it
+                        umma::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) arrive_at<PAIR>(tempty0 + 8 * ts);
+                    }
 #pragma unroll
-                    for (int j = 0; j < W; j += 4) {
-                        float4 f = make_float4(s, s, s, s);
-                        if constexpr (SWAP) {
-                            f = *reinterpret_cast<const float4 *>(sc + j0 + j);
-                            f.x *= s; f.y *= s; f.z *= s; f.w *= s;
-                        }
-                        acc[j0 + j] = fmaf(__uint_as_float(v[j]), f.x, acc[j0 + j]);
-                        acc[j0 + j + 1] = fmaf(__uint_as_float(v[j + 1]), f.y, acc[j0 + j + 1]);
-                        acc[j0 + j + 2] = fmaf(__uint_as_float(v[j + 2]), f.z, acc[j0 + j + 2]);
-                        acc[j0 + j + 3] = fmaf(__uint_as_float(v[j + 3]), f.w, acc[j0 + j + 3]);
+                    for (int j = 0; j < W; j += 2) {
+                        float2 f = make_float2(s, s);
+                        if constexpr (SWAP)
+                            f = make_float2(sc[SG * (c0 + j0 + j) + sg] * s, sc[SG * (c0 + j0 + j + 1) + sg] * s);
+                        float2 &d = acc[(j0 + j) / 2];
+                        d = ffma2(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), f, d);
                     }
                 }
-                umma::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if constexpr (PAIR) arrive_at(at_rank(tempty + ts, 0));
-                    else arrive(tempty + ts);
-                    arrive(sempty + ss);
-                }
                 if (++ts == NT) { ts = 0; tph ^= 1; }
-                if (++ss == NSC) { ss = 0; sph ^= 1; }
+                if (sg == SG - 1 || kb + 1 == k_hi) {
+                    __syncwarp();
+                    if (lane == 0) arrive(sempty + ss);
+                    if (++ss == NSC) { ss = 0; sph ^= 1; }
+                }
             }
-            if (!ok) break;
+            if (*abort_flag) continue;
+            auto el = [&](int j) { return j & 1 ? acc[j / 2].y : acc[j / 2].x; };
             if (split > 1) {
                 // this rank's part, in the stages (every load and MMA of the tile is done)
                 float *buf = reinterpret_cast<float *>(sm);
                 if constexpr (SWAP) {
 #pragma unroll
-                    for (int j = 0; j < EPC; ++j) buf[j * Sh::PART_LD + 32 * qd + lane] = acc[j];
+                    for (int j = 0; j < EPC; ++j) buf[(c0 + j) * Sh::PART_LD + 32 * qd + lane] = el(j);
                 } else {
                     float *p = buf + (32 * qd + lane) * Sh::PART_LD + c0;
 #pragma unroll
                     for (int j = 0; j < EPC; j += 4)
-                        *reinterpret_cast<float4 *>(p + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+                        *reinterpret_cast<float4 *>(p + j) = make_float4(el(j), el(j + 1), el(j + 2), el(j + 3));
                 }
             } else if constexpr (SWAP) {
                 if (row < N) {
 #pragma unroll
                     for (int j = 0; j < EPC; ++j)
-                        if (col0 + j < M) C[(col0 + j) * ldc + row] = from_f32<Tout>(acc[j]);
+                        if (col0 + j < M) C[(col0 + j) * ldc + row] = from_f32<Tout>(el(j));
                 }
             } else if (tma_out) {
                 // rows of this warp through shared memory (128-byte rows, swizzled), then one
@@ -464,7 +488,7 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
                     for (int gq = 0; gq < GROUPS && j0 + gq * SC < EPC; ++gq)
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
-                            store_chunk<Tout>(buf + gq * 4096 + umma::sw128_offset(lane, k), acc + j0 + gq * SC + k * (SC / 8));
+                            store_chunk<Tout>(buf + gq * 4096 + umma::sw128_offset(lane, k), acc + (j0 + gq * SC + k * (SC / 8)) / 2);
                     umma::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
@@ -479,7 +503,7 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
                 Tout *crow = C + row * ldc + col0;
 #pragma unroll
                 for (int j = 0; j < EPC; ++j)
-                    if (col0 + j < N) crow[j] = from_f32<Tout>(acc[j]);
+                    if (col0 + j < N) crow[j] = from_f32<Tout>(el(j));
             }
         }
         if (tma_out && lane == 0) umma::bulk_wait_all();
