@@ -54,12 +54,17 @@ template <int BN_, bool SWAP_, bool PAIR_ = false> struct Shape {
     // Epilogue: 64 columns a thread (32 or 16 in the swapped order), 32 rows a warp.  A K
     // block costs a warp two waits and its TMEM reads in sequence, several hundred clocks
     // at two warps a scheduler; four of them hide it from one another.
-    static constexpr int EPC = SWAP ? (BN < 32 ? BN : 32) : 64;
+    static constexpr int EPC = SWAP ? (BN < 32 ? BN : 32) : PAIR ? 128 : 64;
     static constexpr int EPI_WARPS = 4 * BN / EPC;
-    static constexpr int OUT_WARP = SWAP ? 0 : 4096;                    // result rows of a warp, 128 bytes each
+    static constexpr int OUT_WARP = SWAP ? 0 : 64 * EPC;                 // result rows of a warp, bf16
     static constexpr int OUT = OUT_WARP * EPI_WARPS;
     static constexpr int NS = (226304 - OUT) / ST < 8 ? (226304 - OUT) / ST : 8;
-    static constexpr int NT = 512 / BN < 4 ? 512 / BN : 4;            // TMEM buffers
+    // A buffer's round trip (MMAs 512 clocks, commit, reads 350, hand-back) is longer than
+    // two K blocks' MMAs, and 512 columns hold two products of 256.  So a pair's K block is
+    // two products of 128 columns, each with two buffers and warps of its own: half the MMA
+    // time in the same round trip.
+    static constexpr int HALVES = PAIR ? 2 : 1, HN = BN / HALVES;
+    static constexpr int NT = 512 / BN < 4 ? 512 / BN : 4;            // TMEM buffers of each half
     static constexpr uint32_t TMEM_COLS = NT * BN;                      // 64 .. 512, a power of two
     static constexpr int THREADS = 128 + 32 * EPI_WARPS;
     static constexpr int OFF_OUT = NS * ST;
@@ -73,7 +78,7 @@ template <int BN_, bool SWAP_, bool PAIR_ = false> struct Shape {
 }  // namespace fp8
 
 struct Fp8Maps {
-    CUtensorMap a, b;   // MMA rows (box 128 x 128 bytes) and columns (box 128 bytes x B_ROWS)
+    CUtensorMap a, b;   // MMA rows (box 128 x 128 bytes) and columns (box 128 bytes x B_ROWS, of a pair half that)
     CUtensorMap c;      // the result, boxes of 128 bytes x 32 rows (where its rows are 16-byte aligned)
 };
 
@@ -158,8 +163,8 @@ __device__ __forceinline__ void arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(umma::smem_u32(bar)) : "memory");
 }
 
-// Registers move from the loading warps to the epilogue: 4 warps x 64 + 16 x 104 is what
-// 20 warps x 96 were launched with.
+// Registers move from the loading warps to the epilogue: 4 warps x 72 + 8 x 216 is what
+// 12 warps x 168 were launched with.
 template <int R> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R> __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 
@@ -223,7 +228,8 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = umma::align_smem<1024>(smem_raw);
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + Sh::OFF_BAR), *empty = full + NS;
-    uint64_t *tfull = empty + NS, *tempty = tfull + NT, *sfull = tempty + NT, *sempty = sfull + NSC;
+    constexpr int HALVES = Sh::HALVES, HN = Sh::HN;
+    uint64_t *tfull = empty + NS, *tempty = tfull + HALVES * NT, *sfull = tempty + HALVES * NT, *sempty = sfull + NSC;
     uint64_t *mma_done = sempty + NSC;
     uint32_t *tslot = reinterpret_cast<uint32_t *>(mma_done + 2);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tslot + 1);
@@ -242,11 +248,11 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
             umma::mbar_init(full + i, 1);
-            umma::mbar_init(empty + i, 1);
+            umma::mbar_init(empty + i, HALVES);
         }
-        for (int i = 0; i < NT; ++i) {
+        for (int i = 0; i < HALVES * NT; ++i) {
             umma::mbar_init(tfull + i, 1);
-            umma::mbar_init(tempty + i, (PAIR ? 2 : 1) * Sh::EPI_WARPS);
+            umma::mbar_init(tempty + i, (PAIR ? 2 : 1) * Sh::EPI_WARPS / HALVES);
         }
         for (int i = 0; i < NSC; ++i) {
             umma::mbar_init(sfull + i, 32);
@@ -278,9 +284,9 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
         return false;
     };
 
-    constexpr bool MOVE_REGS = Sh::EPI_WARPS == 16;
+    constexpr bool MOVE_REGS = Sh::EPC == 128;
     if (warp < 4) {
-    if constexpr (MOVE_REGS) regs_dec<64>();
+    if constexpr (MOVE_REGS) regs_dec<72>();
     // Loading and issuing warps walk their loops with all lanes and elect one for the
     // instruction itself: loops of a lone lane lose the uniform registers that descriptors
     // and barriers are addressed with.
@@ -300,7 +306,10 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
                         const uint32_t bar = at_rank(full + st, 0);
                         if (rank == 0) umma::mbar_expect_tx(full + st, 2 * Sh::ST);
                         tma_load_pair(buf, &maps.a, BK * kb, 0, Sh::ROWS * tr + BM * rank, bar);
-                        tma_load_pair(buf + Sh::A_ST, &maps.b, BK * kb, 0, BN * tc + Sh::B_ROWS * rank, bar);
+                        // this CTA's 64 rows of B for each half of the columns
+                        for (int h = 0; h < 2; ++h)
+                            tma_load_pair(buf + Sh::A_ST + h * (Sh::B_ST / 2), &maps.b, BK * kb, 0,
+                                          BN * tc + HN * h + HN / 2 * rank, bar);
                     } else {
                         umma::mbar_expect_tx(full + st, Sh::ST);
                         umma::tma_load_3d(buf, &maps.a, BK * kb, 0, BM * tr, full + st);
@@ -320,35 +329,38 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
             }
     } else if ((warp == 1 || warp == 3) && rank == 0) {
         // -------------------------------------------------------------- MMA issuers
-        // Two warps take the K blocks in turn: one waits for its operands and its buffer
-        // while the other's MMAs are issued.  Every K block has a product of its own, so
-        // their order does not matter.
-        constexpr uint32_t idesc = umma::idesc_f16(Sh::ROWS, BN, false, false);   // format 0 is e4m3 in this kind
+        // Two warps, so that one waits for its operands and its buffer while the other's MMAs
+        // are issued: they take the K blocks in turn, or of a pair's the two halves.  Every
+        // product has a buffer of its own, so their order does not matter.
+        constexpr uint32_t idesc = umma::idesc_f16(Sh::ROWS, HN, false, false);   // format 0 is e4m3 in this kind
         const uint64_t d0 = umma::sw128_desc(umma::smem_u32(sm), 16, 1024);
-        int skip = warp == 3, st = skip, ts = skip;
+        constexpr int TURN = HALVES == 2 ? 1 : 2;   // K blocks from one of this warp's to its next
+        const int half = HALVES == 2 && warp == 3;
+        int skip = HALVES == 1 && warp == 3, st = skip, ts = skip;
         uint32_t ph = 0, tph = 1;
         bool any = false;
         for (int t = first; t < n_tiles; t += step) {
             int kb = k_lo + skip;
-            for (; kb < k_hi; kb += 2) {
-                wait(tempty + ts, tph);
+            for (; kb < k_hi; kb += TURN) {
+                wait(tempty + half * NT + ts, tph);
                 wait(full + st, ph);
                 __syncwarp();
                 umma::tc_fence_after();
                 if (elect_one()) {
-                    const uint64_t ad = d0 + (uint32_t)st * (Sh::ST >> 4), bd = ad + (Sh::A_ST >> 4);
+                    const uint64_t ad = d0 + (uint32_t)st * (Sh::ST >> 4);
+                    const uint64_t bd = ad + ((Sh::A_ST + half * (Sh::B_ST / 2)) >> 4);
 #pragma unroll
                     for (int ks = 0; ks < BK / 32; ++ks)   // 32 bytes of K: start address + 2 (units of 16)
-                        mma_e4m3<PAIR>(tbase + ts * BN, ad + 2 * ks, bd + 2 * ks, idesc, ks > 0);
+                        mma_e4m3<PAIR>(tbase + (half * NT + ts) * HN, ad + 2 * ks, bd + 2 * ks, idesc, ks > 0);
                     commit<PAIR>(empty + st);
-                    commit<PAIR>(tfull + ts);
+                    commit<PAIR>(tfull + half * NT + ts);
                 }
                 __syncwarp();
                 any = true;
-                if ((st += 2) >= NS) { st -= NS; ph ^= 1; }
-                if ((ts += 2) >= NT) { ts -= NT; tph ^= 1; }
+                if ((st += TURN) >= NS) { st -= NS; ph ^= 1; }
+                if ((ts += TURN) >= NT) { ts -= NT; tph ^= 1; }
             }
-            skip = kb - k_hi;   // an odd number of K blocks: the other warp begins the next tile
+            if (TURN == 2) skip = kb - k_hi;   // an odd number of K blocks: the other warp begins the next tile
         }
         // after an abort the epilogue may not have waited for the last MMAs: they
         // complete before the tensor memory is released
@@ -391,15 +403,17 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
         copies_wait();
     }
     } else {
-        if constexpr (MOVE_REGS) regs_inc<104>();
+        if constexpr (MOVE_REGS) regs_inc<216>();
         // ----------------------------------------------------------------- epilogue
         // TMEM lane quadrant warp % 4: one row of the tile per lane; each four warps take
         // the next EPC columns
         const int qd = warp & 3, c0 = EPC * ((warp - 4) >> 2);
-        const uint32_t trow = tbase + ((uint32_t)(32 * qd) << 16) + c0;
+        const int half = c0 / HN;   // buffers and barriers of this warp's product
+        const uint32_t trow = tbase + ((uint32_t)(32 * qd) << 16) + half * NT * HN + c0 % HN;
         int ts = 0, ss = 0;
         uint32_t tph = 0, sph = 0;
-        const uint32_t tempty0 = PAIR ? at_rank(tempty, 0) : umma::smem_u32(tempty);   // the issuers' copy
+        uint64_t *const tf = tfull + half * NT;
+        const uint32_t te = PAIR ? at_rank(tempty + half * NT, 0) : umma::smem_u32(tempty);   // the issuers' copy
         float2 acc[EPC / 2];
         const float *scales = reinterpret_cast<const float *>(sm + Sh::OFF_SC);
         for (Tile t(first, tiles_r); t.i < n_tiles; t.next(step, tiles_r)) {
@@ -423,28 +437,34 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
                 }
                 const float s = s4.x;
                 s4 = make_float4(s4.y, s4.z, s4.w, 0.f);
-                wait(tfull + ts, tph);
+                wait(tf + ts, tph);
                 __syncwarp();
                 umma::tc_fence_after();
-                constexpr int W = EPC < 32 ? EPC : 32;
+                // 32 columns at a time, the next ones on their way while these are added
+                constexpr int W = EPC < 32 ? EPC : 32, NW = EPC / W;
+                uint32_t v[NW > 1 ? 2 : 1][W];
+                auto load = [&](int i) {
+                    if constexpr (W == 32) umma::tmem_ld32_nowait(trow + ts * HN + i * W, v[NW > 1 ? i & 1 : 0]);
+                    else umma::tmem_ld16_nowait(trow + ts * HN + i * W, v[0]);
+                };
+                load(0);
 #pragma unroll
-                for (int j0 = 0; j0 < EPC; j0 += W) {
-                    uint32_t v[W];
-                    if constexpr (W == 32) umma::tmem_ld32_nowait(trow + ts * BN + j0, v);
-                    else umma::tmem_ld16_nowait(trow + ts * BN + j0, v);
+                for (int i = 0; i < NW; ++i) {
                     umma::tmem_ld_wait();
-                    if (j0 + W == EPC) {   // the buffer is read: the next product may take it
+                    if (i + 1 < NW) load(i + 1);
+                    else {   // the buffer is read: the next product may take it
                         umma::tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) arrive_at<PAIR>(tempty0 + 8 * ts);
+                        if (lane == 0) arrive_at<PAIR>(te + 8 * ts);
                     }
+                    const uint32_t *x = v[NW > 1 ? i & 1 : 0];
 #pragma unroll
                     for (int j = 0; j < W; j += 2) {
                         float2 f = make_float2(s, s);
                         if constexpr (SWAP)
-                            f = make_float2(sc[SG * (c0 + j0 + j) + sg] * s, sc[SG * (c0 + j0 + j + 1) + sg] * s);
-                        float2 &d = acc[(j0 + j) / 2];
-                        d = ffma2(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), f, d);
+                            f = make_float2(sc[SG * (c0 + i * W + j) + sg] * s, sc[SG * (c0 + i * W + j + 1) + sg] * s);
+                        float2 &d = acc[(i * W + j) / 2];
+                        d = ffma2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), f, d);
                     }
                 }
                 if (++ts == NT) { ts = 0; tph ^= 1; }
@@ -571,7 +591,7 @@ cudaError_t launch_shape(int M, int N, int K, const void *A, long long lda, cons
                         fp8::BM);
     if (e != cudaSuccess) return e;
     e = make_tma_mat_u8(reinterpret_cast<TmaMap *>(&m.b), Sh::SWAP ? A : B, K, Sh::SWAP ? M : N, Sh::SWAP ? lda : ldb,
-                        Sh::B_ROWS);
+                        Sh::PAIR ? Sh::B_ROWS / 2 : Sh::B_ROWS);
     if (e != cudaSuccess) return e;
     const bool tma_out = !Sh::SWAP && (reinterpret_cast<uintptr_t>(C) & 15) == 0 && ldc * sizeof(Tout) % 16 == 0;
     if (tma_out && (e = make_tma_mat_out(reinterpret_cast<TmaMap *>(&m.c), C, sizeof(Tout) == 2, N, M, ldc)) !=
