@@ -182,12 +182,18 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ float ld_cluster(uint32_t addr, int rank) {
-    uint32_t remote;
-    float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote));   // no clobber: loads overlap
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
+    float4 v;   // no clobber: loads overlap
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
     return v;
+}
+__device__ __forceinline__ void store4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 v) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+    uint2 u;
+    memcpy(&u.x, &a, 4);
+    memcpy(&u.y, &b, 4);
+    *reinterpret_cast<uint2 *>(p) = u;
 }
 
 // One 16-byte chunk of a result row.
@@ -533,19 +539,37 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
     if (split > 1) {
         cluster_sync();
         const int tr = first % tiles_r, tc = first / tiles_r;
-        const uint32_t base = umma::smem_u32(sm);
-        // elements of the tile in the order of C's rows; rank `part` adds its share
-        constexpr int INNER = SWAP ? BM : BN, OUTER = SWAP ? BN : BM;
-        const int total = INNER * OUTER, lo = total / split * part, hi = part + 1 == split ? total : lo + total / split;
+        // the tile four elements at a time in the order of C's rows; rank `part` adds its
+        // share, all ranks' loads of an element in flight together
+        constexpr int V = (SWAP ? BM : BN) / 4, OUTER = SWAP ? BN : BM;
+        constexpr int total = V * OUTER;
+        const int lo = total * part / split, hi = total * (part + 1) / split;
+        uint32_t from[8];
+#pragma unroll
+        for (int p = 0; p < 8; ++p) from[p] = at_rank(sm, p < split ? p : 0);
+        const bool vec = (reinterpret_cast<uintptr_t>(C) & 15) == 0 && ldc % (16 / (int)sizeof(Tout)) == 0;
         const bool whole = *abort_flag == 0;   // after an abort the parts are not complete: write nothing
         for (int i = lo + tid; whole && i < hi; i += Sh::THREADS) {
-            const int o = i / INNER, in = i % INNER;
+            const int o = i / V, in = 4 * (i % V);
             const long long m = SWAP ? (long long)BN * tc + o : (long long)BM * tr + o;
             const long long n = SWAP ? (long long)BM * tr + in : (long long)BN * tc + in;
-            if (m < M && n < N) {
-                float v = 0.f;
-                for (int p = 0; p < split; ++p) v += ld_cluster(base + (uint32_t)(o * Sh::PART_LD + in) * 4, p);
-                C[m * ldc + n] = from_f32<Tout>(v);
+            if (m >= M || n >= N) continue;
+            float4 v[8];
+#pragma unroll
+            for (int p = 0; p < 8; ++p)
+                if (p < split) v[p] = ld_cluster(from[p] + (uint32_t)(o * Sh::PART_LD + in) * 4);
+#pragma unroll
+            for (int p = 1; p < 8; ++p)
+                if (p < split) {
+                    v[0].x += v[p].x; v[0].y += v[p].y; v[0].z += v[p].z; v[0].w += v[p].w;
+                }
+            Tout *dst = C + m * ldc + n;
+            if (vec && n + 4 <= N) store4(dst, v[0]);
+            else {
+                const float x[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (n + e < N) dst[e] = from_f32<Tout>(x[e]);
             }
         }
         __syncwarp();
@@ -559,6 +583,19 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
 }
 
 namespace {
+
+// The kernel's shared-memory limit, set once per device.
+template <class Sh, typename Tout, typename Kernel> cudaError_t allow_smem(Kernel *kernel) {
+    static std::atomic<bool> done[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (done[dev]) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM);
+    if (e == cudaSuccess) done[dev] = true;
+    return e;
+}
 
 // Clusters of two CTAs of this kernel that the current device runs at once (asked once
 // per device and kernel).
@@ -598,8 +635,7 @@ cudaError_t launch_shape(int M, int N, int K, const void *A, long long lda, cons
                        cudaSuccess)
         return e;
     auto *kernel = gemm_fp8_kernel<Sh, Tout>;
-    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM)) != cudaSuccess)
-        return e;
+    if ((e = allow_smem<Sh, Tout>(kernel)) != cudaSuccess) return e;
     const long long rows = Sh::SWAP ? N : M, cols = Sh::SWAP ? M : N;
     const long long tiles = ((rows + Sh::ROWS - 1) / Sh::ROWS) * ((cols + Sh::BN - 1) / Sh::BN);
     const int cluster = Sh::PAIR ? 2 : split;
