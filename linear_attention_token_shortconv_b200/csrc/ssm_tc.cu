@@ -40,7 +40,10 @@ constexpr int REC = 368;          // floats of one (chunk, head) record
 constexpr int R_L = 0, R_U = 64, R_W = 128, R_YI = 192, R_YW = 256, R_UH = 320, R_DEC = 352, R_UMAX = 353;
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr uint32_t MAX_POLLS = 1u << 24;
-constexpr int THREADS = 512;
+// 16 warps compute; one more issues the MMAs and one the copies (and two idle: registers
+// move between groups of four warps, 16 x 104 + 4 x 64 of the 20 x 96 at launch)
+constexpr int CWARPS = 16, MMA_WARP = 16, COPY_WARP = 17, THREADS = 32 * 20;
+constexpr int COMPUTE_REGS = 104, SERVE_REGS = 64;
 // one 64-column block of a tile: B hi | C | B lo, each 64 rows of 128 bytes.  In this
 // order C is followed by B lo and preceded by B hi, so an M = 128 operand that starts
 // at C (or at B hi) has the chunk's C in its rows 0..63 (or 64..127); the other rows
@@ -117,9 +120,15 @@ __device__ __forceinline__ uint4 lds128(uint32_t p) {
     return v;
 }
 
-__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(umma::smem_u32(bar)) : "memory");
+// 32 lanes x 8 columns of tensor memory; valid after tmem_ld_wait().
+__device__ __forceinline__ void tmem_ld8_nowait(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
 }
+
+template <int R> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R> __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
@@ -344,8 +353,8 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = umma::align_smem<1024>(smem_raw);
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + Sm::OFF_BAR);
-    uint64_t *bar_sc = full + 2, *bar_u = full + 3, *bar_y = full + 4, *full_z = full + 5, *bar_w = full + 7;
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(full + 8);
+    uint64_t *bar_sc = full + 2, *bar_u = full + 3, *bar_y = full + 4, *full_z = full + 5;
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(full + 7);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tslot + 1);
     float *cw = reinterpret_cast<float *>(sm + Sm::OFF_CW);
     uint32_t *mx = reinterpret_cast<uint32_t *>(sm + Sm::OFF_MAX);
@@ -369,58 +378,25 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
     if (STATE_ONLY ? (seg >= last_seg && !(seg == 0 && a.s0_copy)) : seg > last_seg) return;
     const int slot0 = first_slot(begin, n) + c_lo;
 
-    // ---- the state of this thread: row 32 q + lane, columns 32 cg .. + 31 of the block
-    const int srow = 32 * q + lane, sc0 = 32 * cg;
-    const bool owner = srow < N && (cg < 2 || live1);
+    // ---- the state of a computing thread: row 32 q + lane, columns 32 cg .. + 31 of the block
+    const bool computes = warp < CWARPS;
+    const int srow = 32 * q + lane, sc0 = 32 * (cg & 3);
+    const bool owner = computes && srow < N && (cg < 2 || live1);
     const int shead = cg < 2 ? head0 : head1;
     const int spc = a.P == 64 ? sc0 & 63 : sc0;                       // column within the head
     const size_t sbase = (((size_t)n * a.H + shead) * N + srow) * a.P + spc;
-    float2 S[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) S[j] = make_float2(0.f, 0.f);
-    auto load_state = [&](const float *p) {
-#pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-            const float4 v = *reinterpret_cast<const float4 *>(p + 2 * j);
-            S[j] = make_float2(v.x, v.y);
-            S[j + 1] = make_float2(v.z, v.w);
-        }
-    };
-    auto store_state = [&](float *p) {
-#pragma unroll
-        for (int j = 0; j < 16; j += 2)
-            *reinterpret_cast<float4 *>(p + 2 * j) = make_float4(S[j].x, S[j].y, S[j + 1].x, S[j + 1].y);
-    };
     const size_t seg_base = ((size_t)n * gridDim.x + blk) * (a.n_seg - 1);   // of this chain's segments
     auto seg_ptr = [&](int k) { return a.seg_state + ((seg_base + k) * N + srow) * 128 + sc0; };
-    if (owner) {
-        if (STATE_ONLY || seg == 0) {
-            if (seg == 0 && a.S0) {
-                const bool copied = !STATE_ONLY && a.s0_copy;
-                load_state((copied ? a.s0_copy : a.S0) + sbase);
-                if (STATE_ONLY && a.s0_copy) store_state(a.s0_copy + sbase);
-            }
-        } else {
-            // the segments before this one joined: I <- decay I + state
-            load_state(seg_ptr(0));
-            for (int k = 1; k < seg; ++k) {
-                const float d = __ldg(a.seg_decay + (seg_base + k) * 2 + (cg >> 1));
-                const float *p = seg_ptr(k);
+    if (STATE_ONLY && seg == 0 && a.s0_copy && owner) {
 #pragma unroll
-                for (int j = 0; j < 16; j += 2) {
-                    const float4 v = *reinterpret_cast<const float4 *>(p + 2 * j);
-                    S[j] = ffma2(make_float2(d, d), S[j], make_float2(v.x, v.y));
-                    S[j + 1] = ffma2(make_float2(d, d), S[j + 1], make_float2(v.z, v.w));
-                }
-            }
-        }
+        for (int j = 0; j < 32; j += 4)
+            *reinterpret_cast<float4 *>(a.s0_copy + sbase + j) = *reinterpret_cast<const float4 *>(a.S0 + sbase + j);
     }
     if (STATE_ONLY && seg >= last_seg) return;   // only the copy of S0 was wanted
 
-    if (warp == 0) umma::tmem_alloc(tslot, 512);
+    if (warp == MMA_WARP) umma::tmem_alloc(tslot, 512);
     if (tid == 0) {
-        for (int i = 0; i < 7; ++i) umma::mbar_init(full + i, i == 4 ? 2 : 1);   // y: two products
-        umma::mbar_init(bar_w, THREADS / 32);
+        for (int i = 0; i < 7; ++i) umma::mbar_init(full + i, 1);
         *abort_flag = 0;
         umma::fence_mbar_init();
     }
@@ -438,8 +414,10 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
     umma::tc_fence_after();
     const uint32_t tb = *tslot;
     const uint32_t T_SC = tb, T_YI = tb + 128, T_YW = tb + 256, T_U = tb + 384;
-    const uint32_t lane_off = (uint32_t)(32 * q) << 16;
+    const uint32_t sT = umma::smem_u32(sm);
 
+    // A wait that expires raises the abort flag: later ones give up soon after, no more
+    // copies are started, and the state is not stored.
     auto wait = [&](uint64_t *bar, uint32_t parity) {
         for (uint32_t i = 0; i < MAX_POLLS; ++i) {
             if (umma::mbar_try_wait(bar, parity)) return;
@@ -448,389 +426,427 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
         *abort_flag = 1;
         atomicOr(&g_ssm_err, 1u);
     };
-    auto issue = [&](int c) {   // tiles and records of chunk c into stage c & 1
-        const int b = c & 1;
-        const size_t slot = (size_t)slot0 + c;
-        umma::mbar_expect_tx(full + b, Sm::TILE + 2 * REC * 4);
-        bulk_load(sm + b * Sm::TILE, a.tiles + (slot * a.G + g) * Sm::TILE, Sm::TILE, full + b);
-        bulk_load(sm + Sm::OFF_REC + b * 2 * REC * 4, a.rec + (slot * a.H + head0) * REC, REC * 4, full + b);
-        bulk_load(sm + Sm::OFF_REC + (b * 2 + 1) * REC * 4, a.rec + (slot * a.H + head1) * REC, REC * 4, full + b);
-    };
-    auto issue_z = [&](int c) {
-        uint8_t *p = sm + Sm::OFF_Z + (c & 1) * 16384;
-        const int t = begin + (c_lo + c) * Q;
-        umma::mbar_expect_tx(full_z + (c & 1), live1 ? 16384 : 8192);
-        umma::tma_load_3d(p, &maps.z, (int)xcol, 0, t, full_z + (c & 1));
-        if (live1) umma::tma_load_3d(p + 8192, &maps.z, (int)xcol + 64, 0, t, full_z + (c & 1));
-    };
-    if (tid == 0)
-        for (int c = 0; c < 2 && c < chunks; ++c) {
-            issue(c);
-            if (!STATE_ONLY && a.z && c == 0) issue_z(c);
-        }
+    // Two barriers a chunk, of the computing warps and the two that serve them: "drained",
+    // after which the previous chunk is done with shared and tensor memory, and "ready",
+    // after which this chunk's operands are there.
+    auto meet = [] { umma::named_bar_sync(1, 32 * (CWARPS + 2)); };
 
-    // ---- raw x of this thread: tokens 4 warp .. + 3 and the three before, columns 4 lane .. + 3
-    const int xc = 4 * lane, half = lane >> 4;
-    const bool xlive = half == 0 || live1;
-    uint2 raw[7];
-    auto fetch = [&](int c) {
-        const int t = begin + (c_lo + c) * Q + 4 * warp - 3;
-        const bf16 *p = a.x + t * a.ld_x + xcol + xc;
-        if (t >= begin && t + 7 <= end && live1) {
-#pragma unroll
-            for (int j = 0; j < 7; ++j) raw[j] = __ldg(reinterpret_cast<const uint2 *>(p + j * a.ld_x));
-            return;
-        }
-#pragma unroll
-        for (int j = 0; j < 7; ++j) {
-            raw[j] = make_uint2(0, 0);
-            if (!xlive) continue;
-            if (t + j >= begin) {
-                if (t + j < end) raw[j] = __ldg(reinterpret_cast<const uint2 *>(p + j * a.ld_x));
-            } else if (a.hist) {
-                raw[j] = __ldg(reinterpret_cast<const uint2 *>(a.hist + ((size_t)n * 3 + (t + j - begin + 3)) * chans +
-                                                               xcol + xc));
-            }
-        }
-    };
-    // convolution and activation of the fetched tokens of chunk c, and the largest |x| of
-    // each half into mx[c & 1][half]
-    float2 xh[4][2];
-    auto convolve = [&](int c) {
-        const int len = min(Q, end - (begin + (c_lo + c) * Q));
-        float2 w[5][2], f[7][2];
-#pragma unroll
-        for (int j = 0; j < 5; ++j) {
-            const float4 v = *reinterpret_cast<const float4 *>(cw + 128 * j + xc);
-            w[j][0] = make_float2(v.x, v.y);
-            w[j][1] = make_float2(v.z, v.w);
-        }
-#pragma unroll
-        for (int j = 0; j < 7; ++j) {
-            f[j][0] = make_float2(bf16lo(raw[j].x), bf16hi(raw[j].x));
-            f[j][1] = make_float2(bf16lo(raw[j].y), bf16hi(raw[j].y));
-        }
-        float m = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const bool in = 4 * warp + i < len;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float2 v = w[4][e];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v = ffma2(w[j][e], f[i + j][e], v);
-                v = silu2(v);
-                xh[i][e] = in ? v : make_float2(0.f, 0.f);
-                m = amax2(m, xh[i][e]);
-            }
-        }
-#pragma unroll
-        for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if ((lane & 15) == 0) atomicMax(mx + (c & 1) * 4 + half, __float_as_uint(m));
-    };
-
-    const float dskip = !STATE_ONLY && a.D ? __ldg(a.D + (q < 2 ? head0 : head1)) : 0.f;
-    float decay0 = 1.f, decay1 = 1.f;   // of the whole segment (state pass)
-    // operand addresses of this thread: a row's 16-byte chunks k, k ^ 1, ... differ by an
-    // exclusive or with the chunk's bits
-    const uint32_t sT = umma::smem_u32(sm);
-    const uint32_t p_x = sT + Sm::OFF_X + half * 8192 + umma::sw128_offset(4 * warp, (lane & 15) >> 1) + 8 * (lane & 1);
-    const uint32_t p_s = sT + Sm::OFF_S + (cg >> 1) * (N * 128) + umma::sw128_offset(srow, (cg & 1) * 4);
-    const int hv = q >> 1, t = 32 * (q & 1) + lane;      // rows of y: half and token of this thread
-    const int oc = 64 * hv + 16 * cg;                    // and its 16 columns
-    const uint32_t p_o = sT + Sm::OFF_X + hv * 8192 + umma::sw128_offset(t, 2 * cg);
-    // matrix descriptors; the start address field counts 16 bytes
-    const uint64_t d_tile = umma::sw128_desc(sT, 16, 1024);
-    const uint64_t d_tile_mn = umma::sw128_desc(sT, N == 128 ? KB : 0, 1024);   // N = 64: rows 64.. repeat rows 0..
-    const uint64_t d_x = umma::sw128_desc(sT + Sm::OFF_X, 8192, 1024);
-    const uint64_t d_s = umma::sw128_desc(sT + Sm::OFF_S, 16, 1024);
-
-    if (chunks > 0) {
-        fetch(0);
-        convolve(0);
-        if (chunks > 1) fetch(1);
-    }
-    for (int c = 0; c < chunks; ++c) {
-        const int b = c & 1;
-        const uint32_t ph = (uint32_t)c & 1u, ph_full = (uint32_t)(c >> 1) & 1u;
-        const int t0 = begin + (c_lo + c) * Q, len = min(Q, end - t0);
-        const float *rec0 = reinterpret_cast<const float *>(sm + Sm::OFF_REC) + b * 2 * REC, *rec1 = rec0 + REC;
-        if (!STATE_ONLY) {
-            float ms = 0.f;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) ms = amax2(ms, S[j]);
-            const uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(ms));
-            if (lane == 0) atomicMax(mx + b * 4 + 2 + (cg >> 1), mb);
-        }
-        __syncthreads();   // the previous chunk is done with the tiles, the stage of chunk c - 1 and x
-        if (tid < 4) mx[(b ^ 1) * 4 + tid] = 0;   // chunk c - 1's, for chunk c + 1, whose x is added after the next barrier
-
-        // ---- scales; operands into shared memory
-        const uint4 mxv = *reinterpret_cast<const uint4 *>(mx + b * 4);
-        float xs0, xs1, xinv0, xinv1;
-        scale_pow2(mxv.x, 13, xs0, xinv0);
-        scale_pow2(mxv.y, 13, xs1, xinv1);
-        float sinv = 0.f;                    // of the rows of y of this thread
-        wait(full + b, ph_full);
-        {
-            const float4 wr4 = *reinterpret_cast<const float4 *>((half ? rec1 : rec0) + R_W + 4 * warp);
-            const float wr[4] = {wr4.x, wr4.y, wr4.z, wr4.w};
-            const float xs = half ? xs1 : xs0;
-            const float2 xs2 = make_float2(xs, xs);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t p = (p_x ^ (16 * i)) + 128 * i;
-                uint32_t x2[2], hi2[2], lo2[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float2 u = fmul2(xh[i][e], xs2), v = fmul2(u, make_float2(wr[i], wr[i]));
-                    x2[e] = pack(u);
-                    hi2[e] = pack(v);
-                    const float2 h = half2_float2(hi2[e]);
-                    lo2[e] = umma::pack_half2(v.x - h.x, v.y - h.y);
-                }
-                if (!STATE_ONLY) sts64(p, x2[0], x2[1]);
-                sts64(p + (Sm::OFF_XH - Sm::OFF_X), hi2[0], hi2[1]);
-                sts64(p + (Sm::OFF_XL - Sm::OFF_X), lo2[0], lo2[1]);
-            }
-        }
-        if (!STATE_ONLY) {
-            float s0, s1, i0, i1;
-            scale_pow2(mxv.z, 13, s0, i0);
-            scale_pow2(mxv.w, 13, s1, i1);
-            sinv = hv ? i1 : i0;
-            const float ss = cg < 2 ? s0 : s1;
-            const float2 ss2 = make_float2(ss, ss);
-            if (srow < N) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    sts128(p_s ^ (16 * j), make_uint4(pack(fmul2(S[4 * j], ss2)), pack(fmul2(S[4 * j + 1], ss2)),
-                                                      pack(fmul2(S[4 * j + 2], ss2)), pack(fmul2(S[4 * j + 3], ss2))));
-            }
-        }
-        umma::fence_proxy_async_smem();
-        umma::tc_fence_before();
-        __syncthreads();
-        // The tensor pipe takes MMAs about as fast as it runs them, so their issuer waits
-        // along.  The four warps with no scores of their own to decay (tokens 0 .. 31
-        // against 32 .. 63) share that work and the copies.
-        const uint64_t dt = d_tile + (uint32_t)(b * (Sm::TILE >> 4));
-        constexpr int KS = N / 16;   // K steps over the state dim
-        if (!STATE_ONLY && warp == 8) {
-            if (elect_one()) {
-                umma::tc_fence_after();
-                const uint32_t id = umma::idesc_f16(128, 64, false, false);
-#pragma unroll
-                for (int j = 0; j < 2; ++j)   // scores: C in rows 64 j .. 64 j + 63
-#pragma unroll
-                    for (int k = 0; k < KS; ++k) {
-                        const uint32_t kb = ((k / 4) * KB + (k % 4) * 32) >> 4;
-                        umma::mma_f16(T_SC + 64 * j, dt + (kb + (j ? 0 : OFF_C >> 4)), dt + kb, id, k > 0);
-                    }
-                umma::mma_commit(bar_sc);
-            }
-            __syncwarp();
-        }
-        if (warp == 10) {
-            if (elect_one()) {
-                umma::tc_fence_after();
-                const uint32_t id = umma::idesc_f16(128, 128, true, true);
-                const uint64_t da = d_tile_mn + (uint32_t)(b * (Sm::TILE >> 4));
-                const uint64_t dxh = d_x + ((Sm::OFF_XH - Sm::OFF_X) >> 4), dxl = d_x + ((Sm::OFF_XL - Sm::OFF_X) >> 4);
-#pragma unroll
-                for (int p = 0; p < 3; ++p)   // hi hi, hi lo, lo hi
-#pragma unroll
-                    for (int k = 0; k < Q / 16; ++k)
-                        umma::mma_f16(T_U, da + (((p == 2 ? OFF_LO : 0) + k * 2048) >> 4),
-                                      (p == 1 ? dxl : dxh) + ((k * 2048) >> 4), id, p > 0 || k > 0);
-                umma::mma_commit(bar_u);
-            }
-            __syncwarp();
-        }
-        if (warp == 14) {
-            if (elect_one() && c >= 1 && c + 1 < chunks) issue(c + 1);
-            __syncwarp();
-        }
-        if (!STATE_ONLY && warp == 12) {
-            if (elect_one() && c >= 1) {   // out of chunk c - 1, written before the barrier
-                const uint8_t *p = sm + Sm::OFF_Z + (b ^ 1) * 16384;
-                umma::tma_store_3d(&maps.out, (int)xcol, 0, t0 - Q, p);
-                if (live1) umma::tma_store_3d(&maps.out, (int)xcol + 64, 0, t0 - Q, p + 8192);
-                umma::bulk_commit();
-            }
-            __syncwarp();
-        }
-        // ---- while they run: x of the next chunk
-        const float *recv = hv ? rec1 : rec0;
-        if (c + 1 < chunks) {
-            convolve(c + 1);
-            if (c + 2 < chunks) fetch(c + 2);
-        }
-        if (!STATE_ONLY && warp == 12) {
-            if (elect_one() && a.z && c + 1 < chunks) {   // its tile takes z of chunk c + 1
-                umma::bulk_wait_read<0>();
-                issue_z(c + 1);
-            }
-            __syncwarp();
-        }
-        if (!STATE_ONLY && warp == 8) {
-            if (elect_one()) {
-                const uint32_t id = umma::idesc_f16(128, 64, false, true);
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int k = 0; k < KS; ++k) {
-                        const uint32_t kb = ((k / 4) * KB + (k % 4) * 32) >> 4;
-                        umma::mma_f16(T_YI + 64 * j, dt + (kb + (j ? 0 : OFF_C >> 4)),
-                                      d_s + ((j * (N * 128) + k * 2048) >> 4), id, k > 0);
-                    }
-                umma::mma_commit(bar_y);
-            }
-            __syncwarp();
-        }
-        if (!STATE_ONLY) {
-            // ---- decayed scores: 16 of them per thread, as the A operand in tensor memory.
-            // Half 0 (lanes 0..63) writes columns 64 .. 95 and half 1 columns 0 .. 31, where
-            // the other half's scores lie in lanes that nobody reads.
-            wait(bar_sc, ph);
-            umma::tc_fence_after();
-            uint32_t p[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if ((q & 1) || cg < 2) {   // tokens 0 .. 31 see nothing of 32 .. 63
-                uint32_t sc[16];
-                umma::tmem_ld16_nowait(T_SC + lane_off + 64 * hv + 16 * cg, sc);
-                umma::tmem_ld_wait();
-                const float Lt = recv[R_L + t];
-                if ((q & 1) && cg < 2) {
-                    // t > 31 >= s: e^{L_t - L_s} = e^{L_t - L_31} e^{L_31 - L_s}, both at most 1
-                    const float et = ex2(Lt - recv[R_L + 31]);
-                    const float2 et2 = make_float2(et, et);
-#pragma unroll
-                    for (int s4 = 0; s4 < 4; ++s4) {
-                        const float4 u4 = *reinterpret_cast<const float4 *>(recv + R_UH + 16 * cg + 4 * s4);
-                        p[2 * s4] = pack(fmul2(fmul2(make_float2(u4.x, u4.y), et2), as_float2(sc[4 * s4], sc[4 * s4 + 1])));
-                        p[2 * s4 + 1] = pack(fmul2(fmul2(make_float2(u4.z, u4.w), et2), as_float2(sc[4 * s4 + 2], sc[4 * s4 + 3])));
-                    }
-                } else {
-#pragma unroll
-                    for (int s4 = 0; s4 < 4; ++s4) {
-                        const int s = 16 * cg + 4 * s4;
-                        const float4 l4 = *reinterpret_cast<const float4 *>(recv + R_L + s);
-                        const float4 u4 = *reinterpret_cast<const float4 *>(recv + R_U + s);
-                        float2 w0 = fmul2(as_float2(sc[4 * s4], sc[4 * s4 + 1]), make_float2(u4.x, u4.y));
-                        float2 w1 = fmul2(as_float2(sc[4 * s4 + 2], sc[4 * s4 + 3]), make_float2(u4.z, u4.w));
-                        w0 = fmul2(w0, make_float2(ex2(Lt - l4.x), ex2(Lt - l4.y)));
-                        w1 = fmul2(w1, make_float2(ex2(Lt - l4.z), ex2(Lt - l4.w)));
-                        p[2 * s4] = pack(make_float2(s > t ? 0.f : w0.x, s + 1 > t ? 0.f : w0.y));
-                        p[2 * s4 + 1] = pack(make_float2(s + 2 > t ? 0.f : w1.x, s + 3 > t ? 0.f : w1.y));
-                    }
-                }
-            }
-            umma::tmem_st8(T_SC + lane_off + (hv ? 0 : 64) + 8 * cg, p);
-            umma::tmem_st_wait();
-            umma::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar_w);
-            if (warp == 14) {
-                wait(bar_w, ph);
+    if (!computes) {
+        regs_dec<SERVE_REGS>();
+        if (warp == MMA_WARP) {
+            // ------------------------------------------------------------ MMA issuer
+            // The tensor pipe takes MMAs about as fast as it runs them, so their issuer
+            // waits along; it has nothing else to do.
+            const uint64_t d_tile = umma::sw128_desc(sT, 16, 1024);
+            const uint64_t d_tile_mn = umma::sw128_desc(sT, N == 128 ? KB : 0, 1024);   // N = 64: rows 64.. repeat 0..
+            const uint64_t d_x = umma::sw128_desc(sT + Sm::OFF_X, 8192, 1024);
+            const uint64_t d_s = umma::sw128_desc(sT + Sm::OFF_S, 16, 1024);
+            constexpr int KS = N / 16;   // K steps over the state dim
+            auto scores = [&](int c) {   // C in rows 64 j .. 64 j + 63
+                const uint64_t dt = d_tile + (uint32_t)((c & 1) * (Sm::TILE >> 4));
+                wait(full + (c & 1), (uint32_t)(c >> 1) & 1u);
+                __syncwarp();
                 if (elect_one()) {
-                    umma::tc_fence_after();
-                    const uint32_t id = umma::idesc_f16(128, 64, false, true);
+                    constexpr uint32_t id = umma::idesc_f16(128, 64, false, false);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)   // rows 64 j .. of the decayed scores, columns of half j
+                    for (int j = 0; j < 2; ++j)
 #pragma unroll
-                        for (int k = 0; k < Q / 16; ++k)
-                            umma::mma_f16_ts(T_YW + 64 * j, T_SC + (j ? 0 : 64) + 8 * k,
-                                             d_x + ((j * 8192 + k * 2048) >> 4), id, k > 0);
-                    umma::mma_commit(bar_y);
+                        for (int k = 0; k < KS; ++k) {
+                            const uint32_t kb = ((k / 4) * KB + (k % 4) * 32) >> 4;
+                            umma::mma_f16(T_SC + 64 * j, dt + (kb + (j ? 0 : OFF_C >> 4)), dt + kb, id, k > 0);
+                        }
+                    umma::mma_commit(bar_sc);
                 }
                 __syncwarp();
-            }
-        }
-        // ---- state
-        wait(bar_u, ph);
-        umma::tc_fence_after();
-        {
-            const float *rs = cg < 2 ? rec0 : rec1;
-            const float dec = rs[R_DEC], add = rs[R_UMAX] * (cg < 2 ? xinv0 : xinv1);
-            const float2 dec2 = make_float2(dec, dec), add2 = make_float2(add, add);
-            uint32_t v[32];
-            umma::tmem_ld32_nowait(T_U + lane_off + sc0, v);
-            umma::tmem_ld_wait();
+            };
+            if (!STATE_ONLY && chunks > 0) scores(0);
+            for (int c = 0; c < chunks; ++c) {
+                const uint32_t st = (uint32_t)((c & 1) * (Sm::TILE >> 4));
+                meet();
+                meet();
+                umma::tc_fence_after();
+                if (elect_one()) {
+                    constexpr uint32_t idu = umma::idesc_f16(128, 128, true, true);
+                    const uint64_t da = d_tile_mn + st;
+                    const uint64_t dxh = d_x + ((Sm::OFF_XH - Sm::OFF_X) >> 4), dxl = d_x + ((Sm::OFF_XL - Sm::OFF_X) >> 4);
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-                S[j] = ffma2(dec2, S[j],
-                             fmul2(add2, make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]))));
-            if (STATE_ONLY) { decay0 *= rec0[R_DEC]; decay1 *= rec1[R_DEC]; }
-        }
-        if (!STATE_ONLY) {
-            // ---- output: token t of half hv, columns oc .. + 15; a whole chunk leaves by TMA
-            // from the z tile, a ragged one directly
-            if (a.z) wait(full_z + b, ph_full);
-            wait(bar_y, ph);
-            umma::tc_fence_after();
-            uint32_t yi[16], yw[16];
-            umma::tmem_ld16_nowait(T_YI + lane_off + oc, yi);
-            umma::tmem_ld16_nowait(T_YW + lane_off + oc, yw);
-            umma::tmem_ld_wait();
-            umma::tc_fence_before();
-            const float fx = hv ? xinv1 : xinv0;
-            const float fi = recv[R_YI + t] * sinv, fw = recv[R_YW + t] * fx, fd = dskip * fx;
-            const float2 fi2 = make_float2(fi, fi), fw2 = make_float2(fw, fw), fd2 = make_float2(fd, fd);
-            bf16 *const o = a.out + (long long)(t0 + t) * (a.H * a.P) + xcol + oc;
-            const uint32_t p_z = p_o + (Sm::OFF_Z - Sm::OFF_X) + b * 16384;
+                    for (int p = 0; p < 3; ++p)   // hi hi, hi lo, lo hi
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const uint4 xx = lds128(p_o ^ (16 * k));
-                const uint4 zz = a.z ? lds128(p_z ^ (16 * k)) : make_uint4(0, 0, 0, 0);
-                const uint32_t xw[4] = {xx.x, xx.y, xx.z, xx.w}, zw[4] = {zz.x, zz.y, zz.z, zz.w};
-                uint32_t w[4];
+                        for (int k = 0; k < Q / 16; ++k)
+                            umma::mma_f16(T_U, da + (((p == 2 ? OFF_LO : 0) + k * 2048) >> 4),
+                                          (p == 1 ? dxl : dxh) + ((k * 2048) >> 4), idu, p > 0 || k > 0);
+                    umma::mma_commit(bar_u);
+                    if (!STATE_ONLY) {
+                        constexpr uint32_t id = umma::idesc_f16(128, 64, false, true);
+                        const uint64_t dt = d_tile + st;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int i = 8 * k + 2 * e;
-                    float2 y = fmul2(half2_float2(xw[e]), fd2);
-                    y = ffma2(make_float2(__uint_as_float(yw[i]), __uint_as_float(yw[i + 1])), fw2, y);
-                    y = ffma2(make_float2(__uint_as_float(yi[i]), __uint_as_float(yi[i + 1])), fi2, y);
-                    if (a.z) y = fmul2(y, silu2(make_float2(bf16lo(zw[e]), bf16hi(zw[e]))));
-                    const __nv_bfloat162 pb = __floats2bfloat162_rn(y.x, y.y);
-                    w[e] = *reinterpret_cast<const uint32_t *>(&pb);
+                        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                            for (int k = 0; k < KS; ++k) {
+                                const uint32_t kb = ((k / 4) * KB + (k % 4) * 32) >> 4;
+                                umma::mma_f16(T_YI + 64 * j, dt + (kb + (j ? 0 : OFF_C >> 4)),
+                                              d_s + ((j * (N * 128) + k * 2048) >> 4), id, k > 0);
+                            }
+#pragma unroll
+                            for (int k = 0; k < Q / 16; ++k)   // rows 64 j .. of the decayed scores, columns of half j
+                                umma::mma_f16_ts(T_YW + 64 * j, T_SC + (j ? 0 : 64) + 8 * k,
+                                                 d_x + ((j * 8192 + k * 2048) >> 4), id, k > 0);
+                        }
+                        umma::mma_commit(bar_y);
+                    }
                 }
-                const uint4 w4 = make_uint4(w[0], w[1], w[2], w[3]);
-                if (len == Q) sts128(p_z ^ (16 * k), w4);
-                else if (t < len && (hv == 0 || live1)) reinterpret_cast<uint4 *>(o)[k] = w4;
+                __syncwarp();
+                if (!STATE_ONLY && c + 1 < chunks) {
+                    wait(bar_y, (uint32_t)c & 1u);   // the decayed scores are used up
+                    umma::tc_fence_after();
+                    scores(c + 1);
+                }
             }
-            umma::fence_proxy_async_smem();
-        }
-    }
-    if (!STATE_ONLY && chunks > 0) {
-        __syncthreads();
-        const int t = begin + (c_lo + chunks - 1) * Q;
-        if (warp == 12 && elect_one()) {   // the last chunk's tile; the copies end before the CTA does
-            if (t + Q <= end) {
-                const uint8_t *p = sm + Sm::OFF_Z + ((chunks - 1) & 1) * 16384;
+        } else if (warp == COPY_WARP) {
+            // ---------------------------------------------------------------- copies
+            const uint8_t *tile = a.tiles + ((size_t)slot0 * a.G + g) * Sm::TILE;
+            const float *rec = a.rec + ((size_t)slot0 * a.H + head0) * REC;
+            const size_t tile_step = (size_t)a.G * Sm::TILE, rec_step = (size_t)a.H * REC;
+            auto issue = [&](int c) {   // tiles and records of chunk c, in turn, into stage c & 1
+                uint64_t *bar = full + (c & 1);
+                uint8_t *r = sm + Sm::OFF_REC + (c & 1) * 2 * REC * 4;
+                umma::mbar_expect_tx(bar, Sm::TILE + 2 * REC * 4);
+                bulk_load(sm + (c & 1) * Sm::TILE, tile, Sm::TILE, bar);
+                bulk_load(r, rec, REC * 4, bar);
+                bulk_load(r + REC * 4, rec + (head1 - head0) * REC, REC * 4, bar);
+                tile += tile_step;
+                rec += rec_step;
+            };
+            auto issue_z = [&](int c) {
+                uint8_t *p = sm + Sm::OFF_Z + (c & 1) * 16384;
+                const int t = begin + (c_lo + c) * Q;
+                umma::mbar_expect_tx(full_z + (c & 1), live1 ? 16384 : 8192);
+                umma::tma_load_3d(p, &maps.z, (int)xcol, 0, t, full_z + (c & 1));
+                if (live1) umma::tma_load_3d(p + 8192, &maps.z, (int)xcol + 64, 0, t, full_z + (c & 1));
+            };
+            auto store_out = [&](int c) {
+                const uint8_t *p = sm + Sm::OFF_Z + (c & 1) * 16384;
+                const int t = begin + (c_lo + c) * Q;
                 umma::tma_store_3d(&maps.out, (int)xcol, 0, t, p);
                 if (live1) umma::tma_store_3d(&maps.out, (int)xcol + 64, 0, t, p + 8192);
                 umma::bulk_commit();
+            };
+            const bool one = elect_one();
+            if (one && chunks > 0) {
+                issue(0);
+                if (!STATE_ONLY && a.z) issue_z(0);
+                if (chunks > 1) issue(1);
             }
-            umma::bulk_wait_all();
+            for (int c = 0; c < chunks; ++c) {
+                meet();
+                if (one) {
+                    const bool go = *abort_flag == 0;
+                    if (c >= 1 && c + 1 < chunks && go) issue(c + 1);
+                    if (!STATE_ONLY) {
+                        // out of chunk c - 1 leaves; its tile then takes z of chunk c + 1
+                        if (c >= 1) {
+                            store_out(c - 1);
+                            umma::bulk_wait_read<0>();
+                        }
+                        if (a.z && c + 1 < chunks && go) issue_z(c + 1);
+                    }
+                }
+                __syncwarp();
+                meet();
+            }
+            if (!STATE_ONLY && chunks > 0) {
+                meet();
+                if (one) {   // the last chunk's tile, if it is whole; the copies end before the CTA does
+                    if (begin + (c_lo + chunks) * Q <= end) store_out(chunks - 1);
+                    umma::bulk_wait_all();
+                }
+                __syncwarp();
+            }
+            // after an abort, copies in flight land before the CTA leaves (bounded)
+            if (one && *abort_flag)
+                for (int b = 0; b < 2 && b < chunks; ++b) {
+                    umma::mbar_wait_bounded(full + b, (uint32_t)((chunks - 1 - b) / 2) & 1u, 1u << 16);
+                    if (!STATE_ONLY && a.z)
+                        umma::mbar_wait_bounded(full_z + b, (uint32_t)((chunks - 1 - b) / 2) & 1u, 1u << 16);
+                }
         }
-    }
-    if (owner && !*abort_flag) {
-        if (STATE_ONLY) {
-            store_state(seg_ptr(seg));
-            if (lane == 0 && q == 0 && (cg & 1) == 0)
+        if (!STATE_ONLY && chunks > 0 && warp == MMA_WARP) meet();
+    } else {
+        regs_inc<COMPUTE_REGS>();
+        const uint32_t lane_off = (uint32_t)(32 * q) << 16;
+        float2 S[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) S[j] = make_float2(0.f, 0.f);
+        if (owner) {
+            // the initial state, or the segments before this one joined: I <- decay I + state
+            const bool joined = !STATE_ONLY && seg > 0;
+            const float *p = joined ? seg_ptr(0) : seg > 0 || !a.S0 ? nullptr : (!STATE_ONLY && a.s0_copy ? a.s0_copy : a.S0) + sbase;
+            for (int k = 0; p && k < (joined ? seg : 1); ++k) {
+                if (k > 0) p = seg_ptr(k);
+                const float d = k > 0 ? __ldg(a.seg_decay + (seg_base + k) * 2 + (cg >> 1)) : 0.f;
+#pragma unroll
+                for (int j = 0; j < 16; j += 2) {
+                    const float4 v = *reinterpret_cast<const float4 *>(p + 2 * j);
+                    S[j] = ffma2(make_float2(d, d), S[j], make_float2(v.x, v.y));
+                    S[j + 1] = ffma2(make_float2(d, d), S[j + 1], make_float2(v.z, v.w));
+                }
+            }
+        }
+
+        // ---- raw x of this thread: tokens 4 warp .. + 3 and the three before, columns 4 lane .. + 3
+        const int xc = 4 * lane, half = lane >> 4;
+        const bool xlive = half == 0 || live1;
+        uint2 raw[7];
+        auto fetch = [&](int c) {
+            const int t = begin + (c_lo + c) * Q + 4 * warp - 3;
+            const bf16 *p = a.x + t * a.ld_x + xcol + xc;
+            if (t >= begin && t + 7 <= end && live1) {
+#pragma unroll
+                for (int j = 0; j < 7; ++j) raw[j] = __ldg(reinterpret_cast<const uint2 *>(p + j * a.ld_x));
+                return;
+            }
+#pragma unroll
+            for (int j = 0; j < 7; ++j) {
+                raw[j] = make_uint2(0, 0);
+                if (!xlive) continue;
+                if (t + j >= begin) {
+                    if (t + j < end) raw[j] = __ldg(reinterpret_cast<const uint2 *>(p + j * a.ld_x));
+                } else if (a.hist) {
+                    raw[j] = __ldg(reinterpret_cast<const uint2 *>(
+                        a.hist + ((size_t)n * 3 + (t + j - begin + 3)) * chans + xcol + xc));
+                }
+            }
+        };
+        // convolution and activation of the fetched tokens of chunk c, and the largest |x| of
+        // each half into mx[c & 1][half]
+        float2 xh[4][2];
+        auto convolve = [&](int c) {
+            const int len = min(Q, end - (begin + (c_lo + c) * Q));
+            float2 w[5][2], f[7][2];
+#pragma unroll
+            for (int j = 0; j < 5; ++j) {
+                const float4 v = *reinterpret_cast<const float4 *>(cw + 128 * j + xc);
+                w[j][0] = make_float2(v.x, v.y);
+                w[j][1] = make_float2(v.z, v.w);
+            }
+#pragma unroll
+            for (int j = 0; j < 7; ++j) {
+                f[j][0] = make_float2(bf16lo(raw[j].x), bf16hi(raw[j].x));
+                f[j][1] = make_float2(bf16lo(raw[j].y), bf16hi(raw[j].y));
+            }
+            float m = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool in = 4 * warp + i < len;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float2 v = w[4][e];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v = ffma2(w[j][e], f[i + j][e], v);
+                    v = silu2(v);
+                    xh[i][e] = in ? v : make_float2(0.f, 0.f);
+                    m = amax2(m, xh[i][e]);
+                }
+            }
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if ((lane & 15) == 0) atomicMax(mx + (c & 1) * 4 + half, __float_as_uint(m));
+        };
+
+        const float dskip = !STATE_ONLY && a.D ? __ldg(a.D + (q < 2 ? head0 : head1)) : 0.f;
+        float decay0 = 1.f, decay1 = 1.f;   // of the whole segment (state pass)
+        // operand addresses of this thread: a row's 16-byte chunks k, k ^ 1, ... differ by an
+        // exclusive or with the chunk's bits
+        const uint32_t p_x = sT + Sm::OFF_X + half * 8192 + umma::sw128_offset(4 * warp, (lane & 15) >> 1) + 8 * (lane & 1);
+        const uint32_t p_s = sT + Sm::OFF_S + (cg >> 1) * (N * 128) + umma::sw128_offset(srow, (cg & 1) * 4);
+        const int hv = q >> 1, t = 32 * (q & 1) + lane;      // rows of y: half and token of this thread
+        const int oc = 64 * hv + 16 * cg;                    // and its 16 columns
+        const uint32_t p_o = sT + Sm::OFF_X + hv * 8192 + umma::sw128_offset(t, 2 * cg);
+
+        if (chunks > 0) {
+            fetch(0);
+            convolve(0);
+            if (chunks > 1) fetch(1);
+        }
+        for (int c = 0; c < chunks; ++c) {
+            const int b = c & 1;
+            const uint32_t ph = (uint32_t)c & 1u, ph_full = (uint32_t)(c >> 1) & 1u;
+            const float *rec0 = reinterpret_cast<const float *>(sm + Sm::OFF_REC) + b * 2 * REC, *rec1 = rec0 + REC;
+            const float *recv = hv ? rec1 : rec0;
+            if (!STATE_ONLY) {
+                float ms = 0.f;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) ms = amax2(ms, S[j]);
+                const uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(ms));
+                if (lane == 0) atomicMax(mx + b * 4 + 2 + (cg >> 1), mb);
+            }
+            meet();   // drained
+            if (tid < 4) mx[(b ^ 1) * 4 + tid] = 0;   // chunk c - 1's, for chunk c + 1, whose x is added when this one is ready
+
+            // ---- scales; operands into shared memory
+            const uint4 mxv = *reinterpret_cast<const uint4 *>(mx + b * 4);
+            float xs0, xs1, xinv0, xinv1;
+            scale_pow2(mxv.x, 13, xs0, xinv0);
+            scale_pow2(mxv.y, 13, xs1, xinv1);
+            float sinv = 0.f;                    // of the rows of y of this thread
+            wait(full + b, ph_full);
+            {
+                const float4 wr4 = *reinterpret_cast<const float4 *>((half ? rec1 : rec0) + R_W + 4 * warp);
+                const float wr[4] = {wr4.x, wr4.y, wr4.z, wr4.w};
+                const float xs = half ? xs1 : xs0;
+                const float2 xs2 = make_float2(xs, xs);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t p = (p_x ^ (16 * i)) + 128 * i;
+                    uint32_t x2[2], hi2[2], lo2[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float2 u = fmul2(xh[i][e], xs2), v = fmul2(u, make_float2(wr[i], wr[i]));
+                        x2[e] = pack(u);
+                        hi2[e] = pack(v);
+                        const float2 h = half2_float2(hi2[e]);
+                        lo2[e] = umma::pack_half2(v.x - h.x, v.y - h.y);
+                    }
+                    if (!STATE_ONLY) sts64(p, x2[0], x2[1]);
+                    sts64(p + (Sm::OFF_XH - Sm::OFF_X), hi2[0], hi2[1]);
+                    sts64(p + (Sm::OFF_XL - Sm::OFF_X), lo2[0], lo2[1]);
+                }
+            }
+            if (!STATE_ONLY) {
+                float s0, s1, i0, i1;
+                scale_pow2(mxv.z, 13, s0, i0);
+                scale_pow2(mxv.w, 13, s1, i1);
+                sinv = hv ? i1 : i0;
+                const float ss = cg < 2 ? s0 : s1;
+                const float2 ss2 = make_float2(ss, ss);
+                if (srow < N) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        sts128(p_s ^ (16 * j), make_uint4(pack(fmul2(S[4 * j], ss2)), pack(fmul2(S[4 * j + 1], ss2)),
+                                                          pack(fmul2(S[4 * j + 2], ss2)), pack(fmul2(S[4 * j + 3], ss2))));
+                }
+                umma::fence_proxy_async_smem();
+                // ---- decayed scores: 16 of them per thread, as the A operand in tensor memory.
+                // Half 0 (lanes 0..63) writes columns 64 .. 95 and half 1 columns 0 .. 31, where
+                // the other half's scores lie in lanes that nobody reads.
+                wait(bar_sc, ph);
+                umma::tc_fence_after();
+                uint32_t p[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                if ((q & 1) || cg < 2) {   // tokens 0 .. 31 see nothing of 32 .. 63
+                    uint32_t sc[16];
+                    umma::tmem_ld16_nowait(T_SC + lane_off + 64 * hv + 16 * cg, sc);
+                    const float Lt = recv[R_L + t];
+                    umma::tmem_ld_wait();
+                    if ((q & 1) && cg < 2) {
+                        // t > 31 >= s: e^{L_t - L_s} = e^{L_t - L_31} e^{L_31 - L_s}, both at most 1
+                        const float et = ex2(Lt - recv[R_L + 31]);
+                        const float2 et2 = make_float2(et, et);
+#pragma unroll
+                        for (int s4 = 0; s4 < 4; ++s4) {
+                            const float4 u4 = *reinterpret_cast<const float4 *>(recv + R_UH + 16 * cg + 4 * s4);
+                            p[2 * s4] = pack(fmul2(fmul2(make_float2(u4.x, u4.y), et2), as_float2(sc[4 * s4], sc[4 * s4 + 1])));
+                            p[2 * s4 + 1] = pack(fmul2(fmul2(make_float2(u4.z, u4.w), et2), as_float2(sc[4 * s4 + 2], sc[4 * s4 + 3])));
+                        }
+                    } else {
+#pragma unroll
+                        for (int s4 = 0; s4 < 4; ++s4) {
+                            const int s = 16 * cg + 4 * s4;
+                            const float4 l4 = *reinterpret_cast<const float4 *>(recv + R_L + s);
+                            const float4 u4 = *reinterpret_cast<const float4 *>(recv + R_U + s);
+                            float2 w0 = fmul2(as_float2(sc[4 * s4], sc[4 * s4 + 1]), make_float2(u4.x, u4.y));
+                            float2 w1 = fmul2(as_float2(sc[4 * s4 + 2], sc[4 * s4 + 3]), make_float2(u4.z, u4.w));
+                            w0 = fmul2(w0, make_float2(ex2(Lt - l4.x), ex2(Lt - l4.y)));
+                            w1 = fmul2(w1, make_float2(ex2(Lt - l4.z), ex2(Lt - l4.w)));
+                            p[2 * s4] = pack(make_float2(s > t ? 0.f : w0.x, s + 1 > t ? 0.f : w0.y));
+                            p[2 * s4 + 1] = pack(make_float2(s + 2 > t ? 0.f : w1.x, s + 3 > t ? 0.f : w1.y));
+                        }
+                    }
+                }
+                umma::tmem_st8(T_SC + lane_off + (hv ? 0 : 64) + 8 * cg, p);
+                umma::tmem_st_wait();
+            } else {
+                umma::fence_proxy_async_smem();
+            }
+            umma::tc_fence_before();
+            meet();   // ready
+            // ---- while the products run: x of the next chunk
+            if (c + 1 < chunks) {
+                convolve(c + 1);
+                if (c + 2 < chunks) fetch(c + 2);
+            }
+            // ---- state
+            wait(bar_u, ph);
+            umma::tc_fence_after();
+            {
+                const float *rs = cg < 2 ? rec0 : rec1;
+                const float dec = rs[R_DEC], add = rs[R_UMAX] * (cg < 2 ? xinv0 : xinv1);
+                const float2 dec2 = make_float2(dec, dec), add2 = make_float2(add, add);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t v[16];
+                    umma::tmem_ld16_nowait(T_U + lane_off + sc0 + 16 * i, v);
+                    umma::tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        S[8 * i + j] = ffma2(dec2, S[8 * i + j], fmul2(add2, as_float2(v[2 * j], v[2 * j + 1])));
+                }
+                if (STATE_ONLY) { decay0 *= rec0[R_DEC]; decay1 *= rec1[R_DEC]; }
+            }
+            if (!STATE_ONLY) {
+                // ---- output: token t of half hv, columns oc .. + 15; a whole chunk leaves by TMA
+                // from the z tile, a ragged one directly
+                const int t0 = begin + (c_lo + c) * Q, len = min(Q, end - t0);
+                const float fx = hv ? xinv1 : xinv0;
+                const float fi = recv[R_YI + t] * sinv, fw = recv[R_YW + t] * fx, fd = dskip * fx;
+                const float2 fi2 = make_float2(fi, fi), fw2 = make_float2(fw, fw), fd2 = make_float2(fd, fd);
+                bf16 *const o = a.out + (long long)(t0 + t) * (a.H * a.P) + xcol + oc;
+                const uint32_t p_z = p_o + (Sm::OFF_Z - Sm::OFF_X) + b * 16384;
+                if (a.z) wait(full_z + b, ph_full);
+                wait(bar_y, ph);
+                umma::tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    uint32_t yi[8], yw[8];
+                    tmem_ld8_nowait(T_YI + lane_off + oc + 8 * k, yi);
+                    tmem_ld8_nowait(T_YW + lane_off + oc + 8 * k, yw);
+                    const uint4 xx = lds128(p_o ^ (16 * k));
+                    const uint4 zz = a.z ? lds128(p_z ^ (16 * k)) : make_uint4(0, 0, 0, 0);
+                    const uint32_t xw[4] = {xx.x, xx.y, xx.z, xx.w}, zw[4] = {zz.x, zz.y, zz.z, zz.w};
+                    umma::tmem_ld_wait();
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float2 y = fmul2(half2_float2(xw[e]), fd2);
+                        y = ffma2(as_float2(yw[2 * e], yw[2 * e + 1]), fw2, y);
+                        y = ffma2(as_float2(yi[2 * e], yi[2 * e + 1]), fi2, y);
+                        if (a.z) y = fmul2(y, silu2(make_float2(bf16lo(zw[e]), bf16hi(zw[e]))));
+                        const __nv_bfloat162 pb = __floats2bfloat162_rn(y.x, y.y);
+                        w[e] = *reinterpret_cast<const uint32_t *>(&pb);
+                    }
+                    const uint4 w4 = make_uint4(w[0], w[1], w[2], w[3]);
+                    if (len == Q) sts128(p_z ^ (16 * k), w4);
+                    else if (t < len && (hv == 0 || live1)) reinterpret_cast<uint4 *>(o)[k] = w4;
+                }
+                umma::tc_fence_before();
+                umma::fence_proxy_async_smem();
+            }
+        }
+        if (!STATE_ONLY && chunks > 0) meet();
+        float *const to = !owner || *abort_flag         ? nullptr
+                          : STATE_ONLY                  ? seg_ptr(seg)
+                          : seg == last_seg && a.S_final ? a.S_final + sbase
+                                                         : nullptr;
+        if (to) {
+#pragma unroll
+            for (int j = 0; j < 16; j += 2)
+                *reinterpret_cast<float4 *>(to + 2 * j) = make_float4(S[j].x, S[j].y, S[j + 1].x, S[j + 1].y);
+            if (STATE_ONLY && lane == 0 && q == 0 && (cg & 1) == 0)
                 a.seg_decay[(seg_base + seg) * 2 + (cg >> 1)] = cg < 2 ? decay0 : decay1;
-        } else if (seg == last_seg && a.S_final) {
-            store_state(a.S_final + sbase);
         }
     }
     umma::tc_fence_before();
     __syncthreads();
-    if (*abort_flag && tid == 0)   // copies in flight land before the CTA leaves (bounded)
-        for (int b = 0; b < 2 && b < chunks; ++b) {
-            umma::mbar_wait_bounded(full + b, (uint32_t)((chunks - 1 - b) / 2) & 1u, 1u << 16);
-            if (!STATE_ONLY && a.z) umma::mbar_wait_bounded(full_z + b, (uint32_t)((chunks - 1 - b) / 2) & 1u, 1u << 16);
-        }
-    if (warp == 0) umma::tmem_dealloc(tb, 512);
+    if (warp == MMA_WARP) umma::tmem_dealloc(tb, 512);
 }
 
 namespace {
