@@ -120,11 +120,8 @@ __device__ __forceinline__ uint4 lds128(uint32_t p) {
     return v;
 }
 
-// 32 lanes x 8 columns of tensor memory; valid after tmem_ld_wait().
-__device__ __forceinline__ void tmem_ld8_nowait(uint32_t taddr, uint32_t (&r)[8]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr));
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(umma::smem_u32(bar)) : "memory");
 }
 
 template <int R> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
@@ -336,8 +333,8 @@ template <int N> struct Smem {
     static constexpr int OFF_Z = OFF_S + 2 * N * 128;  // [2 stages]: z, then out in its place, 64 rows x 128 columns
     static constexpr int OFF_REC = OFF_Z + 2 * 16384;  // [2 stages][2 halves][REC]
     static constexpr int OFF_CW = OFF_REC + 4 * REC * 4;  // conv weights [5][128]
-    static constexpr int OFF_MAX = OFF_CW + 5 * 128 * 4;  // bits of the largest |.|, [2 chunks][x, x, state, state]
-    static constexpr int OFF_BAR = OFF_MAX + 8 * 4;
+    static constexpr int OFF_MAX = OFF_CW + 5 * 128 * 4;  // bits of the largest |.|, [3 chunks][x, x, state, state]
+    static constexpr int OFF_BAR = OFF_MAX + 12 * 4;
     static constexpr int SIZE = OFF_BAR + 128 + 1024;     // barriers, TMEM slot, abort flag; alignment slack
 };
 static_assert(Smem<128>::SIZE <= 232448, "227 KB per block");
@@ -354,7 +351,8 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
     uint8_t *sm = umma::align_smem<1024>(smem_raw);
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + Sm::OFF_BAR);
     uint64_t *bar_sc = full + 2, *bar_u = full + 3, *bar_y = full + 4, *full_z = full + 5;
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(full + 7);
+    uint64_t *bar_x = full + 7, *bar_w = full + 8;   // the computing warps' operands, and decayed scores, are there
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(full + 9);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tslot + 1);
     float *cw = reinterpret_cast<float *>(sm + Sm::OFF_CW);
     uint32_t *mx = reinterpret_cast<uint32_t *>(sm + Sm::OFF_MAX);
@@ -396,11 +394,11 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
 
     if (warp == MMA_WARP) umma::tmem_alloc(tslot, 512);
     if (tid == 0) {
-        for (int i = 0; i < 7; ++i) umma::mbar_init(full + i, 1);
+        for (int i = 0; i < 9; ++i) umma::mbar_init(full + i, i < 7 ? 1 : CWARPS);
         *abort_flag = 0;
         umma::fence_mbar_init();
     }
-    if (tid < 8) mx[tid] = 0;
+    if (tid < 12) mx[tid] = 0;
     for (int i = tid; i < 5 * 128; i += THREADS) {
         const int j = i >> 7, c = i & 127;
         const bool in = c < 64 || live1;
@@ -426,9 +424,8 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
         *abort_flag = 1;
         atomicOr(&g_ssm_err, 1u);
     };
-    // Two barriers a chunk, of the computing warps and the two that serve them: "drained",
-    // after which the previous chunk is done with shared and tensor memory, and "ready",
-    // after which this chunk's operands are there.
+    // Once a chunk the computing warps and the two that serve them meet: the previous chunk
+    // is done with shared and tensor memory.
     auto meet = [] { umma::named_bar_sync(1, 32 * (CWARPS + 2)); };
 
     if (!computes) {
@@ -463,7 +460,8 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
             for (int c = 0; c < chunks; ++c) {
                 const uint32_t st = (uint32_t)((c & 1) * (Sm::TILE >> 4));
                 meet();
-                meet();
+                wait(bar_x, (uint32_t)c & 1u);
+                __syncwarp();
                 umma::tc_fence_after();
                 if (elect_one()) {
                     constexpr uint32_t idu = umma::idesc_f16(128, 128, true, true);
@@ -480,22 +478,32 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
                         constexpr uint32_t id = umma::idesc_f16(128, 64, false, true);
                         const uint64_t dt = d_tile + st;
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
+                        for (int j = 0; j < 2; ++j)
 #pragma unroll
                             for (int k = 0; k < KS; ++k) {
                                 const uint32_t kb = ((k / 4) * KB + (k % 4) * 32) >> 4;
                                 umma::mma_f16(T_YI + 64 * j, dt + (kb + (j ? 0 : OFF_C >> 4)),
                                               d_s + ((j * (N * 128) + k * 2048) >> 4), id, k > 0);
                             }
-#pragma unroll
-                            for (int k = 0; k < Q / 16; ++k)   // rows 64 j .. of the decayed scores, columns of half j
-                                umma::mma_f16_ts(T_YW + 64 * j, T_SC + (j ? 0 : 64) + 8 * k,
-                                                 d_x + ((j * 8192 + k * 2048) >> 4), id, k > 0);
-                        }
-                        umma::mma_commit(bar_y);
                     }
                 }
                 __syncwarp();
+                if (!STATE_ONLY) {
+                    wait(bar_w, (uint32_t)c & 1u);
+                    __syncwarp();
+                    umma::tc_fence_after();
+                    if (elect_one()) {
+                        constexpr uint32_t id = umma::idesc_f16(128, 64, false, true);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)   // rows 64 j .. of the decayed scores, columns of half j
+#pragma unroll
+                            for (int k = 0; k < Q / 16; ++k)
+                                umma::mma_f16_ts(T_YW + 64 * j, T_SC + (j ? 0 : 64) + 8 * k,
+                                                 d_x + ((j * 8192 + k * 2048) >> 4), id, k > 0);
+                        umma::mma_commit(bar_y);
+                    }
+                    __syncwarp();
+                }
                 if (!STATE_ONLY && c + 1 < chunks) {
                     wait(bar_y, (uint32_t)c & 1u);   // the decayed scores are used up
                     umma::tc_fence_after();
@@ -552,7 +560,6 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
                     }
                 }
                 __syncwarp();
-                meet();
             }
             if (!STATE_ONLY && chunks > 0) {
                 meet();
@@ -618,9 +625,9 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
             }
         };
         // convolution and activation of the fetched tokens of chunk c, and the largest |x| of
-        // each half into mx[c & 1][half]
+        // each half into m3[half]
         float2 xh[4][2];
-        auto convolve = [&](int c) {
+        auto convolve = [&](int c, uint32_t *m3) {
             const int len = min(Q, end - (begin + (c_lo + c) * Q));
             float2 w[5][2], f[7][2];
 #pragma unroll
@@ -650,7 +657,7 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
             }
 #pragma unroll
             for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            if ((lane & 15) == 0) atomicMax(mx + (c & 1) * 4 + half, __float_as_uint(m));
+            if ((lane & 15) == 0) atomicMax(m3 + half, __float_as_uint(m));
         };
 
         const float dskip = !STATE_ONLY && a.D ? __ldg(a.D + (q < 2 ? head0 : head1)) : 0.f;
@@ -665,9 +672,12 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
 
         if (chunks > 0) {
             fetch(0);
-            convolve(0);
+            convolve(0, mx);
             if (chunks > 1) fetch(1);
         }
+        // maxima of this chunk, of the next (written from its convolution on) and of the one
+        // after (cleared now; its last readers, of the previous chunk, have met since)
+        uint32_t *m_now = mx, *m_next = mx + 4, *m_after = mx + 8;
         for (int c = 0; c < chunks; ++c) {
             const int b = c & 1;
             const uint32_t ph = (uint32_t)c & 1u, ph_full = (uint32_t)(c >> 1) & 1u;
@@ -678,13 +688,13 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) ms = amax2(ms, S[j]);
                 const uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(ms));
-                if (lane == 0) atomicMax(mx + b * 4 + 2 + (cg >> 1), mb);
+                if (lane == 0) atomicMax(m_now + 2 + (cg >> 1), mb);
             }
             meet();   // drained
-            if (tid < 4) mx[(b ^ 1) * 4 + tid] = 0;   // chunk c - 1's, for chunk c + 1, whose x is added when this one is ready
+            if (tid < 4) m_after[tid] = 0;
 
             // ---- scales; operands into shared memory
-            const uint4 mxv = *reinterpret_cast<const uint4 *>(mx + b * 4);
+            const uint4 mxv = *reinterpret_cast<const uint4 *>(m_now);
             float xs0, xs1, xinv0, xinv1;
             scale_pow2(mxv.x, 13, xs0, xinv0);
             scale_pow2(mxv.y, 13, xs1, xinv1);
@@ -726,6 +736,9 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
                                                           pack(fmul2(S[4 * j + 2], ss2)), pack(fmul2(S[4 * j + 3], ss2))));
                 }
                 umma::fence_proxy_async_smem();
+                umma::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_x);
                 // ---- decayed scores: 16 of them per thread, as the A operand in tensor memory.
                 // Half 0 (lanes 0..63) writes columns 64 .. 95 and half 1 columns 0 .. 31, where
                 // the other half's scores lie in lanes that nobody reads.
@@ -764,16 +777,17 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
                 }
                 umma::tmem_st8(T_SC + lane_off + (hv ? 0 : 64) + 8 * cg, p);
                 umma::tmem_st_wait();
+                umma::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_w);
             } else {
                 umma::fence_proxy_async_smem();
+                umma::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_x);
             }
-            umma::tc_fence_before();
-            meet();   // ready
             // ---- while the products run: x of the next chunk
-            if (c + 1 < chunks) {
-                convolve(c + 1);
-                if (c + 2 < chunks) fetch(c + 2);
-            }
+            if (c + 1 < chunks) convolve(c + 1, m_next);
             // ---- state
             wait(bar_u, ph);
             umma::tc_fence_after();
@@ -781,15 +795,11 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
                 const float *rs = cg < 2 ? rec0 : rec1;
                 const float dec = rs[R_DEC], add = rs[R_UMAX] * (cg < 2 ? xinv0 : xinv1);
                 const float2 dec2 = make_float2(dec, dec), add2 = make_float2(add, add);
+                uint32_t v[32];
+                umma::tmem_ld32_nowait(T_U + lane_off + sc0, v);
+                umma::tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    uint32_t v[16];
-                    umma::tmem_ld16_nowait(T_U + lane_off + sc0 + 16 * i, v);
-                    umma::tmem_ld_wait();
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        S[8 * i + j] = ffma2(dec2, S[8 * i + j], fmul2(add2, as_float2(v[2 * j], v[2 * j + 1])));
-                }
+                for (int j = 0; j < 16; ++j) S[j] = ffma2(dec2, S[j], fmul2(add2, as_float2(v[2 * j], v[2 * j + 1])));
                 if (STATE_ONLY) { decay0 *= rec0[R_DEC]; decay1 *= rec1[R_DEC]; }
             }
             if (!STATE_ONLY) {
@@ -804,23 +814,35 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
                 if (a.z) wait(full_z + b, ph_full);
                 wait(bar_y, ph);
                 umma::tc_fence_after();
+                wait(bar_w, ph);   // x of the other warps, too
+                float2 y[8];
+                {
+                    uint32_t yi[16], yw[16];
+                    umma::tmem_ld16_nowait(T_YI + lane_off + oc, yi);
+                    umma::tmem_ld16_nowait(T_YW + lane_off + oc, yw);
+                    umma::tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        y[e] = ffma2(as_float2(yi[2 * e], yi[2 * e + 1]), fi2,
+                                     fmul2(as_float2(yw[2 * e], yw[2 * e + 1]), fw2));
+                }
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    uint32_t yi[8], yw[8];
-                    tmem_ld8_nowait(T_YI + lane_off + oc + 8 * k, yi);
-                    tmem_ld8_nowait(T_YW + lane_off + oc + 8 * k, yw);
                     const uint4 xx = lds128(p_o ^ (16 * k));
-                    const uint4 zz = a.z ? lds128(p_z ^ (16 * k)) : make_uint4(0, 0, 0, 0);
-                    const uint32_t xw[4] = {xx.x, xx.y, xx.z, xx.w}, zw[4] = {zz.x, zz.y, zz.z, zz.w};
-                    umma::tmem_ld_wait();
+                    const uint32_t xw[4] = {xx.x, xx.y, xx.z, xx.w};
                     uint32_t w[4];
 #pragma unroll
+                    for (int e = 0; e < 4; ++e) y[4 * k + e] = ffma2(half2_float2(xw[e]), fd2, y[4 * k + e]);
+                    if (a.z) {
+                        const uint4 zz = lds128(p_z ^ (16 * k));
+                        const uint32_t zw[4] = {zz.x, zz.y, zz.z, zz.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            y[4 * k + e] = fmul2(y[4 * k + e], silu2(make_float2(bf16lo(zw[e]), bf16hi(zw[e]))));
+                    }
+#pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float2 y = fmul2(half2_float2(xw[e]), fd2);
-                        y = ffma2(as_float2(yw[2 * e], yw[2 * e + 1]), fw2, y);
-                        y = ffma2(as_float2(yi[2 * e], yi[2 * e + 1]), fi2, y);
-                        if (a.z) y = fmul2(y, silu2(make_float2(bf16lo(zw[e]), bf16hi(zw[e]))));
-                        const __nv_bfloat162 pb = __floats2bfloat162_rn(y.x, y.y);
+                        const __nv_bfloat162 pb = __floats2bfloat162_rn(y[4 * k + e].x, y[4 * k + e].y);
                         w[e] = *reinterpret_cast<const uint32_t *>(&pb);
                     }
                     const uint4 w4 = make_uint4(w[0], w[1], w[2], w[3]);
@@ -830,6 +852,11 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
                 umma::tc_fence_before();
                 umma::fence_proxy_async_smem();
             }
+            if (c + 2 < chunks) fetch(c + 2);   // last, so that it holds no registers meanwhile
+            uint32_t *const done = m_now;
+            m_now = m_next;
+            m_next = m_after;
+            m_after = done;
         }
         if (!STATE_ONLY && chunks > 0) meet();
         float *const to = !owner || *abort_flag         ? nullptr
