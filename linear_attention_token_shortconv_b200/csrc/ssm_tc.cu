@@ -97,6 +97,10 @@ __device__ __forceinline__ float2 half2_float2(uint32_t h) {
 __device__ __forceinline__ float2 as_float2(uint32_t a, uint32_t b) {
     return make_float2(__uint_as_float(a), __uint_as_float(b));
 }
+__device__ __forceinline__ uint32_t pack_bf16(float2 v) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
+    return *reinterpret_cast<const uint32_t *>(&b);
+}
 __device__ __forceinline__ uint32_t pack(float2 v) { return umma::pack_half2(v.x, v.y); }
 __device__ __forceinline__ float amax2(float m, float2 v) { return fmaxf(m, fmaxf(fabsf(v.x), fabsf(v.y))); }
 
@@ -543,27 +547,29 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
             if (one && chunks > 0) {
                 issue(0);
                 if (!STATE_ONLY && a.z) issue_z(0);
-                if (chunks > 1) issue(1);
+                if (chunks > 1) {
+                    issue(1);
+                    if (!STATE_ONLY && a.z) issue_z(1);
+                }
             }
             for (int c = 0; c < chunks; ++c) {
                 meet();
                 if (one) {
                     const bool go = *abort_flag == 0;
                     if (c >= 1 && c + 1 < chunks && go) issue(c + 1);
-                    if (!STATE_ONLY) {
-                        // out of chunk c - 1 leaves; its tile then takes z of chunk c + 1
-                        if (c >= 1) {
-                            store_out(c - 1);
-                            umma::bulk_wait_read<0>();
-                        }
-                        if (a.z && c + 1 < chunks && go) issue_z(c + 1);
+                    if (!STATE_ONLY && c >= 2) {
+                        // out of chunk c - 2, gated before this meeting, leaves; its tile takes z of chunk c
+                        store_out(c - 2);
+                        umma::bulk_wait_read<0>();
+                        if (a.z && go) issue_z(c);
                     }
                 }
                 __syncwarp();
             }
             if (!STATE_ONLY && chunks > 0) {
                 meet();
-                if (one) {   // the last chunk's tile, if it is whole; the copies end before the CTA does
+                if (one) {   // the last two tiles (the last only if it is whole); the copies end before the CTA does
+                    if (chunks > 1) store_out(chunks - 2);
                     if (begin + (c_lo + chunks) * Q <= end) store_out(chunks - 1);
                     umma::bulk_wait_all();
                 }
@@ -673,8 +679,47 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
         if (chunks > 0) {
             fetch(0);
             convolve(0, mx);
-            if (chunks > 1) fetch(1);
         }
+        auto state_max = [&](uint32_t *m3) {
+            float ms = 0.f;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) ms = amax2(ms, S[j]);
+            const uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(ms));
+            if (lane == 0) atomicMax(m3 + 2 + (cg >> 1), mb);
+        };
+        if (!STATE_ONLY) state_max(mx);
+        // y of this thread (token t of half hv, columns oc .. + 15) of chunk c through the gate:
+        // a whole chunk into the tile that z came in, from where it leaves by TMA, a ragged one
+        // straight out
+        float2 y[8];
+        auto gate = [&](int c) {
+            const int t0 = begin + (c_lo + c) * Q, len = min(Q, end - t0);
+            const uint32_t p_z = p_o + (Sm::OFF_Z - Sm::OFF_X) + (c & 1) * 16384;
+            if (a.z) {
+                wait(full_z + (c & 1), (uint32_t)(c >> 1) & 1u);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint4 zz = lds128(p_z ^ (16 * k));
+                    const uint32_t zw[4] = {zz.x, zz.y, zz.z, zz.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        y[4 * k + e] = fmul2(y[4 * k + e], silu2(make_float2(bf16lo(zw[e]), bf16hi(zw[e]))));
+                }
+            }
+            uint4 w[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                w[k] = make_uint4(pack_bf16(y[4 * k]), pack_bf16(y[4 * k + 1]), pack_bf16(y[4 * k + 2]), pack_bf16(y[4 * k + 3]));
+            if (len == Q) {
+                sts128(p_z, w[0]);
+                sts128(p_z ^ 16, w[1]);
+                umma::fence_proxy_async_smem();
+            } else if (t < len && (hv == 0 || live1)) {
+                uint4 *o = reinterpret_cast<uint4 *>(a.out + (long long)(t0 + t) * (a.H * a.P) + xcol + oc);
+                o[0] = w[0];
+                o[1] = w[1];
+            }
+        };
         // maxima of this chunk, of the next (written from its convolution on) and of the one
         // after (cleared now; its last readers, of the previous chunk, have met since)
         uint32_t *m_now = mx, *m_next = mx + 4, *m_after = mx + 8;
@@ -683,14 +728,7 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
             const uint32_t ph = (uint32_t)c & 1u, ph_full = (uint32_t)(c >> 1) & 1u;
             const float *rec0 = reinterpret_cast<const float *>(sm + Sm::OFF_REC) + b * 2 * REC, *rec1 = rec0 + REC;
             const float *recv = hv ? rec1 : rec0;
-            if (!STATE_ONLY) {
-                float ms = 0.f;
-#pragma unroll
-                for (int j = 0; j < 16; ++j) ms = amax2(ms, S[j]);
-                const uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(ms));
-                if (lane == 0) atomicMax(m_now + 2 + (cg >> 1), mb);
-            }
-            meet();   // drained
+            meet();
             if (tid < 4) m_after[tid] = 0;
 
             // ---- scales; operands into shared memory
@@ -739,7 +777,11 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
                 umma::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar_x);
-                // ---- decayed scores: 16 of them per thread, as the A operand in tensor memory.
+                // ---- under the products: the previous chunk's gate, this one's decayed scores,
+                // the next one's x
+                if (c + 1 < chunks) fetch(c + 1);
+                if (c > 0) gate(c - 1);
+                // decayed scores: 16 of them per thread, as the A operand in tensor memory.
                 // Half 0 (lanes 0..63) writes columns 64 .. 95 and half 1 columns 0 .. 31, where
                 // the other half's scores lie in lanes that nobody reads.
                 wait(bar_sc, ph);
@@ -785,8 +827,8 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
                 umma::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar_x);
+                if (c + 1 < chunks) fetch(c + 1);
             }
-            // ---- while the products run: x of the next chunk
             if (c + 1 < chunks) convolve(c + 1, m_next);
             // ---- state
             wait(bar_u, ph);
@@ -803,62 +845,37 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
                 if (STATE_ONLY) { decay0 *= rec0[R_DEC]; decay1 *= rec1[R_DEC]; }
             }
             if (!STATE_ONLY) {
-                // ---- output: token t of half hv, columns oc .. + 15; a whole chunk leaves by TMA
-                // from the z tile, a ragged one directly
-                const int t0 = begin + (c_lo + c) * Q, len = min(Q, end - t0);
+                state_max(m_next);
+                // ---- y before its gate
                 const float fx = hv ? xinv1 : xinv0;
                 const float fi = recv[R_YI + t] * sinv, fw = recv[R_YW + t] * fx, fd = dskip * fx;
                 const float2 fi2 = make_float2(fi, fi), fw2 = make_float2(fw, fw), fd2 = make_float2(fd, fd);
-                bf16 *const o = a.out + (long long)(t0 + t) * (a.H * a.P) + xcol + oc;
-                const uint32_t p_z = p_o + (Sm::OFF_Z - Sm::OFF_X) + b * 16384;
-                if (a.z) wait(full_z + b, ph_full);
+                wait(bar_w, ph);   // x of the other warps
+                const uint4 xa = lds128(p_o), xb = lds128(p_o ^ 16);
+                const uint32_t xw[8] = {xa.x, xa.y, xa.z, xa.w, xb.x, xb.y, xb.z, xb.w};
                 wait(bar_y, ph);
                 umma::tc_fence_after();
-                wait(bar_w, ph);   // x of the other warps, too
-                float2 y[8];
-                {
-                    uint32_t yi[16], yw[16];
-                    umma::tmem_ld16_nowait(T_YI + lane_off + oc, yi);
-                    umma::tmem_ld16_nowait(T_YW + lane_off + oc, yw);
-                    umma::tmem_ld_wait();
+                uint32_t yi[16], yw[16];
+                umma::tmem_ld16_nowait(T_YI + lane_off + oc, yi);
+                umma::tmem_ld16_nowait(T_YW + lane_off + oc, yw);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        y[e] = ffma2(as_float2(yi[2 * e], yi[2 * e + 1]), fi2,
-                                     fmul2(as_float2(yw[2 * e], yw[2 * e + 1]), fw2));
-                }
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint4 xx = lds128(p_o ^ (16 * k));
-                    const uint32_t xw[4] = {xx.x, xx.y, xx.z, xx.w};
-                    uint32_t w[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) y[4 * k + e] = ffma2(half2_float2(xw[e]), fd2, y[4 * k + e]);
-                    if (a.z) {
-                        const uint4 zz = lds128(p_z ^ (16 * k));
-                        const uint32_t zw[4] = {zz.x, zz.y, zz.z, zz.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            y[4 * k + e] = fmul2(y[4 * k + e], silu2(make_float2(bf16lo(zw[e]), bf16hi(zw[e]))));
-                    }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const __nv_bfloat162 pb = __floats2bfloat162_rn(y[4 * k + e].x, y[4 * k + e].y);
-                        w[e] = *reinterpret_cast<const uint32_t *>(&pb);
-                    }
-                    const uint4 w4 = make_uint4(w[0], w[1], w[2], w[3]);
-                    if (len == Q) sts128(p_z ^ (16 * k), w4);
-                    else if (t < len && (hv == 0 || live1)) reinterpret_cast<uint4 *>(o)[k] = w4;
-                }
+                for (int e = 0; e < 8; ++e) y[e] = fmul2(half2_float2(xw[e]), fd2);
+                umma::tmem_ld_wait();
                 umma::tc_fence_before();
-                umma::fence_proxy_async_smem();
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    y[e] = ffma2(as_float2(yi[2 * e], yi[2 * e + 1]), fi2,
+                                 ffma2(as_float2(yw[2 * e], yw[2 * e + 1]), fw2, y[e]));
             }
-            if (c + 2 < chunks) fetch(c + 2);   // last, so that it holds no registers meanwhile
             uint32_t *const done = m_now;
             m_now = m_next;
             m_next = m_after;
             m_after = done;
         }
-        if (!STATE_ONLY && chunks > 0) meet();
+        if (!STATE_ONLY && chunks > 0) {
+            gate(chunks - 1);
+            meet();
+        }
         float *const to = !owner || *abort_flag         ? nullptr
                           : STATE_ONLY                  ? seg_ptr(seg)
                           : seg == last_seg && a.S_final ? a.S_final + sbase
