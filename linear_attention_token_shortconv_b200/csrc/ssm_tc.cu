@@ -44,10 +44,7 @@ constexpr uint32_t MAX_POLLS = 1u << 24;
 // move between groups of four warps, 16 x 104 + 4 x 64 of the 20 x 96 at launch)
 constexpr int CWARPS = 16, MMA_WARP = 16, COPY_WARP = 17, THREADS = 32 * 20;
 constexpr int COMPUTE_REGS = 104, SERVE_REGS = 64;
-// one 64-column block of a tile: B hi | C | B lo, each 64 rows of 128 bytes.  In this
-// order C is followed by B lo and preceded by B hi, so an M = 128 operand that starts
-// at C (or at B hi) has the chunk's C in its rows 0..63 (or 64..127); the other rows
-// are finite values whose products nobody reads.
+// one 64-column block of a tile: B hi | C | B lo, each 64 rows of 128 bytes
 constexpr int KB = 24576;
 constexpr int OFF_C = 8192, OFF_LO = 16384;
 }  // namespace stc
@@ -152,7 +149,7 @@ struct PrepArgs {
 
 // One CTA per (slot, group).
 template <int N>
-__global__ void __launch_bounds__(stc::PREP_THREADS) ssm_prep_kernel(const PrepArgs a) {
+__global__ void __launch_bounds__(stc::PREP_THREADS, 2) ssm_prep_kernel(const PrepArgs a) {
     using namespace stc;
     __shared__ float eb[Q], ec[Q];        // inverse scales of the rows of B and C
     __shared__ float dts[Q][33];
@@ -171,72 +168,84 @@ __global__ void __launch_bounds__(stc::PREP_THREADS) ssm_prep_kernel(const PrepA
     const int len = min(Q, end - t0);
     const int gn = a.G * N, chans = a.hp + 2 * gn;
 
-    // ---- B and C: 8 channels x 8 consecutive tokens per thread; a row of B (or C) lies
-    // in N / 8 neighbouring lanes
-    constexpr int VEC = N / 8;                    // lanes of a row
+    // ---- B and C: 4 channels x RUN consecutive tokens per thread; a row of B (or C) lies in
+    // N / 4 neighbouring lanes.  Few registers, so that two CTAs hide each other's latency.
+    constexpr int VEC = N / 4;                    // lanes of a row
     constexpr int LANES = 2 * VEC;                // threads across B | C
-    constexpr int RUN = Q / (PREP_THREADS / LANES);        // tokens of a thread
+    constexpr int RUN = Q / (PREP_THREADS / LANES);   // tokens of a thread
     {
-        const int v = tid % LANES, isC = v / VEC, c = (v % VEC) * 8;
+        const int v = tid % LANES, isC = v / VEC, c = (v % VEC) * 4;
         const int r0 = (tid / LANES) * RUN;
         const int ch = a.hp + isC * gn + g * N + c;
         const bf16 *src = (isC ? a.C : a.B) + g * N + c;
         const long long ld = isC ? a.ld_C : a.ld_B;
-        float w[8][4], bias[8];
+        float2 w[4][2], bias[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};   // [tap][channel pair]
+        {
+            float4 w4[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float4 w4 = __ldg(reinterpret_cast<const float4 *>(a.conv_w) + ch + e);
-            w[e][0] = w4.x; w[e][1] = w4.y; w[e][2] = w4.z; w[e][3] = w4.w;
-            bias[e] = a.conv_b ? __ldg(a.conv_b + ch + e) : 0.f;
-        }
-        float win[4][8];
-        auto row = [&](int t, float (&x)[8]) {
-            if (t >= begin && t < end) load8(src + t * ld, x);
-            else if (t < begin && a.hist) load8(a.hist + ((size_t)lo * 3 + (t - begin + 3)) * chans + ch, x);
-            else {
+            for (int e = 0; e < 4; ++e) w4[e] = __ldg(reinterpret_cast<const float4 *>(a.conv_w) + ch + e);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = 0.f;
+            for (int e = 0; e < 2; ++e) {
+                w[0][e] = make_float2(w4[2 * e].x, w4[2 * e + 1].x);
+                w[1][e] = make_float2(w4[2 * e].y, w4[2 * e + 1].y);
+                w[2][e] = make_float2(w4[2 * e].z, w4[2 * e + 1].z);
+                w[3][e] = make_float2(w4[2 * e].w, w4[2 * e + 1].w);
             }
+            if (a.conv_b) {
+                const float4 b4 = __ldg(reinterpret_cast<const float4 *>(a.conv_b + ch));
+                bias[0] = make_float2(b4.x, b4.y);
+                bias[1] = make_float2(b4.z, b4.w);
+            }
+        }
+        auto row = [&](int t) -> uint2 {
+            if (t >= begin && t < end) return __ldg(reinterpret_cast<const uint2 *>(src + t * ld));
+            if (t < begin && a.hist)
+                return __ldg(reinterpret_cast<const uint2 *>(a.hist + ((size_t)lo * 3 + (t - begin + 3)) * chans + ch));
+            return make_uint2(0, 0);
         };
+        uint2 raw[RUN + 3];
 #pragma unroll
-        for (int j = 0; j < 3; ++j) row(t0 + r0 - 3 + j, win[j]);
-        uint8_t *tile = a.tiles + ((size_t)slot * a.G + g) * (N / 64) * KB + (c / 64) * KB;
+        for (int j = 0; j < RUN + 3; ++j) raw[j] = row(t0 + r0 - 3 + j);
+        uint8_t *tile = a.tiles + ((size_t)slot * a.G + g) * (N / 64) * KB + (c / 64) * KB + (isC ? OFF_C : 0);
+        const uint32_t sub = 8 * ((c / 4) & 1);
 #pragma unroll
         for (int i = 0; i < RUN; ++i) {
             const int r = r0 + i;
-            row(t0 + r, win[(3 + i) & 3]);
-            float x[8];
-            uint32_t m = 0;
+            float2 x[2];
+            float mf = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-                float s[2] = {bias[e], bias[e + 1]};
+            for (int e = 0; e < 2; ++e) {
+                float2 s = bias[e];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    s[0] = fmaf(w[e][j], win[(i + j) & 3][e], s[0]);
-                    s[1] = fmaf(w[e + 1][j], win[(i + j) & 3][e + 1], s[1]);
+                    const uint32_t u = e ? raw[i + j].y : raw[i + j].x;
+                    s = ffma2(w[j][e], make_float2(bf16lo(u), bf16hi(u)), s);
                 }
-                const float2 v = silu2(make_float2(s[0], s[1]));
-                x[e] = r < len ? v.x : 0.f;
-                x[e + 1] = r < len ? v.y : 0.f;
-                m = max(m, max(__float_as_uint(x[e]) & 0x7fffffffu, __float_as_uint(x[e + 1]) & 0x7fffffffu));
+                s = silu2(s);
+                x[e] = r < len ? s : make_float2(0.f, 0.f);
+                mf = amax2(mf, x[e]);
             }
+            uint32_t m = __float_as_uint(mf);
+            if constexpr (VEC == 32) m = __reduce_max_sync(0xffffffffu, m);
+            else {
 #pragma unroll
-            for (int o = 1; o < VEC; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+                for (int o = 1; o < VEC; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+            }
             float s, inv;
             scale_pow2(m, 3, s, inv);   // |B'|, |C'| < 16: scores stay below 128 x 256
             if (v % VEC == 0) (isC ? ec : eb)[r] = inv;
-            uint32_t h[4], l[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float u0 = x[2 * e] * s, u1 = x[2 * e + 1] * s;
-                const __half2 p = __floats2half2_rn(u0, u1);
-                const float2 f = __half22float2(p);
-                h[e] = *reinterpret_cast<const uint32_t *>(&p);
-                l[e] = umma::pack_half2(u0 - f.x, u1 - f.y);
+            uint2 hi, lo2;
+            const float2 u0 = fmul2(x[0], make_float2(s, s)), u1 = fmul2(x[1], make_float2(s, s));
+            hi.x = pack(u0);
+            hi.y = pack(u1);
+            uint8_t *p = tile + umma::sw128_offset(r, (c % 64) / 8) + sub;
+            *reinterpret_cast<uint2 *>(p) = hi;
+            if (!isC) {
+                const float2 h0 = half2_float2(hi.x), h1 = half2_float2(hi.y);
+                lo2.x = umma::pack_half2(u0.x - h0.x, u0.y - h0.y);
+                lo2.y = umma::pack_half2(u1.x - h1.x, u1.y - h1.y);
+                *reinterpret_cast<uint2 *>(p + OFF_LO) = lo2;
             }
-            const int chunk = (c % 64) / 8;
-            umma::st_chunk(tile + (isC ? OFF_C : 0), r, chunk, make_uint4(h[0], h[1], h[2], h[3]));
-            if (!isC) umma::st_chunk(tile + OFF_LO, r, chunk, make_uint4(l[0], l[1], l[2], l[3]));
         }
     }
     // ---- the heads' records, one warp per head, two tokens per lane
@@ -415,7 +424,9 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
     __syncthreads();
     umma::tc_fence_after();
     const uint32_t tb = *tslot;
-    const uint32_t T_SC = tb, T_YI = tb + 128, T_YW = tb + 256, T_U = tb + 384;
+    // tensor memory: scores [64] (the decayed ones, packed, over the first 32), C packed [64],
+    // and the 128-column results: C S, decayed scores x, and the state's addition
+    const uint32_t T_SC = tb, T_C = tb + 64, T_YI = tb + 128, T_YW = tb + 256, T_U = tb + 384;
     const uint32_t sT = umma::smem_u32(sm);
 
     // A wait that expires raises the abort flag: later ones give up soon after, no more
@@ -441,30 +452,22 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
             const uint64_t d_tile = umma::sw128_desc(sT, 16, 1024);
             const uint64_t d_tile_mn = umma::sw128_desc(sT, N == 128 ? KB : 0, 1024);   // N = 64: rows 64.. repeat 0..
             const uint64_t d_x = umma::sw128_desc(sT + Sm::OFF_X, 8192, 1024);
-            const uint64_t d_s = umma::sw128_desc(sT + Sm::OFF_S, 16, 1024);
+            const uint64_t d_s = umma::sw128_desc(sT + Sm::OFF_S, N * 128, 1024);
             constexpr int KS = N / 16;   // K steps over the state dim
-            auto scores = [&](int c) {   // C in rows 64 j .. 64 j + 63
-                const uint64_t dt = d_tile + (uint32_t)((c & 1) * (Sm::TILE >> 4));
+            for (int c = 0; c < chunks; ++c) {
+                const uint32_t st = (uint32_t)((c & 1) * (Sm::TILE >> 4)), ph = (uint32_t)c & 1u;
+                meet();
+                umma::tc_fence_after();
                 wait(full + (c & 1), (uint32_t)(c >> 1) & 1u);
                 __syncwarp();
-                if (elect_one()) {
+                if (!STATE_ONLY && elect_one()) {
                     constexpr uint32_t id = umma::idesc_f16(128, 64, false, false);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int k = 0; k < KS; ++k) {
-                            const uint32_t kb = ((k / 4) * KB + (k % 4) * 32) >> 4;
-                            umma::mma_f16(T_SC + 64 * j, dt + (kb + (j ? 0 : OFF_C >> 4)), dt + kb, id, k > 0);
-                        }
+                    for (int k = 0; k < KS; ++k)   // C B^T, for either half of the rows
+                        umma::mma_f16_ts(T_SC, T_C + 8 * k, d_tile + st + (((k / 4) * KB + (k % 4) * 32) >> 4), id, k > 0);
                     umma::mma_commit(bar_sc);
                 }
-                __syncwarp();
-            };
-            if (!STATE_ONLY && chunks > 0) scores(0);
-            for (int c = 0; c < chunks; ++c) {
-                const uint32_t st = (uint32_t)((c & 1) * (Sm::TILE >> 4));
-                meet();
-                wait(bar_x, (uint32_t)c & 1u);
+                wait(bar_x, ph);
                 __syncwarp();
                 umma::tc_fence_after();
                 if (elect_one()) {
@@ -479,39 +482,25 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
                                           (p == 1 ? dxl : dxh) + ((k * 2048) >> 4), idu, p > 0 || k > 0);
                     umma::mma_commit(bar_u);
                     if (!STATE_ONLY) {
-                        constexpr uint32_t id = umma::idesc_f16(128, 64, false, true);
-                        const uint64_t dt = d_tile + st;
+                        constexpr uint32_t id = umma::idesc_f16(128, 128, false, true);
 #pragma unroll
-                        for (int j = 0; j < 2; ++j)
-#pragma unroll
-                            for (int k = 0; k < KS; ++k) {
-                                const uint32_t kb = ((k / 4) * KB + (k % 4) * 32) >> 4;
-                                umma::mma_f16(T_YI + 64 * j, dt + (kb + (j ? 0 : OFF_C >> 4)),
-                                              d_s + ((j * (N * 128) + k * 2048) >> 4), id, k > 0);
-                            }
+                        for (int k = 0; k < KS; ++k)
+                            umma::mma_f16_ts(T_YI, T_C + 8 * k, d_s + ((k * 2048) >> 4), id, k > 0);
                     }
                 }
                 __syncwarp();
                 if (!STATE_ONLY) {
-                    wait(bar_w, (uint32_t)c & 1u);
+                    wait(bar_w, ph);
                     __syncwarp();
                     umma::tc_fence_after();
                     if (elect_one()) {
-                        constexpr uint32_t id = umma::idesc_f16(128, 64, false, true);
+                        constexpr uint32_t id = umma::idesc_f16(128, 128, false, true);
 #pragma unroll
-                        for (int j = 0; j < 2; ++j)   // rows 64 j .. of the decayed scores, columns of half j
-#pragma unroll
-                            for (int k = 0; k < Q / 16; ++k)
-                                umma::mma_f16_ts(T_YW + 64 * j, T_SC + (j ? 0 : 64) + 8 * k,
-                                                 d_x + ((j * 8192 + k * 2048) >> 4), id, k > 0);
+                        for (int k = 0; k < Q / 16; ++k)   // a half's rows against both halves' columns: its own are read
+                            umma::mma_f16_ts(T_YW, T_SC + 8 * k, d_x + ((k * 2048) >> 4), id, k > 0);
                         umma::mma_commit(bar_y);
                     }
                     __syncwarp();
-                }
-                if (!STATE_ONLY && c + 1 < chunks) {
-                    wait(bar_y, (uint32_t)c & 1u);   // the decayed scores are used up
-                    umma::tc_fence_after();
-                    scores(c + 1);
                 }
             }
         } else if (warp == COPY_WARP) {
@@ -720,6 +709,29 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
                 o[1] = w[1];
             }
         };
+        // C of chunk c, two values a column, as the A operand of both products with C: the
+        // same 64 tokens in lanes 0 .. 63 and 64 .. 127, one half's rows each
+        auto place_c = [&](int c) {
+            wait(full + (c & 1), (uint32_t)(c >> 1) & 1u);
+            const uint32_t p = sT + (c & 1) * Sm::TILE + OFF_C;
+            if constexpr (N == 128) {
+                const uint32_t r = p + (cg >> 1) * KB + umma::sw128_offset(t, (cg & 1) * 4);
+                uint32_t v[16];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint4 u = lds128(r ^ (16 * j));
+                    v[4 * j] = u.x; v[4 * j + 1] = u.y; v[4 * j + 2] = u.z; v[4 * j + 3] = u.w;
+                }
+                umma::tmem_st16(T_C + lane_off + 16 * cg, v);
+            } else {
+                const uint32_t r = p + umma::sw128_offset(t, 2 * cg);
+                const uint4 u = lds128(r), w = lds128(r ^ 16);
+                const uint32_t v[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
+                umma::tmem_st8(T_C + lane_off + 8 * cg, v);
+            }
+            umma::tmem_st_wait();
+        };
+        if (!STATE_ONLY && chunks > 0) place_c(0);
         // maxima of this chunk, of the next (written from its convolution on) and of the one
         // after (cleared now; its last readers, of the previous chunk, have met since)
         uint32_t *m_now = mx, *m_next = mx + 4, *m_after = mx + 8;
@@ -728,6 +740,7 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
             const uint32_t ph = (uint32_t)c & 1u, ph_full = (uint32_t)(c >> 1) & 1u;
             const float *rec0 = reinterpret_cast<const float *>(sm + Sm::OFF_REC) + b * 2 * REC, *rec1 = rec0 + REC;
             const float *recv = hv ? rec1 : rec0;
+            umma::tc_fence_before();
             meet();
             if (tid < 4) m_after[tid] = 0;
 
@@ -781,15 +794,13 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
                 // the next one's x
                 if (c + 1 < chunks) fetch(c + 1);
                 if (c > 0) gate(c - 1);
-                // decayed scores: 16 of them per thread, as the A operand in tensor memory.
-                // Half 0 (lanes 0..63) writes columns 64 .. 95 and half 1 columns 0 .. 31, where
-                // the other half's scores lie in lanes that nobody reads.
+                // decayed scores: 16 of them per thread, as the A operand in tensor memory
                 wait(bar_sc, ph);
                 umma::tc_fence_after();
                 uint32_t p[8] = {0, 0, 0, 0, 0, 0, 0, 0};
                 if ((q & 1) || cg < 2) {   // tokens 0 .. 31 see nothing of 32 .. 63
                     uint32_t sc[16];
-                    umma::tmem_ld16_nowait(T_SC + lane_off + 64 * hv + 16 * cg, sc);
+                    umma::tmem_ld16_nowait(T_SC + lane_off + 16 * cg, sc);
                     const float Lt = recv[R_L + t];
                     umma::tmem_ld_wait();
                     if ((q & 1) && cg < 2) {
@@ -817,7 +828,8 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
                         }
                     }
                 }
-                umma::tmem_st8(T_SC + lane_off + (hv ? 0 : 64) + 8 * cg, p);
+                umma::named_bar_sync(2 + q, 128);   // the four warps of these lanes have read their scores
+                umma::tmem_st8(T_SC + lane_off + 8 * cg, p);
                 umma::tmem_st_wait();
                 umma::tc_fence_before();
                 __syncwarp();
@@ -861,11 +873,11 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) y[e] = fmul2(half2_float2(xw[e]), fd2);
                 umma::tmem_ld_wait();
-                umma::tc_fence_before();
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     y[e] = ffma2(as_float2(yi[2 * e], yi[2 * e + 1]), fi2,
                                  ffma2(as_float2(yw[2 * e], yw[2 * e + 1]), fw2, y[e]));
+                if (c + 1 < chunks) place_c(c + 1);
             }
             uint32_t *const done = m_now;
             m_now = m_next;
