@@ -44,7 +44,10 @@ constexpr uint32_t MAX_POLLS = 1u << 24;
 // move between groups of four warps, 16 x 104 + 4 x 64 of the 20 x 96 at launch)
 constexpr int CWARPS = 16, MMA_WARP = 16, COPY_WARP = 17, THREADS = 32 * 20;
 constexpr int COMPUTE_REGS = 104, SERVE_REGS = 64;
-// one 64-column block of a tile: B hi | C | B lo, each 64 rows of 128 bytes
+// one 64-column block of a tile: B hi | C | B lo, each 64 rows of 128 bytes.  In this
+// order C is followed by B lo and preceded by B hi, so an M = 128 operand that starts
+// at C (or at B hi) has the chunk's C in its rows 0..63 (or 64..127); the other rows
+// are finite values whose products nobody reads.
 constexpr int KB = 24576;
 constexpr int OFF_C = 8192, OFF_LO = 16384;
 }  // namespace stc
@@ -424,9 +427,7 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
     __syncthreads();
     umma::tc_fence_after();
     const uint32_t tb = *tslot;
-    // tensor memory: scores [64] (the decayed ones, packed, over the first 32), C packed [64],
-    // and the 128-column results: C S, decayed scores x, and the state's addition
-    const uint32_t T_SC = tb, T_C = tb + 64, T_YI = tb + 128, T_YW = tb + 256, T_U = tb + 384;
+    const uint32_t T_SC = tb, T_YI = tb + 128, T_YW = tb + 256, T_U = tb + 384;
     const uint32_t sT = umma::smem_u32(sm);
 
     // A wait that expires raises the abort flag: later ones give up soon after, no more
@@ -452,22 +453,30 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
             const uint64_t d_tile = umma::sw128_desc(sT, 16, 1024);
             const uint64_t d_tile_mn = umma::sw128_desc(sT, N == 128 ? KB : 0, 1024);   // N = 64: rows 64.. repeat 0..
             const uint64_t d_x = umma::sw128_desc(sT + Sm::OFF_X, 8192, 1024);
-            const uint64_t d_s = umma::sw128_desc(sT + Sm::OFF_S, N * 128, 1024);
+            const uint64_t d_s = umma::sw128_desc(sT + Sm::OFF_S, 16, 1024);
             constexpr int KS = N / 16;   // K steps over the state dim
-            for (int c = 0; c < chunks; ++c) {
-                const uint32_t st = (uint32_t)((c & 1) * (Sm::TILE >> 4)), ph = (uint32_t)c & 1u;
-                meet();
-                umma::tc_fence_after();
+            auto scores = [&](int c) {   // C in rows 64 j .. 64 j + 63
+                const uint64_t dt = d_tile + (uint32_t)((c & 1) * (Sm::TILE >> 4));
                 wait(full + (c & 1), (uint32_t)(c >> 1) & 1u);
                 __syncwarp();
-                if (!STATE_ONLY && elect_one()) {
+                if (elect_one()) {
                     constexpr uint32_t id = umma::idesc_f16(128, 64, false, false);
 #pragma unroll
-                    for (int k = 0; k < KS; ++k)   // C B^T, for either half of the rows
-                        umma::mma_f16_ts(T_SC, T_C + 8 * k, d_tile + st + (((k / 4) * KB + (k % 4) * 32) >> 4), id, k > 0);
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int k = 0; k < KS; ++k) {
+                            const uint32_t kb = ((k / 4) * KB + (k % 4) * 32) >> 4;
+                            umma::mma_f16(T_SC + 64 * j, dt + (kb + (j ? 0 : OFF_C >> 4)), dt + kb, id, k > 0);
+                        }
                     umma::mma_commit(bar_sc);
                 }
-                wait(bar_x, ph);
+                __syncwarp();
+            };
+            if (!STATE_ONLY && chunks > 0) scores(0);
+            for (int c = 0; c < chunks; ++c) {
+                const uint32_t st = (uint32_t)((c & 1) * (Sm::TILE >> 4));
+                meet();
+                wait(bar_x, (uint32_t)c & 1u);
                 __syncwarp();
                 umma::tc_fence_after();
                 if (elect_one()) {
@@ -482,25 +491,39 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
                                           (p == 1 ? dxl : dxh) + ((k * 2048) >> 4), idu, p > 0 || k > 0);
                     umma::mma_commit(bar_u);
                     if (!STATE_ONLY) {
-                        constexpr uint32_t id = umma::idesc_f16(128, 128, false, true);
+                        constexpr uint32_t id = umma::idesc_f16(128, 64, false, true);
+                        const uint64_t dt = d_tile + st;
 #pragma unroll
-                        for (int k = 0; k < KS; ++k)
-                            umma::mma_f16_ts(T_YI, T_C + 8 * k, d_s + ((k * 2048) >> 4), id, k > 0);
+                        for (int j = 0; j < 2; ++j)
+#pragma unroll
+                            for (int k = 0; k < KS; ++k) {
+                                const uint32_t kb = ((k / 4) * KB + (k % 4) * 32) >> 4;
+                                umma::mma_f16(T_YI + 64 * j, dt + (kb + (j ? 0 : OFF_C >> 4)),
+                                              d_s + ((j * (N * 128) + k * 2048) >> 4), id, k > 0);
+                            }
                     }
                 }
                 __syncwarp();
                 if (!STATE_ONLY) {
-                    wait(bar_w, ph);
+                    wait(bar_w, (uint32_t)c & 1u);
                     __syncwarp();
                     umma::tc_fence_after();
                     if (elect_one()) {
-                        constexpr uint32_t id = umma::idesc_f16(128, 128, false, true);
+                        constexpr uint32_t id = umma::idesc_f16(128, 64, false, true);
 #pragma unroll
-                        for (int k = 0; k < Q / 16; ++k)   // a half's rows against both halves' columns: its own are read
-                            umma::mma_f16_ts(T_YW, T_SC + 8 * k, d_x + ((k * 2048) >> 4), id, k > 0);
+                        for (int j = 0; j < 2; ++j)   // rows 64 j .. of the decayed scores, columns of half j
+#pragma unroll
+                            for (int k = 0; k < Q / 16; ++k)
+                                umma::mma_f16_ts(T_YW + 64 * j, T_SC + (j ? 0 : 64) + 8 * k,
+                                                 d_x + ((j * 8192 + k * 2048) >> 4), id, k > 0);
                         umma::mma_commit(bar_y);
                     }
                     __syncwarp();
+                }
+                if (!STATE_ONLY && c + 1 < chunks) {
+                    wait(bar_y, (uint32_t)c & 1u);   // the decayed scores are used up
+                    umma::tc_fence_after();
+                    scores(c + 1);
                 }
             }
         } else if (warp == COPY_WARP) {
@@ -709,29 +732,6 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
                 o[1] = w[1];
             }
         };
-        // C of chunk c, two values a column, as the A operand of both products with C: the
-        // same 64 tokens in lanes 0 .. 63 and 64 .. 127, one half's rows each
-        auto place_c = [&](int c) {
-            wait(full + (c & 1), (uint32_t)(c >> 1) & 1u);
-            const uint32_t p = sT + (c & 1) * Sm::TILE + OFF_C;
-            if constexpr (N == 128) {
-                const uint32_t r = p + (cg >> 1) * KB + umma::sw128_offset(t, (cg & 1) * 4);
-                uint32_t v[16];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint4 u = lds128(r ^ (16 * j));
-                    v[4 * j] = u.x; v[4 * j + 1] = u.y; v[4 * j + 2] = u.z; v[4 * j + 3] = u.w;
-                }
-                umma::tmem_st16(T_C + lane_off + 16 * cg, v);
-            } else {
-                const uint32_t r = p + umma::sw128_offset(t, 2 * cg);
-                const uint4 u = lds128(r), w = lds128(r ^ 16);
-                const uint32_t v[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
-                umma::tmem_st8(T_C + lane_off + 8 * cg, v);
-            }
-            umma::tmem_st_wait();
-        };
-        if (!STATE_ONLY && chunks > 0) place_c(0);
         // maxima of this chunk, of the next (written from its convolution on) and of the one
         // after (cleared now; its last readers, of the previous chunk, have met since)
         uint32_t *m_now = mx, *m_next = mx + 4, *m_after = mx + 8;
@@ -740,7 +740,6 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
             const uint32_t ph = (uint32_t)c & 1u, ph_full = (uint32_t)(c >> 1) & 1u;
             const float *rec0 = reinterpret_cast<const float *>(sm + Sm::OFF_REC) + b * 2 * REC, *rec1 = rec0 + REC;
             const float *recv = hv ? rec1 : rec0;
-            umma::tc_fence_before();
             meet();
             if (tid < 4) m_after[tid] = 0;
 
@@ -794,13 +793,15 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
                 // the next one's x
                 if (c + 1 < chunks) fetch(c + 1);
                 if (c > 0) gate(c - 1);
-                // decayed scores: 16 of them per thread, as the A operand in tensor memory
+                // decayed scores: 16 of them per thread, as the A operand in tensor memory.
+                // Half 0 (lanes 0..63) writes columns 64 .. 95 and half 1 columns 0 .. 31, where
+                // the other half's scores lie in lanes that nobody reads.
                 wait(bar_sc, ph);
                 umma::tc_fence_after();
                 uint32_t p[8] = {0, 0, 0, 0, 0, 0, 0, 0};
                 if ((q & 1) || cg < 2) {   // tokens 0 .. 31 see nothing of 32 .. 63
                     uint32_t sc[16];
-                    umma::tmem_ld16_nowait(T_SC + lane_off + 16 * cg, sc);
+                    umma::tmem_ld16_nowait(T_SC + lane_off + 64 * hv + 16 * cg, sc);
                     const float Lt = recv[R_L + t];
                     umma::tmem_ld_wait();
                     if ((q & 1) && cg < 2) {
@@ -828,8 +829,7 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
                         }
                     }
                 }
-                umma::named_bar_sync(2 + q, 128);   // the four warps of these lanes have read their scores
-                umma::tmem_st8(T_SC + lane_off + 8 * cg, p);
+                umma::tmem_st8(T_SC + lane_off + (hv ? 0 : 64) + 8 * cg, p);
                 umma::tmem_st_wait();
                 umma::tc_fence_before();
                 __syncwarp();
@@ -873,11 +873,11 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) y[e] = fmul2(half2_float2(xw[e]), fd2);
                 umma::tmem_ld_wait();
+                umma::tc_fence_before();
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     y[e] = ffma2(as_float2(yi[2 * e], yi[2 * e + 1]), fi2,
                                  ffma2(as_float2(yw[2 * e], yw[2 * e + 1]), fw2, y[e]));
-                if (c + 1 < chunks) place_c(c + 1);
             }
             uint32_t *const done = m_now;
             m_now = m_next;
