@@ -42,6 +42,35 @@ __device__ __forceinline__ float block_amax(uint32_t bits) {
     return __uint_as_float(max(bits, __float_as_uint(kTiny)));
 }
 
+// Eight elements as they were loaded (half the registers of their floats for bf16, so
+// that more loads are in flight), and as floats.
+template <typename T> struct Raw8;
+template <> struct Raw8<bf16> {
+    uint4 u;
+    __device__ __forceinline__ void load(const bf16 *p) { u = __ldg(reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void floats(float (&x)[8]) const {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            x[2 * e] = bf16lo(w[e]);
+            x[2 * e + 1] = bf16hi(w[e]);
+        }
+    }
+};
+template <> struct Raw8<float> {
+    float v[8];
+    __device__ __forceinline__ void load(const float *p) { load8(p, v); }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = 0.f;
+    }
+    __device__ __forceinline__ void floats(float (&x)[8]) const {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = v[e];
+    }
+};
+
 constexpr int QB = 4;   // row blocks per half warp
 
 template <typename T>
@@ -60,26 +89,25 @@ quant_rows_kernel(const T *__restrict__ x, long long ld_x, uint32_t n_blocks, in
         r[i] = r[i - 1] + wrap;
         c[i] = wrap ? 0 : c[i - 1] + 1;
     }
-    float v[QB][8];
+    Raw8<T> raw[QB];
 #pragma unroll
     for (int i = 0; i < QB; ++i) {
         const int col = (int)c[i] * 128 + 8 * sub;
-        if (first + i < n_blocks && col < cols) load8(x + r[i] * ld_x + col, v[i]);
-        else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
-        }
+        if (first + i < n_blocks && col < cols) raw[i].load(x + r[i] * ld_x + col);
+        else raw[i].zero();
     }
 #pragma unroll
     for (int i = 0; i < QB; ++i) {
-        uint32_t m = amax8(v[i]);
+        float v[8];
+        raw[i].floats(v);
+        uint32_t m = amax8(v);
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
         const float amax = block_amax(m);
         const int col = (int)c[i] * 128 + 8 * sub;
         if (first + i < n_blocks) {
             if (sub == 0) scale[first + i] = __fdiv_rn(amax, kFp8Max);
-            if (col < cols) *reinterpret_cast<uint2 *>(q + r[i] * ld_q + col) = to_e4m3x8(v[i], __fdiv_rn(kFp8Max, amax));
+            if (col < cols) *reinterpret_cast<uint2 *>(q + r[i] * ld_q + col) = to_e4m3x8(v, __fdiv_rn(kFp8Max, amax));
         }
     }
 }
@@ -91,18 +119,19 @@ quant_tiles_kernel(const T *__restrict__ x, long long ld_x, int rows, int cols, 
     __shared__ uint32_t part[8];
     const int sub = threadIdx.x & 15, c = blockIdx.x * 128 + 8 * sub;
     const long long r0 = (long long)blockIdx.y * 128 + (threadIdx.x >> 4);
-    float v[8][8];
+    Raw8<T> raw[8];
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        if (r0 + 16 * i < rows && c < cols) load8(x + (r0 + 16 * i) * ld_x + c, v[i]);
-        else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
-        }
+        if (r0 + 16 * i < rows && c < cols) raw[i].load(x + (r0 + 16 * i) * ld_x + c);
+        else raw[i].zero();
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, amax8(v[i]));
+    for (int i = 0; i < 8; ++i) {
+        float v[8];
+        raw[i].floats(v);
+        m = max(m, amax8(v));
+    }
     m = __reduce_max_sync(0xffffffffu, m);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
     __syncthreads();
@@ -112,8 +141,11 @@ quant_tiles_kernel(const T *__restrict__ x, long long ld_x, int rows, int cols, 
     if (threadIdx.x == 0) scale[(size_t)blockIdx.y * gridDim.x + blockIdx.x] = __fdiv_rn(amax, kFp8Max);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        if (r0 + 16 * i < rows && c < cols)
-            *reinterpret_cast<uint2 *>(q + (r0 + 16 * i) * ld_q + c) = to_e4m3x8(v[i], inv);
+        if (r0 + 16 * i < rows && c < cols) {
+            float v[8];
+            raw[i].floats(v);
+            *reinterpret_cast<uint2 *>(q + (r0 + 16 * i) * ld_q + c) = to_e4m3x8(v, inv);
+        }
 }
 
 template <typename T>

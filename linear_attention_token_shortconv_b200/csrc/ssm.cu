@@ -258,44 +258,47 @@ namespace {
 
 constexpr int DEC_THREADS = 256;
 
-// One CTA per (head, sequence): the state's loads are issued first, the convolution
+// One CTA per 64 state columns (a head of 64, half of one of 128) of a sequence, 8 or 16
+// float4 of state a thread, four or two such CTAs an SM: the state's loads are issued first, the convolution
 // of the head's x channels and of its group's B and C runs while they are in
 // flight, then every element is updated, written back and added into y.  The
 // history of the x channels, which no other CTA reads, is shifted here; that of
 // B and C, which all heads of a group read, by ssm_shift after this kernel.
-template <int N, int P, typename T, typename Tout>
+template <int N, typename T, typename Tout>
 __global__ void __launch_bounds__(DEC_THREADS)
 ssm_decode_kernel(const Raw<T> raw, const T *__restrict__ dt, long long ld_dt, const float *__restrict__ conv_w,
                   const float *__restrict__ conv_b, T *hist, const float *__restrict__ A,
                   const float *__restrict__ b_dt, const float *__restrict__ Dw, const T *__restrict__ z,
-                  long long ld_z, float *S, Tout *__restrict__ out, int H, int G) {
-    constexpr int F4 = P / 4, ROWS = DEC_THREADS / F4, NV = N / ROWS;
-    __shared__ __align__(16) float xs[P], bs[N], cs[N];
-    __shared__ __align__(16) float part[ROWS][P];
-    const int tid = threadIdx.x, h = blockIdx.x, b = blockIdx.y, g = h / (H / G);
+                  long long ld_z, float *S, Tout *__restrict__ out, int H, int G, int P) {
+    constexpr int COLS = 64, F4 = COLS / 4, ROWS = DEC_THREADS / F4, NV = N / ROWS;
+    __shared__ __align__(16) float xs[COLS], bs[N], cs[N];
+    __shared__ __align__(16) float part[ROWS][COLS];
+    const int tid = threadIdx.x, col0 = blockIdx.x * COLS, h = col0 / P, b = blockIdx.y, g = h / (H / G);
+    const int q = tid % F4, row0 = tid / F4;
     const int chans = raw.hp + 2 * raw.gn;
-    float4 *Sh = reinterpret_cast<float4 *>(S + ((size_t)b * H + h) * N * P);
+    float *Sh = S + (((size_t)b * H + h) * N + row0) * P + col0 % P + 4 * q;   // rows ROWS apart
     float4 s[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) s[i] = __ldcs(Sh + tid + i * DEC_THREADS);
+    for (int i = 0; i < NV; ++i) s[i] = __ldcs(reinterpret_cast<const float4 *>(Sh + (size_t)i * ROWS * P));
     const float d = softplus_acc(to_f32(dt[b * ld_dt + h]) + __ldg(b_dt + h));
     const float a = expf(-expf(__ldg(A + h)) * d);
-    for (int i = tid; i < P + 2 * N; i += DEC_THREADS) {
-        const int c = i < P ? h * P + i : i < P + N ? raw.hp + g * N + (i - P) : raw.hp + raw.gn + g * N + (i - P - N);
+    for (int i = tid; i < COLS + 2 * N; i += DEC_THREADS) {
+        const int c = i < COLS       ? col0 + i
+                      : i < COLS + N ? raw.hp + g * N + (i - COLS)
+                                     : raw.hp + raw.gn + g * N + (i - COLS - N);
         const float4 w = __ldg(reinterpret_cast<const float4 *>(conv_w) + c);
         T *hb = hist + (size_t)b * 3 * chans + c;
         const T r0 = hb[0], r1 = hb[chans], r2 = hb[2 * (size_t)chans], r3 = *raw.at(b, c);
         float v = conv_b ? __ldg(conv_b + c) : 0.f;
         v = fmaf(w.w, to_f32(r3), fmaf(w.z, to_f32(r2), fmaf(w.y, to_f32(r1), fmaf(w.x, to_f32(r0), v))));
         v = ssm::silu(v);
-        if (i < P) {
+        if (i < COLS) {
             xs[i] = v;
             hb[0] = r1; hb[chans] = r2; hb[2 * (size_t)chans] = r3;
-        } else if (i < P + N) bs[i - P] = d * v;
-        else cs[i - P - N] = v;
+        } else if (i < COLS + N) bs[i - COLS] = d * v;
+        else cs[i - COLS - N] = v;
     }
     __syncthreads();
-    const int q = tid % F4, row0 = tid / F4;
     const float4 x = *reinterpret_cast<const float4 *>(&xs[4 * q]);
     float4 y = make_float4(0, 0, 0, 0);
 #pragma unroll
@@ -306,17 +309,17 @@ ssm_decode_kernel(const Raw<T> raw, const T *__restrict__ dt, long long ld_dt, c
         s[i].y = fmaf(a, s[i].y, bb * x.y); y.y = fmaf(cc, s[i].y, y.y);
         s[i].z = fmaf(a, s[i].z, bb * x.z); y.z = fmaf(cc, s[i].z, y.z);
         s[i].w = fmaf(a, s[i].w, bb * x.w); y.w = fmaf(cc, s[i].w, y.w);
-        __stcs(Sh + tid + i * DEC_THREADS, s[i]);
+        __stcs(reinterpret_cast<float4 *>(Sh + (size_t)i * ROWS * P), s[i]);
     }
     *reinterpret_cast<float4 *>(&part[row0][4 * q]) = y;
     __syncthreads();
-    if (tid < P) {
+    if (tid < COLS) {
         float v = 0.f;
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) v += part[r][tid];
         if (Dw) v = fmaf(__ldg(Dw + h), xs[tid], v);
-        if (z) v *= ssm::silu(to_f32(z[b * ld_z + (long long)h * P + tid]));
-        out[((size_t)b * H + h) * P + tid] = from_f32<Tout>(v);
+        if (z) v *= ssm::silu(to_f32(z[b * ld_z + col0 + tid]));
+        out[(size_t)b * H * P + col0 + tid] = from_f32<Tout>(v);
     }
 }
 
@@ -334,30 +337,29 @@ __global__ void __launch_bounds__(128) ssm_shift_kernel(const Raw<T> raw, T *his
     *reinterpret_cast<V *>(hb + 2 * (size_t)chans) = r3;
 }
 
-template <int N, int P, typename T, typename Tout>
+template <int N, typename T, typename Tout>
 cudaError_t launch_decode_typed(const SsmArgs &a) {
     T *hist = static_cast<T *>(const_cast<void *>(a.hist));
-    ssm_decode_kernel<N, P, T, Tout><<<dim3(a.H, a.n_seq), DEC_THREADS, 0, a.stream>>>(
+    ssm_decode_kernel<N, T, Tout><<<dim3(a.H * (a.P / 64), a.n_seq), DEC_THREADS, 0, a.stream>>>(
         raw_of<T>(a), static_cast<const T *>(a.dt), a.ld_dt, a.conv_w, a.conv_b, hist, a.A, a.b_dt, a.D,
-        static_cast<const T *>(a.z), a.ld_z, a.S_final, static_cast<Tout *>(a.out), a.H, a.G);
+        static_cast<const T *>(a.z), a.ld_z, a.S_final, static_cast<Tout *>(a.out), a.H, a.G, a.P);
     const cudaError_t e = launched();
     if (e != cudaSuccess) return e;
     ssm_shift_kernel<T><<<dim3((2 * a.G * a.N / 4 + 127) / 128, a.n_seq), 128, 0, a.stream>>>(raw_of<T>(a), hist);
     return launched();
 }
 
-template <int N, int P>
+template <int N>
 cudaError_t launch_decode_dims(const SsmArgs &a) {
     if (a.in_bf16)
-        return a.out_bf16 ? launch_decode_typed<N, P, bf16, bf16>(a) : launch_decode_typed<N, P, bf16, float>(a);
-    return a.out_bf16 ? launch_decode_typed<N, P, float, bf16>(a) : launch_decode_typed<N, P, float, float>(a);
+        return a.out_bf16 ? launch_decode_typed<N, bf16, bf16>(a) : launch_decode_typed<N, bf16, float>(a);
+    return a.out_bf16 ? launch_decode_typed<N, float, bf16>(a) : launch_decode_typed<N, float, float>(a);
 }
 
 }  // namespace
 
 cudaError_t launch_ssm_decode(const SsmArgs &a) {
-    if (a.N == 128) return a.P == 128 ? launch_decode_dims<128, 128>(a) : launch_decode_dims<128, 64>(a);
-    return a.P == 128 ? launch_decode_dims<64, 128>(a) : launch_decode_dims<64, 64>(a);
+    return a.N == 128 ? launch_decode_dims<128>(a) : launch_decode_dims<64>(a);
 }
 
 }  // namespace gdn
