@@ -9,11 +9,10 @@
 //
 // The prefill is two kernels.  ssm_act writes the convolved channels and (D_t, a_t)
 // of every token in fp32; ssm_scan runs the recurrence with the state in registers.
-// A column p of the state depends on no other column, so a CTA takes 32 columns of
-// one (sequence, head): 128 threads, each two columns of N / 8 rows, 8 lanes of a
-// warp sharing the columns and adding their parts of y by shuffles.  What bounds it
-// is the chain of tokens: per token and warp 3 N / 4 fp32 instructions and N / 16
-// shared loads at one warp per scheduler.
+// A column p of the state depends on no other column, so a CTA takes 16 columns of
+// one (sequence, head): 64 threads, each two columns of N / 8 rows, 8 lanes of a
+// warp sharing the columns and adding their parts of y by shuffles, four tokens
+// together.  What bounds it is the chain of tokens, at one or two warps a scheduler.
 #include <cuda_runtime.h>
 
 #include "ssm.cuh"
@@ -91,23 +90,51 @@ ssm_act_kernel(const Raw<T> raw, const T *__restrict__ hist, const float *__rest
     }
 }
 
-constexpr int SCAN_COLS = 32, SCAN_TOK = 16;
+constexpr int SCAN_COLS = 16, SCAN_TOK = 16, SCAN_THREADS = 64;
+
+// An asynchronous copy of B bytes to shared memory, zeros where `in` is false.
+template <int B> __device__ __forceinline__ void copy_async(void *dst, const void *src, bool in) {
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+    if constexpr (B == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(in ? 16 : 0) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d), "l"(src), "n"(B), "r"(in ? B : 0) : "memory");
+}
 
 template <int N, typename T, typename Tout>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(SCAN_THREADS)
 ssm_scan_kernel(const float *__restrict__ act, const float2 *__restrict__ step, const float *__restrict__ Dw,
                 const T *__restrict__ z, long long ld_z, const float *S0, const int32_t *__restrict__ cu, int n_seq,
                 int n_tok, int H, int G, int P, Tout *__restrict__ out, float *S_final) {
     constexpr int R = N / 8;             // state rows of a thread
-    __shared__ __align__(16) float bs[SCAN_TOK][N], cs[SCAN_TOK][N], xs[SCAN_TOK][SCAN_COLS];
-    __shared__ float2 ds[SCAN_TOK];
+    struct Stage {
+        float b[SCAN_TOK][N], c[SCAN_TOK][N], x[SCAN_TOK][SCAN_COLS];
+        float2 d[SCAN_TOK];
+    };
+    __shared__ __align__(16) Stage stages[2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int p0 = blockIdx.x * SCAN_COLS, h = blockIdx.y, n = blockIdx.z;
-    const int slice = lane & 7, col = 8 * warp + 2 * (lane >> 3);   // rows 4 slice + 32 i + e, columns col, col + 1
+    const int slice = lane & 7, lcol = 8 * warp + 2 * (lane >> 3);   // rows 4 slice + 32 i + e, columns lcol, lcol + 1
     const int chans = H * P + 2 * G * N, g = h / (H / G);
     int begin, end;
     seq_range(cu, n_seq, n_tok, n, begin, end);
-    const size_t sbase = ((size_t)n * H + h) * N * P + p0 + col;
+    auto load = [&](int t0, Stage &st) {
+        const int len = end - t0;   // rows past the end are zeros
+        const float *rows = act + (size_t)t0 * chans;
+        for (int i = tid; i < SCAN_TOK * (N / 4); i += SCAN_THREADS) {
+            const int r = i / (N / 4), q = i % (N / 4);
+            const float *src = rows + (r < len ? (size_t)r * chans : 0) + H * P + g * N + 4 * q;
+            copy_async<16>(&st.b[r][4 * q], src, r < len);
+            copy_async<16>(&st.c[r][4 * q], src + G * N, r < len);
+        }
+        for (int i = tid; i < SCAN_TOK * (SCAN_COLS / 4); i += SCAN_THREADS) {
+            const int r = i / (SCAN_COLS / 4), q = i % (SCAN_COLS / 4);
+            copy_async<16>(&st.x[r][4 * q], rows + (r < len ? (size_t)r * chans : 0) + h * P + p0 + 4 * q, r < len);
+        }
+        if (tid < SCAN_TOK) copy_async<8>(&st.d[tid], step + (size_t)(t0 + (tid < len ? tid : 0)) * H + h, tid < len);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    const size_t sbase = ((size_t)n * H + h) * N * P + p0 + lcol;
     float2 S[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -115,53 +142,62 @@ ssm_scan_kernel(const float *__restrict__ act, const float2 *__restrict__ step, 
         S[i] = S0 ? *reinterpret_cast<const float2 *>(S0 + sbase + (size_t)row * P) : make_float2(0.f, 0.f);
     }
     const float dw = Dw ? __ldg(Dw + h) : 0.f;
-    for (int t0 = begin; t0 < end; t0 += SCAN_TOK) {
+    if (begin < end) load(begin, stages[0]);
+    for (int t0 = begin, k = 0; t0 < end; t0 += SCAN_TOK, ++k) {
         const int len = min(SCAN_TOK, end - t0);
-        __syncthreads();
-        for (int i = tid; i < len * (N / 4); i += 128) {
-            const int r = i / (N / 4), q = i % (N / 4);
-            const float *row = act + (size_t)(t0 + r) * chans + H * P + g * N + 4 * q;
-            *reinterpret_cast<float4 *>(&bs[r][4 * q]) = __ldg(reinterpret_cast<const float4 *>(row));
-            *reinterpret_cast<float4 *>(&cs[r][4 * q]) = __ldg(reinterpret_cast<const float4 *>(row + G * N));
+        const Stage &st = stages[k & 1];
+        if (t0 + SCAN_TOK < end) {
+            load(t0 + SCAN_TOK, stages[(k + 1) & 1]);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+        } else {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
         }
-        for (int i = tid; i < len * (SCAN_COLS / 4); i += 128) {
-            const int r = i / (SCAN_COLS / 4), q = i % (SCAN_COLS / 4);
-            *reinterpret_cast<float4 *>(&xs[r][4 * q]) =
-                __ldg(reinterpret_cast<const float4 *>(act + (size_t)(t0 + r) * chans + h * P + p0 + 4 * q));
-        }
-        if (tid < len) ds[tid] = __ldg(step + (size_t)(t0 + tid) * H + h);
         __syncthreads();
-        for (int r = 0; r < len; ++r) {
-            const float2 da = ds[r];
-            const float2 x = *reinterpret_cast<const float2 *>(&xs[r][col]);
-            const float2 dx = make_float2(da.x * x.x, da.x * x.y);
-            const float2 aa = make_float2(da.y, da.y);
-            float2 y = make_float2(0.f, 0.f);
+        // four tokens at a time: their recurrences follow one another, but their parts of y
+        // (8 values) are added over the eight slices together, one value staying in each lane
+        for (int r = 0; r < len; r += 4) {
+            float v[8];
 #pragma unroll
-            for (int i4 = 0; i4 < R / 4; ++i4) {
-                const float4 b = *reinterpret_cast<const float4 *>(&bs[r][32 * i4 + 4 * slice]);
-                const float4 c = *reinterpret_cast<const float4 *>(&cs[r][32 * i4 + 4 * slice]);
-                const float bb[4] = {b.x, b.y, b.z, b.w}, cc[4] = {c.x, c.y, c.z, c.w};
+            for (int u = 0; u < 4; ++u) {
+                const float2 da = st.d[r + u];
+                const float a = r + u < len ? da.y : 1.f;
+                const float2 x = *reinterpret_cast<const float2 *>(&st.x[r + u][lcol]);
+                const float2 dx = make_float2(da.x * x.x, da.x * x.y), aa = make_float2(a, a);
+                float2 y = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float2 &s = S[4 * i4 + e];
-                    s = ffma2(aa, s, fmul2(make_float2(bb[e], bb[e]), dx));
-                    y = ffma2(make_float2(cc[e], cc[e]), s, y);
+                for (int i4 = 0; i4 < R / 4; ++i4) {
+                    const float4 b = *reinterpret_cast<const float4 *>(&st.b[r + u][32 * i4 + 4 * slice]);
+                    const float4 c = *reinterpret_cast<const float4 *>(&st.c[r + u][32 * i4 + 4 * slice]);
+                    const float bb[4] = {b.x, b.y, b.z, b.w}, cc[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float2 &s = S[4 * i4 + e];
+                        s = ffma2(aa, s, fmul2(make_float2(bb[e], bb[e]), dx));
+                        y = ffma2(make_float2(cc[e], cc[e]), s, y);
+                    }
+                }
+                v[2 * u] = y.x;
+                v[2 * u + 1] = y.y;
+            }
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) {
+                const bool up = slice & o;
+#pragma unroll
+                for (int i = 0; i < o; ++i) {
+                    const float give = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
+                    v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
                 }
             }
-#pragma unroll
-            for (int o = 1; o < 8; o <<= 1) {
-                y.x += __shfl_xor_sync(0xffffffffu, y.x, o);
-                y.y += __shfl_xor_sync(0xffffffffu, y.y, o);
-            }
-            if (slice < 2) {   // lane `slice` of the eight writes column col + slice
-                const long long t = t0 + r;
-                float v = slice ? fmaf(dw, x.y, y.y) : fmaf(dw, x.x, y.x);
-                const int p = p0 + col + slice;
-                if (z) v *= ssm::silu(to_f32(z[t * ld_z + (long long)h * P + p]));
-                out[(t * H + h) * P + p] = from_f32<Tout>(v);
+            const int ru = r + (slice >> 1), cu1 = lcol + (slice & 1);   // this lane's token and column
+            if (ru < len) {
+                const long long t = t0 + ru;
+                const int p = p0 + cu1;
+                float o = fmaf(dw, st.x[ru][cu1], v[0]);
+                if (z) o *= ssm::silu(to_f32(z[t * ld_z + (long long)h * P + p]));
+                out[(t * H + h) * P + p] = from_f32<Tout>(o);
             }
         }
+        __syncthreads();   // before the stage is loaded again
     }
     if (S_final) {
 #pragma unroll
@@ -207,7 +243,7 @@ cudaError_t launch_tail(const SsmArgs &a) {
 template <int N, typename T, typename Tout>
 cudaError_t launch_scan(const SsmArgs &a, const float *act, const float2 *step) {
     const dim3 grid(a.P / SCAN_COLS, a.H, a.n_seq);
-    ssm_scan_kernel<N, T, Tout><<<grid, 128, 0, a.stream>>>(act, step, a.D, static_cast<const T *>(a.z), a.ld_z, a.S0,
+    ssm_scan_kernel<N, T, Tout><<<grid, SCAN_THREADS, 0, a.stream>>>(act, step, a.D, static_cast<const T *>(a.z), a.ld_z, a.S0,
                                                             a.cu_seqlens, a.n_seq, a.n_tok, a.H, a.G, a.P,
                                                             static_cast<Tout *>(a.out), a.S_final);
     return launched();
