@@ -671,26 +671,36 @@ cudaError_t launch_typed(int M, int N, int K, const void *A, long long lda, cons
     cudaError_t e = sm_count(&sms);
     if (e != cudaSuccess) return e;
     const int kbs = (K + fp8::BK - 1) / fp8::BK;
-    auto tiles = [&](long long rows, long long cols, int bn) { return ((rows + 127) / 128) * ((cols + bn - 1) / bn); };
-    // K split until the tiles cover the SMs, at least two K blocks per rank
+    auto tiles = [&](long long rows, long long cols, int height, int bn) {
+        return ((rows + height - 1) / height) * ((cols + bn - 1) / bn);
+    };
+    // K split where tiles leave half of the SMs idle, over at most 4 CTAs with two K blocks
+    // each (4 x 2048 x 4096: 10.6 us whole, 6.2 over 4; over 8, whose clusters fit fewer at
+    // once, 9.5)
     auto split_for = [&](long long n) {
         int s = 1;
-        while (s < 8 && n * s * 2 <= sms && kbs >= 4 * s) s *= 2;
+        while (s < 4 && n * s * 2 <= sms && kbs >= 4 * s) s *= 2;
         return s;
     };
 #define GDN_FP8(BN, SWAP, S)                                                                                       \
     launch_shape<fp8::Shape<BN, SWAP>, Tout>(M, N, K, A, lda, a_scale, B, ldb, b_scale, C, ldc, S, sms, stream)
     if (M <= 64) {
-        const int s = split_for(tiles(N, M, 64));
+        const int s = split_for(tiles(N, M, 128, 64));
         if (M <= 16) return GDN_FP8(16, true, s);
         if (M <= 32) return GDN_FP8(32, true, s);
         return GDN_FP8(64, true, s);
     }
-    if (tiles(M, N, 256) >= sms)
-        return launch_shape<fp8::Shape<256, false, true>, Tout>(M, N, K, A, lda, a_scale, B, ldb, b_scale, C, ldc, 1,
-                                                                sms, stream);
-    if (tiles(M, N, 128) >= sms) return GDN_FP8(128, false, 1);
-    return GDN_FP8(64, false, split_for(tiles(M, N, 64)));
+    // Otherwise the shape whose waves take least, by the microseconds a K block takes (in
+    // hundredths): 31 at 64 columns, 34 at 128, 53 at a pair's 256 x 256 (512 x 4096 x 4096:
+    // 23.6, 14.6 and 19.3 us; 2048 x 2048 x 4096: 40, 24 and 20 us)
+    auto cost = [&](long long n, int at_once, int block) { return (n + at_once - 1) / at_once * block; };
+    const long long t64 = tiles(M, N, 128, 64);
+    const long long c64 = cost(t64, sms, 31), c128 = cost(tiles(M, N, 128, 128), sms, 34);
+    const long long c256 = cost(tiles(M, N, 256, 256), sms / 2, 53);
+    if (c64 <= c128 && c64 <= c256) return GDN_FP8(64, false, split_for(t64));
+    if (c128 <= c256) return GDN_FP8(128, false, 1);
+    return launch_shape<fp8::Shape<256, false, true>, Tout>(M, N, K, A, lda, a_scale, B, ldb, b_scale, C, ldc, 1, sms,
+                                                            stream);
 #undef GDN_FP8
 }
 
