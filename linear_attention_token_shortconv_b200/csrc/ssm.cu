@@ -292,33 +292,30 @@ cudaError_t launch_ssm_prefill(const SsmArgs &a, void *ws, int sms) {
 
 namespace {
 
-constexpr int DEC_THREADS = 256;
-
-// One CTA per 64 state columns (a head of 64, half of one of 128) of a sequence, 8 or 16
-// float4 of state a thread, four or two such CTAs an SM: the state's loads are issued first, the convolution
+// One CTA per (head, sequence), N P / 16 bytes of state a thread: the state's loads are issued first, the convolution
 // of the head's x channels and of its group's B and C runs while they are in
 // flight, then every element is updated, written back and added into y.  The
 // history of the x channels, which no other CTA reads, is shifted here; that of
 // B and C, which all heads of a group read, by ssm_shift after this kernel.
-template <int N, typename T, typename Tout>
-__global__ void __launch_bounds__(DEC_THREADS)
+template <int N, int COLS, typename T, typename Tout>
+__global__ void __launch_bounds__(4 * COLS)
 ssm_decode_kernel(const Raw<T> raw, const T *__restrict__ dt, long long ld_dt, const float *__restrict__ conv_w,
                   const float *__restrict__ conv_b, T *hist, const float *__restrict__ A,
                   const float *__restrict__ b_dt, const float *__restrict__ Dw, const T *__restrict__ z,
-                  long long ld_z, float *S, Tout *__restrict__ out, int H, int G, int P) {
-    constexpr int COLS = 64, F4 = COLS / 4, ROWS = DEC_THREADS / F4, NV = N / ROWS;
+                  long long ld_z, float *S, Tout *__restrict__ out, int H, int G) {
+    constexpr int P = COLS, THREADS = 4 * COLS, F4 = COLS / 4, ROWS = 16, NV = N / ROWS;
     __shared__ __align__(16) float xs[COLS], bs[N], cs[N];
     __shared__ __align__(16) float part[ROWS][COLS];
-    const int tid = threadIdx.x, col0 = blockIdx.x * COLS, h = col0 / P, b = blockIdx.y, g = h / (H / G);
+    const int tid = threadIdx.x, h = blockIdx.x, col0 = h * COLS, b = blockIdx.y, g = h / (H / G);
     const int q = tid % F4, row0 = tid / F4;
     const int chans = raw.hp + 2 * raw.gn;
-    float *Sh = S + (((size_t)b * H + h) * N + row0) * P + col0 % P + 4 * q;   // rows ROWS apart
+    float *Sh = S + (((size_t)b * H + h) * N + row0) * P + 4 * q;   // rows ROWS apart
     float4 s[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) s[i] = __ldcs(reinterpret_cast<const float4 *>(Sh + (size_t)i * ROWS * P));
     const float d = softplus_acc(to_f32(dt[b * ld_dt + h]) + __ldg(b_dt + h));
     const float a = expf(-expf(__ldg(A + h)) * d);
-    for (int i = tid; i < COLS + 2 * N; i += DEC_THREADS) {
+    for (int i = tid; i < COLS + 2 * N; i += THREADS) {
         const int c = i < COLS       ? col0 + i
                       : i < COLS + N ? raw.hp + g * N + (i - COLS)
                                      : raw.hp + raw.gn + g * N + (i - COLS - N);
@@ -373,29 +370,30 @@ __global__ void __launch_bounds__(128) ssm_shift_kernel(const Raw<T> raw, T *his
     *reinterpret_cast<V *>(hb + 2 * (size_t)chans) = r3;
 }
 
-template <int N, typename T, typename Tout>
+template <int N, int P, typename T, typename Tout>
 cudaError_t launch_decode_typed(const SsmArgs &a) {
     T *hist = static_cast<T *>(const_cast<void *>(a.hist));
-    ssm_decode_kernel<N, T, Tout><<<dim3(a.H * (a.P / 64), a.n_seq), DEC_THREADS, 0, a.stream>>>(
+    ssm_decode_kernel<N, P, T, Tout><<<dim3(a.H, a.n_seq), 4 * P, 0, a.stream>>>(
         raw_of<T>(a), static_cast<const T *>(a.dt), a.ld_dt, a.conv_w, a.conv_b, hist, a.A, a.b_dt, a.D,
-        static_cast<const T *>(a.z), a.ld_z, a.S_final, static_cast<Tout *>(a.out), a.H, a.G, a.P);
+        static_cast<const T *>(a.z), a.ld_z, a.S_final, static_cast<Tout *>(a.out), a.H, a.G);
     const cudaError_t e = launched();
     if (e != cudaSuccess) return e;
     ssm_shift_kernel<T><<<dim3((2 * a.G * a.N / 4 + 127) / 128, a.n_seq), 128, 0, a.stream>>>(raw_of<T>(a), hist);
     return launched();
 }
 
-template <int N>
+template <int N, int P>
 cudaError_t launch_decode_dims(const SsmArgs &a) {
     if (a.in_bf16)
-        return a.out_bf16 ? launch_decode_typed<N, bf16, bf16>(a) : launch_decode_typed<N, bf16, float>(a);
-    return a.out_bf16 ? launch_decode_typed<N, float, bf16>(a) : launch_decode_typed<N, float, float>(a);
+        return a.out_bf16 ? launch_decode_typed<N, P, bf16, bf16>(a) : launch_decode_typed<N, P, bf16, float>(a);
+    return a.out_bf16 ? launch_decode_typed<N, P, float, bf16>(a) : launch_decode_typed<N, P, float, float>(a);
 }
 
 }  // namespace
 
 cudaError_t launch_ssm_decode(const SsmArgs &a) {
-    return a.N == 128 ? launch_decode_dims<128>(a) : launch_decode_dims<64>(a);
+    if (a.N == 128) return a.P == 128 ? launch_decode_dims<128, 128>(a) : launch_decode_dims<128, 64>(a);
+    return a.P == 128 ? launch_decode_dims<64, 128>(a) : launch_decode_dims<64, 64>(a);
 }
 
 }  // namespace gdn
