@@ -239,7 +239,7 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
     uint64_t *mma_done = sempty + NSC;
     uint32_t *tslot = reinterpret_cast<uint32_t *>(mma_done + 2);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tslot + 1);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int rows = SWAP ? N : M, cols = SWAP ? M : N;              // of the MMA's operands
     const int tiles_r = (rows + Sh::ROWS - 1) / Sh::ROWS, tiles_c = (cols + BN - 1) / BN;
     const int kbs = (K + BK - 1) / BK;
