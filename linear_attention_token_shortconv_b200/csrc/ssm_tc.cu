@@ -22,6 +22,10 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
+#include <climits>
+#include <limits>
+
 #include "ssm.cuh"
 #include "umma.cuh"
 
@@ -102,7 +106,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float2 v) {
     return *reinterpret_cast<const uint32_t *>(&b);
 }
 __device__ __forceinline__ uint32_t pack(float2 v) { return umma::pack_half2(v.x, v.y); }
+// The scales are those of the finite values: an infinity or a NaN stays what it is at any
+// scale, and must not cost its neighbours theirs.  fmaxf leaves out NaN; infinities are
+// rare and left out when one was met.
 __device__ __forceinline__ float amax2(float m, float2 v) { return fmaxf(m, fmaxf(fabsf(v.x), fabsf(v.y))); }
+constexpr uint32_t kInf = 0x7f800000u;
+constexpr float kNan = std::numeric_limits<float>::quiet_NaN();
+__device__ __forceinline__ float finite_abs(float x) { return __float_as_uint(fabsf(x)) < kInf ? fabsf(x) : 0.f; }
 
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
@@ -226,7 +236,7 @@ __global__ void __launch_bounds__(stc::PREP_THREADS, 2) ssm_prep_kernel(const Pr
                 }
                 s = silu2(s);
                 x[e] = r < len ? s : make_float2(0.f, 0.f);
-                mf = amax2(mf, x[e]);
+                mf = fmaxf(mf, fmaxf(finite_abs(x[e].x), finite_abs(x[e].y)));
             }
             uint32_t m = __float_as_uint(mf);
             if constexpr (VEC == 32) m = __reduce_max_sync(0xffffffffu, m);
@@ -293,8 +303,7 @@ __global__ void __launch_bounds__(stc::PREP_THREADS, 2) ssm_prep_kernel(const Pr
             if (lane == 31) { aft0 = half1; aft1 = 0.f; }
             const float total = __shfl_sync(0xffffffffu, suf[0], 0);
             float u[2] = {d[0] * eb[lane], d[1] * eb[lane + 32]};
-            const uint32_t m = __reduce_max_sync(0xffffffffu, max(__float_as_uint(u[0]) & 0x7fffffffu,
-                                                                    __float_as_uint(u[1]) & 0x7fffffffu));
+            const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(finite_abs(u[0]), finite_abs(u[1]))));
             float s, inv;
             scale_pow2(m, -1, s, inv);   // u < 1
             float *rec = a.rec + ((size_t)slot * a.H + h) * REC;
@@ -350,7 +359,8 @@ template <int N> struct Smem {
     static constexpr int OFF_REC = OFF_Z + 2 * 16384;  // [2 stages][2 halves][REC]
     static constexpr int OFF_CW = OFF_REC + 4 * REC * 4;  // conv weights [5][128]
     static constexpr int OFF_MAX = OFF_CW + 5 * 128 * 4;  // bits of the largest |.|, [3 chunks][x, x, state, state]
-    static constexpr int OFF_BAR = OFF_MAX + 12 * 4;
+    static constexpr int OFF_ODD = OFF_MAX + 12 * 4;      // per column the first token whose x is not finite; any
+    static constexpr int OFF_BAR = OFF_ODD + 132 * 4;
     static constexpr int SIZE = OFF_BAR + 128 + 1024;     // barriers, TMEM slot, abort flag; alignment slack
 };
 static_assert(Smem<128>::SIZE <= 232448, "227 KB per block");
@@ -372,6 +382,7 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tslot + 1);
     float *cw = reinterpret_cast<float *>(sm + Sm::OFF_CW);
     uint32_t *mx = reinterpret_cast<uint32_t *>(sm + Sm::OFF_MAX);
+    int *odd = reinterpret_cast<int *>(sm + Sm::OFF_ODD);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int q = warp & 3, cg = warp >> 2;
     const int blk = blockIdx.x, n = blockIdx.y, seg = blockIdx.z;
@@ -415,6 +426,7 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
         umma::fence_mbar_init();
     }
     if (tid < 12) mx[tid] = 0;
+    if (tid <= 128) odd[tid] = tid < 128 ? INT_MAX : 0;
     for (int i = tid; i < 5 * 128; i += THREADS) {
         const int j = i >> 7, c = i & 127;
         const bool in = c < 64 || live1;
@@ -660,6 +672,7 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
                 f[j][1] = make_float2(bf16lo(raw[j].y), bf16hi(raw[j].y));
             }
             float m = 0.f;
+            float2 chk = make_float2(0.f, 0.f);   // stays 0 while all are finite
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const bool in = 4 * warp + i < len;
@@ -671,7 +684,25 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
                     v = silu2(v);
                     xh[i][e] = in ? v : make_float2(0.f, 0.f);
                     m = amax2(m, xh[i][e]);
+                    chk = ffma2(xh[i][e], make_float2(0.f, 0.f), chk);
                 }
+            }
+            if (__any_sync(0xffffffffu, chk.x + chk.y != 0.f)) {
+                // A product's zero for a token before it would make NaN of such a value, so
+                // it is left out here, and its column written over behind the last chunk.
+                m = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float &v = e & 1 ? xh[i][e >> 1].y : xh[i][e >> 1].x;
+                        if (!(fabsf(v) <= FLT_MAX)) {
+                            v = 0.f;
+                            atomicMin(odd + xc + e, (c_lo + c) * Q + 4 * warp + i);
+                            odd[128] = 1;
+                        }
+                        m = fmaxf(m, fabsf(v));
+                    }
             }
 #pragma unroll
             for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -696,7 +727,13 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
             float ms = 0.f;
 #pragma unroll
             for (int j = 0; j < 16; ++j) ms = amax2(ms, S[j]);
-            const uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(ms));
+            uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(ms));
+            if (mb >= kInf) {
+                ms = 0.f;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) ms = fmaxf(ms, fmaxf(finite_abs(S[j].x), finite_abs(S[j].y)));
+                mb = __reduce_max_sync(0xffffffffu, __float_as_uint(ms));
+            }
             if (lane == 0) atomicMax(m3 + 2 + (cg >> 1), mb);
         };
         if (!STATE_ONLY) state_max(mx);
@@ -893,6 +930,13 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
                           : seg == last_seg && a.S_final ? a.S_final + sbase
                                                          : nullptr;
         if (to) {
+            if (odd[128]) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    if (odd[sc0 + 2 * j] < INT_MAX) S[j].x = kNan;
+                    if (odd[sc0 + 2 * j + 1] < INT_MAX) S[j].y = kNan;
+                }
+            }
 #pragma unroll
             for (int j = 0; j < 16; j += 2)
                 *reinterpret_cast<float4 *>(to + 2 * j) = make_float4(S[j].x, S[j].y, S[j + 1].x, S[j + 1].y);
@@ -902,6 +946,13 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
     }
     umma::tc_fence_before();
     __syncthreads();
+    if (!STATE_ONLY && odd[128]) {
+        // from the first x of a column that is not finite on, its outputs are NaN
+        const int col = tid & 127, from = odd[col], to = min(c_hi * Q, end - begin);   // from INT_MAX: none
+        for (int u = from; u < to; ++u)
+            if (u % (THREADS / 128) == tid >> 7)
+                a.out[(long long)(begin + u) * (a.H * a.P) + xcol + col] = __float2bfloat16(kNan);
+    }
     if (warp == MMA_WARP) umma::tmem_dealloc(tb, 512);
 }
 
