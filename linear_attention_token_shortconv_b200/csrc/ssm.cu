@@ -12,8 +12,12 @@
 // A column p of the state depends on no other column, so a CTA takes 16 columns of
 // one (sequence, head): 64 threads, each two columns of N / 8 rows, 8 lanes of a
 // warp sharing the columns and adding their parts of y by shuffles, four tokens
-// together.  What bounds it is the chain of tokens, at one or two warps a scheduler.
+// together.  What bounds it is the chain of tokens, at one or two warps a scheduler; few
+// and long sequences are cut into segments, whose states a first pass finds.
+// 1000 + 999 tokens, 16 heads of 64, N = 64: 71 us, of it 11 for ssm_act (111 uncut).
 #include <cuda_runtime.h>
+
+#include <climits>
 
 #include "ssm.cuh"
 
@@ -101,11 +105,25 @@ template <int B> __device__ __forceinline__ void copy_async(void *dst, const voi
         asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d), "l"(src), "n"(B), "r"(in ? B : 0) : "memory");
 }
 
-template <int N, typename T, typename Tout>
+// Sequences of at least `from` tokens in segments of `len` (a multiple of SCAN_TOK).
+// STATE_ONLY runs every segment but a sequence's last from zero, segment 0 from S0, and
+// leaves the state and the product of its decays; the main pass starts each segment from
+// those before it, joined.
+struct Segments {
+    int from, len;           // from = INT_MAX: no sequence
+    // segment 0 of sequence n has slot n, its segment k > 0 slot n_seq + begin / len + k - 1:
+    // the blocks that all sequences have start first, and spread over the SMs
+    int slots;
+    float *state;            // [slot][H][N][P]
+    float *decay;            // [slot][H]
+    float *s0_copy;          // S0 where the final state replaces it, else NULL
+};
+
+template <int N, typename T, typename Tout, bool STATE_ONLY>
 __global__ void __launch_bounds__(SCAN_THREADS)
 ssm_scan_kernel(const float *__restrict__ act, const float2 *__restrict__ step, const float *__restrict__ Dw,
                 const T *__restrict__ z, long long ld_z, const float *S0, const int32_t *__restrict__ cu, int n_seq,
-                int n_tok, int H, int G, int P, Tout *__restrict__ out, float *S_final) {
+                int n_tok, int H, int G, int P, const Segments seg, Tout *__restrict__ out, float *S_final) {
     constexpr int R = N / 8;             // state rows of a thread
     struct Stage {
         float b[SCAN_TOK][N], c[SCAN_TOK][N], x[SCAN_TOK][SCAN_COLS];
@@ -113,11 +131,26 @@ ssm_scan_kernel(const float *__restrict__ act, const float2 *__restrict__ step, 
     };
     __shared__ __align__(16) Stage stages[2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int p0 = blockIdx.x * SCAN_COLS, h = blockIdx.y, n = blockIdx.z;
+    const int cols = P / SCAN_COLS, slot = blockIdx.y, h = blockIdx.x / cols, p0 = blockIdx.x % cols * SCAN_COLS;
     const int slice = lane & 7, lcol = 8 * warp + 2 * (lane >> 3);   // rows 4 slice + 32 i + e, columns lcol, lcol + 1
     const int chans = H * P + 2 * G * N, g = h / (H / G);
-    int begin, end;
+    int n = slot, begin, end;
+    if (slot >= n_seq) {   // the last sequence whose later segments start at or before this slot
+        n = 0;
+        for (int hi = n_seq; hi - n > 1;) {
+            const int mid = (n + hi) >> 1;
+            seq_range(cu, n_seq, n_tok, mid, begin, end);
+            if (n_seq + begin / seg.len <= slot) n = mid; else hi = mid;
+        }
+    }
     seq_range(cu, n_seq, n_tok, n, begin, end);
+    const int later = n_seq + begin / seg.len - 1;             // slot of segment k > 0: later + k
+    const int k = slot < n_seq ? 0 : slot - later;
+    if (slot >= n_seq && k < 1) return;
+    const int last = end - begin >= seg.from ? (end - begin - 1) / seg.len : 0;
+    if (STATE_ONLY ? k >= last : k > last) return;
+    if (k < last) end = begin + (k + 1) * seg.len;
+    begin += k * seg.len;
     auto load = [&](int t0, Stage &st) {
         const int len = end - t0;   // rows past the end are zeros
         const float *rows = act + (size_t)t0 * chans;
@@ -125,7 +158,7 @@ ssm_scan_kernel(const float *__restrict__ act, const float2 *__restrict__ step, 
             const int r = i / (N / 4), q = i % (N / 4);
             const float *src = rows + (r < len ? (size_t)r * chans : 0) + H * P + g * N + 4 * q;
             copy_async<16>(&st.b[r][4 * q], src, r < len);
-            copy_async<16>(&st.c[r][4 * q], src + G * N, r < len);
+            if (!STATE_ONLY) copy_async<16>(&st.c[r][4 * q], src + G * N, r < len);
         }
         for (int i = tid; i < SCAN_TOK * (SCAN_COLS / 4); i += SCAN_THREADS) {
             const int r = i / (SCAN_COLS / 4), q = i % (SCAN_COLS / 4);
@@ -134,20 +167,36 @@ ssm_scan_kernel(const float *__restrict__ act, const float2 *__restrict__ step, 
         if (tid < SCAN_TOK) copy_async<8>(&st.d[tid], step + (size_t)(t0 + (tid < len ? tid : 0)) * H + h, tid < len);
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    const size_t sbase = ((size_t)n * H + h) * N * P + p0 + lcol;
+    if (begin < end) load(begin, stages[0]);
+    // element of state row i of this thread in a [H][N][P] state
+    auto at = [&](int i) { return ((size_t)h * N + 32 * (i / 4) + 4 * slice + (i & 3)) * P + p0 + lcol; };
+    const size_t one = (size_t)H * N * P;
     float2 S[R];
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const int row = 32 * (i / 4) + 4 * slice + (i & 3);
-        S[i] = S0 ? *reinterpret_cast<const float2 *>(S0 + sbase + (size_t)row * P) : make_float2(0.f, 0.f);
+    for (int i = 0; i < R; ++i) S[i] = make_float2(0.f, 0.f);
+    if (STATE_ONLY || k == 0) {
+        const float *from = k > 0 ? nullptr : !STATE_ONLY && last > 0 && seg.s0_copy ? seg.s0_copy : S0;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            if (from) S[i] = *reinterpret_cast<const float2 *>(from + n * one + at(i));
+            if (STATE_ONLY && from && seg.s0_copy) *reinterpret_cast<float2 *>(seg.s0_copy + n * one + at(i)) = S[i];
+        }
+    } else {
+        for (int i0 = 0; i0 < k; ++i0) {   // S <- decay S + state
+            const size_t j = i0 == 0 ? n : later + i0;
+            const float d = i0 > 0 ? seg.decay[j * H + h] : 0.f;
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                S[i] = ffma2(make_float2(d, d), S[i], *reinterpret_cast<const float2 *>(seg.state + j * one + at(i)));
+        }
     }
     const float dw = Dw ? __ldg(Dw + h) : 0.f;
-    if (begin < end) load(begin, stages[0]);
-    for (int t0 = begin, k = 0; t0 < end; t0 += SCAN_TOK, ++k) {
+    float decay = 1.f;
+    for (int t0 = begin, b = 0; t0 < end; t0 += SCAN_TOK, b ^= 1) {
         const int len = min(SCAN_TOK, end - t0);
-        const Stage &st = stages[k & 1];
+        const Stage &st = stages[b];
         if (t0 + SCAN_TOK < end) {
-            load(t0 + SCAN_TOK, stages[(k + 1) & 1]);
+            load(t0 + SCAN_TOK, stages[b ^ 1]);
             asm volatile("cp.async.wait_group 1;" ::: "memory");
         } else {
             asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -163,49 +212,51 @@ ssm_scan_kernel(const float *__restrict__ act, const float2 *__restrict__ step, 
                 const float a = r + u < len ? da.y : 1.f;
                 const float2 x = *reinterpret_cast<const float2 *>(&st.x[r + u][lcol]);
                 const float2 dx = make_float2(da.x * x.x, da.x * x.y), aa = make_float2(a, a);
+                if (STATE_ONLY) decay *= a;
                 float2 y = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int i4 = 0; i4 < R / 4; ++i4) {
                     const float4 b = *reinterpret_cast<const float4 *>(&st.b[r + u][32 * i4 + 4 * slice]);
-                    const float4 c = *reinterpret_cast<const float4 *>(&st.c[r + u][32 * i4 + 4 * slice]);
+                    const float4 c = STATE_ONLY ? b : *reinterpret_cast<const float4 *>(&st.c[r + u][32 * i4 + 4 * slice]);
                     const float bb[4] = {b.x, b.y, b.z, b.w}, cc[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         float2 &s = S[4 * i4 + e];
                         s = ffma2(aa, s, fmul2(make_float2(bb[e], bb[e]), dx));
-                        y = ffma2(make_float2(cc[e], cc[e]), s, y);
+                        if (!STATE_ONLY) y = ffma2(make_float2(cc[e], cc[e]), s, y);
                     }
                 }
                 v[2 * u] = y.x;
                 v[2 * u + 1] = y.y;
             }
+            if constexpr (!STATE_ONLY) {
 #pragma unroll
-            for (int o = 4; o > 0; o >>= 1) {
-                const bool up = slice & o;
+                for (int o = 4; o > 0; o >>= 1) {
+                    const bool up = slice & o;
 #pragma unroll
-                for (int i = 0; i < o; ++i) {
-                    const float give = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
-                    v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                    for (int i = 0; i < o; ++i) {
+                        const float give = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
+                        v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                    }
                 }
-            }
-            const int ru = r + (slice >> 1), cu1 = lcol + (slice & 1);   // this lane's token and column
-            if (ru < len) {
-                const long long t = t0 + ru;
-                const int p = p0 + cu1;
-                float o = fmaf(dw, st.x[ru][cu1], v[0]);
-                if (z) o *= ssm::silu(to_f32(z[t * ld_z + (long long)h * P + p]));
-                out[(t * H + h) * P + p] = from_f32<Tout>(o);
+                const int ru = r + (slice >> 1), cu1 = lcol + (slice & 1);   // this lane's token and column
+                if (ru < len) {
+                    const long long t = t0 + ru;
+                    const int p = p0 + cu1;
+                    float o = fmaf(dw, st.x[ru][cu1], v[0]);
+                    if (z) o *= ssm::silu(to_f32(z[t * ld_z + (long long)h * P + p]));
+                    out[(t * H + h) * P + p] = from_f32<Tout>(o);
+                }
             }
         }
         __syncthreads();   // before the stage is loaded again
     }
-    if (S_final) {
+    float *const to = STATE_ONLY ? seg.state + slot * one : k == last && S_final ? S_final + n * one : nullptr;
+    if (to) {
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const int row = 32 * (i / 4) + 4 * slice + (i & 3);
-            *reinterpret_cast<float2 *>(S_final + sbase + (size_t)row * P) = S[i];
-        }
+        for (int i = 0; i < R; ++i) *reinterpret_cast<float2 *>(to + at(i)) = S[i];
     }
+    if (STATE_ONLY && p0 == 0 && tid == 0) seg.decay[(size_t)slot * H + h] = decay;
 }
 
 // tail [n, j] = the raw channels of token end - 3 + j of sequence n, or the row of
@@ -240,22 +291,66 @@ cudaError_t launch_tail(const SsmArgs &a) {
     return launched();
 }
 
+size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// Workspace of the fp32 prefill, and its segments.  A block alone on an SM takes 126 ns a
+// token, a full SM 58 per block (N = 128), and segments cost half as much again for their
+// states.  So they are made where the sequences have no more blocks than there are SMs,
+// SCAN_FULL of them an SM, of the sequences that are longer than an even share of the work
+// (one of 8000 tokens, 16 heads of 64, N = 128: 1009 us whole, 471 with 3 to an SM, 333
+// with 6, 348 with 10; 4 of 2000 with 32 heads, more blocks than SMs: 467 whole, 697 cut).
+struct ScanPlan {
+    int from, len, slots;
+    size_t act, step, state, decay, s0_copy;
+    size_t bytes() const { return act + step + state + decay + s0_copy; }
+};
+constexpr int SCAN_FULL = 6, SCAN_MIN = 64;
+
+ScanPlan scan_plan(const SsmArgs &a, int sms) {
+    ScanPlan p = {};
+    const size_t chans = (size_t)a.H * a.P + 2 * (size_t)a.G * a.N, one = (size_t)a.H * a.N * a.P * 4;
+    p.act = round256((size_t)a.n_tok * chans * 4);
+    p.step = round256((size_t)a.n_tok * a.H * 8);
+    p.slots = a.n_seq;
+    p.from = INT_MAX;
+    p.len = 1;
+    const long long blocks = (long long)a.H * a.P / SCAN_COLS, all = a.n_seq * blocks;
+    const long long len = all <= sms ? a.n_tok * blocks / (SCAN_FULL * sms - all) / SCAN_TOK * SCAN_TOK + SCAN_TOK : 0;
+    const long long even = a.n_tok * blocks / sms;
+    const int longest = a.cu_seqlens ? a.n_tok : a.n_tok / a.n_seq;
+    if (all <= sms && longest >= 2 * SCAN_MIN) {
+        p.len = len > SCAN_MIN ? (int)len : SCAN_MIN;
+        p.from = even > 2 * p.len ? (int)even : 2 * p.len;
+        p.slots += a.n_tok / p.len;
+        p.state = round256(p.slots * one);
+        p.decay = round256((size_t)p.slots * a.H * 4);
+        p.s0_copy = round256(a.n_seq * one);
+    }
+    return p;
+}
+
 template <int N, typename T, typename Tout>
-cudaError_t launch_scan(const SsmArgs &a, const float *act, const float2 *step) {
-    const dim3 grid(a.P / SCAN_COLS, a.H, a.n_seq);
-    ssm_scan_kernel<N, T, Tout><<<grid, SCAN_THREADS, 0, a.stream>>>(act, step, a.D, static_cast<const T *>(a.z), a.ld_z, a.S0,
-                                                            a.cu_seqlens, a.n_seq, a.n_tok, a.H, a.G, a.P,
-                                                            static_cast<Tout *>(a.out), a.S_final);
+cudaError_t launch_scan(const SsmArgs &a, const float *act, const float2 *step, const ScanPlan &p, const Segments &seg) {
+    const dim3 grid(a.H * (a.P / SCAN_COLS), p.slots);
+    if (p.from < INT_MAX) {
+        ssm_scan_kernel<N, T, Tout, true><<<grid, SCAN_THREADS, 0, a.stream>>>(
+            act, step, a.D, static_cast<const T *>(a.z), a.ld_z, a.S0, a.cu_seqlens, a.n_seq, a.n_tok, a.H, a.G, a.P,
+            seg, static_cast<Tout *>(a.out), a.S_final);
+        const cudaError_t e = launched();
+        if (e != cudaSuccess) return e;
+    }
+    ssm_scan_kernel<N, T, Tout, false><<<grid, SCAN_THREADS, 0, a.stream>>>(
+        act, step, a.D, static_cast<const T *>(a.z), a.ld_z, a.S0, a.cu_seqlens, a.n_seq, a.n_tok, a.H, a.G, a.P, seg,
+        static_cast<Tout *>(a.out), a.S_final);
     return launched();
 }
 
-size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
-
 template <typename T, typename Tout>
-cudaError_t launch_fp32(const SsmArgs &a, char *ws) {
+cudaError_t launch_fp32(const SsmArgs &a, char *ws, int sms) {
+    const ScanPlan p = scan_plan(a, sms);
     const int chans = a.H * a.P + 2 * a.G * a.N;
     float *act = reinterpret_cast<float *>(ws);
-    float2 *step = reinterpret_cast<float2 *>(ws + round256((size_t)a.n_tok * chans * 4));
+    float2 *step = reinterpret_cast<float2 *>(ws + p.act);
     if (a.n_tok > 0) {
         const dim3 grid((a.n_tok + ACT_TOK - 1) / ACT_TOK, (chans / 4 + a.H + 255) / 256);
         ssm_act_kernel<T><<<grid, 256, 0, a.stream>>>(raw_of<T>(a), static_cast<const T *>(a.hist), a.conv_w, a.conv_b,
@@ -264,24 +359,26 @@ cudaError_t launch_fp32(const SsmArgs &a, char *ws) {
         const cudaError_t e = launched();
         if (e != cudaSuccess) return e;
     }
-    return a.N == 128 ? launch_scan<128, T, Tout>(a, act, step) : launch_scan<64, T, Tout>(a, act, step);
+    char *const w = ws + p.act + p.step;
+    const Segments seg = {p.from, p.len, p.slots, reinterpret_cast<float *>(w), reinterpret_cast<float *>(w + p.state),
+                          p.s0_copy && a.S0 && a.S0 == a.S_final ? reinterpret_cast<float *>(w + p.state + p.decay) : nullptr};
+    return a.N == 128 ? launch_scan<128, T, Tout>(a, act, step, p, seg) : launch_scan<64, T, Tout>(a, act, step, p, seg);
 }
 
 }  // namespace
 
 size_t ssm_workspace_bytes(const SsmArgs &a, int sms) {
     if (ssm_tc_supported(a)) return ssm_tc_workspace_bytes(a, sms);
-    const size_t chans = (size_t)a.H * a.P + 2 * (size_t)a.G * a.N;
-    return round256((size_t)a.n_tok * chans * 4) + round256((size_t)a.n_tok * a.H * 8);
+    return scan_plan(a, sms).bytes();
 }
 
 cudaError_t launch_ssm_prefill(const SsmArgs &a, void *ws, int sms) {
     cudaError_t e;
     if (ssm_tc_supported(a)) e = launch_ssm_tc(a, ws, sms);
-    else if (a.in_bf16) e = launch_fp32<bf16, float>(a, static_cast<char *>(ws));
+    else if (a.in_bf16) e = launch_fp32<bf16, float>(a, static_cast<char *>(ws), sms);
     else {
-        e = a.out_bf16 ? launch_fp32<float, bf16>(a, static_cast<char *>(ws))
-                       : launch_fp32<float, float>(a, static_cast<char *>(ws));
+        e = a.out_bf16 ? launch_fp32<float, bf16>(a, static_cast<char *>(ws), sms)
+                       : launch_fp32<float, float>(a, static_cast<char *>(ws), sms);
     }
     if (e != cudaSuccess || !a.tail) return e;
     // last: every reader of the history has finished, so the tail may replace it
