@@ -340,8 +340,8 @@ struct ChainArgs {
     float *S_final;
     float *seg_state;   // [n_seq][blocks][n_seg - 1][N][128], then decays [n_seq][blocks][n_seg - 1][2]
     float *seg_decay;
-    float *s0_copy;     // [n_seq][H][N][P] when S_final may be S0
-    int n_seq, n_tok, H, G, P, blocks_per_group, seg_chunks, n_seg;
+    int n_seq, n_tok, H, G, P, blocks_per_group, n_seg;
+    int seg0;                       // the main pass's first segment
 };
 struct ChainMaps {
     CUtensorMap z, out;   // [N_tok][H P], boxes of 64 columns x 64 tokens
@@ -349,6 +349,7 @@ struct ChainMaps {
 }  // namespace
 
 namespace stc {
+constexpr int MIN_SEG = 3;   // chunks of a segment
 template <int N> struct Smem {
     static constexpr int TILE = (N / 64) * KB;
     static constexpr int OFF_X = 2 * TILE;             // x'' fp16, token rows x 128 columns (two 64-column blocks)
@@ -366,11 +367,11 @@ template <int N> struct Smem {
 static_assert(Smem<128>::SIZE <= 232448, "227 KB per block");
 }  // namespace stc
 
-// STATE_ONLY: segment k of a split sequence, from zero (segment 0: from S0) to its
-// final state in seg_state.  Otherwise the whole mixer over the segment.
+// One CTA per 128 columns of a sequence's segment.  STATE_ONLY: only the state, from zero,
+// into seg_state with the product of its decays.  Otherwise the whole mixer over the
+// segment.
 template <int N, bool STATE_ONLY>
-__global__ void __launch_bounds__(stc::THREADS, 1)
-ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
+__device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMaps &maps, const int seg) {
     using namespace stc;
     using Sm = Smem<N>;
     extern __shared__ uint8_t smem_raw[];
@@ -385,7 +386,7 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
     int *odd = reinterpret_cast<int *>(sm + Sm::OFF_ODD);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int q = warp & 3, cg = warp >> 2;
-    const int blk = blockIdx.x, n = blockIdx.y, seg = blockIdx.z;
+    const int blk = blockIdx.x, n = blockIdx.y;
     // columns: heads h0 + half * (P == 64); the second half of a group's last block may be empty
     const int R = a.H / a.G, g = blk / a.blocks_per_group, bi = blk % a.blocks_per_group;
     const int col0 = bi * 128, gcols = R * a.P;                       // columns within the group
@@ -396,11 +397,15 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
     int begin, end;
     seq_range(a.cu, a.n_seq, a.n_tok, n, begin, end);
     const int all_chunks = (end - begin + Q - 1) / Q;
-    const int c_lo = seg * a.seg_chunks, c_hi = min(c_lo + a.seg_chunks, all_chunks);
+    // this sequence's segments: MIN_SEG chunks each at least, the first half as long as the others
+    const int parts = min(a.n_seg, all_chunks / MIN_SEG);
+    const int seg_chunks = parts < 3 ? max(all_chunks, 1) : (2 * all_chunks + 2 * parts - 2) / (2 * parts - 1);
+    const int first = parts < 3 ? seg_chunks : (seg_chunks + 1) / 2;
+    const int c_lo = seg == 0 ? 0 : first + (seg - 1) * seg_chunks;
+    const int c_hi = min(seg == 0 ? first : c_lo + seg_chunks, all_chunks);
     const int chunks = max(0, c_hi - c_lo);
-    const int last_seg = all_chunks > 0 ? (all_chunks - 1) / a.seg_chunks : 0;
-    // state pass: every segment but a sequence's last; else the segments it has
-    if (STATE_ONLY ? (seg >= last_seg && !(seg == 0 && a.s0_copy)) : seg > last_seg) return;
+    const int last_seg = all_chunks > first ? (all_chunks - first - 1) / seg_chunks + 1 : 0;
+    if (STATE_ONLY ? seg >= last_seg : seg > last_seg) return;   // a last segment's state has no reader
     const int slot0 = first_slot(begin, n) + c_lo;
 
     // ---- the state of a computing thread: row 32 q + lane, columns 32 cg .. + 31 of the block
@@ -412,13 +417,6 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
     const size_t sbase = (((size_t)n * a.H + shead) * N + srow) * a.P + spc;
     const size_t seg_base = ((size_t)n * gridDim.x + blk) * (a.n_seg - 1);   // of this chain's segments
     auto seg_ptr = [&](int k) { return a.seg_state + ((seg_base + k) * N + srow) * 128 + sc0; };
-    if (STATE_ONLY && seg == 0 && a.s0_copy && owner) {
-#pragma unroll
-        for (int j = 0; j < 32; j += 4)
-            *reinterpret_cast<float4 *>(a.s0_copy + sbase + j) = *reinterpret_cast<const float4 *>(a.S0 + sbase + j);
-    }
-    if (STATE_ONLY && seg >= last_seg) return;   // only the copy of S0 was wanted
-
     if (warp == MMA_WARP) umma::tmem_alloc(tslot, 512);
     if (tid == 0) {
         for (int i = 0; i < 9; ++i) umma::mbar_init(full + i, i < 7 ? 1 : CWARPS);
@@ -617,7 +615,7 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
         if (owner) {
             // the initial state, or the segments before this one joined: I <- decay I + state
             const bool joined = !STATE_ONLY && seg > 0;
-            const float *p = joined ? seg_ptr(0) : seg > 0 || !a.S0 ? nullptr : (!STATE_ONLY && a.s0_copy ? a.s0_copy : a.S0) + sbase;
+            const float *p = joined ? seg_ptr(0) : seg > 0 || !a.S0 ? nullptr : a.S0 + sbase;
             for (int k = 0; p && k < (joined ? seg : 1); ++k) {
                 if (k > 0) p = seg_ptr(k);
                 const float d = k > 0 ? __ldg(a.seg_decay + (seg_base + k) * 2 + (cg >> 1)) : 0.f;
@@ -925,10 +923,10 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
             gate(chunks - 1);
             meet();
         }
-        float *const to = !owner || *abort_flag         ? nullptr
-                          : STATE_ONLY                  ? seg_ptr(seg)
-                          : seg == last_seg && a.S_final ? a.S_final + sbase
-                                                         : nullptr;
+        float *const to = !owner || *abort_flag                         ? nullptr
+                          : STATE_ONLY || (seg == 0 && last_seg > 0)    ? seg_ptr(seg)
+                          : seg == last_seg && a.S_final                ? a.S_final + sbase
+                                                                        : nullptr;
         if (to) {
             if (odd[128]) {
 #pragma unroll
@@ -956,17 +954,32 @@ ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
     if (warp == MMA_WARP) umma::tmem_dealloc(tb, 512);
 }
 
+// FIRST: the mixer over segment 0, and beside it the states of the segments behind it.
+// Else the mixer over the segments from seg0 on.
+template <int N, bool FIRST>
+__global__ void __launch_bounds__(stc::THREADS, 1)
+ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
+    if (FIRST && blockIdx.z > 0) chain_segment<N, true>(a, maps, blockIdx.z);
+    else chain_segment<N, false>(a, maps, FIRST ? 0 : a.seg0 + blockIdx.z);
+}
+
 namespace {
 
 size_t round256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 struct Plan {
-    int blocks_per_group, blocks, slots, seg_chunks, n_seg;
-    size_t tiles, rec, seg_state, seg_decay, s0_copy, bytes;
+    int blocks_per_group, blocks, slots, n_seg;
+    size_t tiles, rec, seg_state, seg_decay, bytes;
 };
 
-// Segments: a chain (128 columns of a sequence) is sequential over its chunks, so with
-// fewer chains than SMs the sequence is cut and a first pass finds the segments' states.
+// Segments: a chain (128 columns of a sequence) is sequential over its chunks, 4.6 us each
+// however many chains there are.  With fewer than half as many chains as SMs a sequence is
+// cut in sms / chains + 1: a first launch runs segment 0, half as long, and beside it the
+// states of the others, which take 2.4 us a chunk; a second one the others.  One prompt of
+// 32768 tokens, 32 heads of 128, N = 128: 793 us (885 with four equal segments, the state
+// of the first three by themselves before); 2 x 2048 tokens, 64 heads of 64: 161 us uncut, 130.
+// Pieces of 2, 3 or 4 chunks at least: 768 tokens, 32 heads of 64: 56, 58, 65 us; 400
+// tokens, 16 heads: 51, 49, 49.
 Plan plan_for(const SsmArgs &a, int sms) {
     Plan p;
     const int R = a.H / a.G;
@@ -975,22 +988,17 @@ Plan plan_for(const SsmArgs &a, int sms) {
     p.slots = a.n_tok / stc::Q + a.n_seq;
     const long long chains = (long long)p.blocks * a.n_seq;
     const int longest = a.cu_seqlens ? a.n_tok : a.n_tok / a.n_seq;
-    const int max_chunks = (longest + stc::Q - 1) / stc::Q;
     p.n_seg = 1;
     if (chains * 2 <= sms) {
-        const int k = (int)(sms / chains);
-        p.n_seg = max_chunks / 4 < k ? max_chunks / 4 : k;
-        if (p.n_seg < 1) p.n_seg = 1;
+        const int most = (int)(sms / chains) + 1, pieces = (longest + stc::Q - 1) / stc::Q / stc::MIN_SEG;
+        p.n_seg = most < pieces ? most : pieces;
+        if (p.n_seg < 3) p.n_seg = 1;
     }
-    p.seg_chunks = (max_chunks + p.n_seg - 1) / p.n_seg;
-    if (p.seg_chunks < 1) p.seg_chunks = 1;
-    p.n_seg = max_chunks > 0 ? (max_chunks + p.seg_chunks - 1) / p.seg_chunks : 1;
     p.tiles = round256((size_t)p.slots * a.G * (a.N / 64) * stc::KB);
     p.rec = round256((size_t)p.slots * a.H * stc::REC * 4);
     p.seg_state = round256((size_t)chains * (p.n_seg - 1) * a.N * 128 * 4);
     p.seg_decay = round256((size_t)chains * (p.n_seg - 1) * 2 * 4);
-    p.s0_copy = p.n_seg > 1 ? round256((size_t)a.n_seq * a.H * a.N * a.P * 4) : 0;
-    p.bytes = p.tiles + p.rec + p.seg_state + p.seg_decay + p.s0_copy;
+    p.bytes = p.tiles + p.rec + p.seg_state + p.seg_decay;
     return p;
 }
 
@@ -1021,12 +1029,9 @@ cudaError_t launch_tc(const SsmArgs &a, char *ws, int sms) {
     ca.S_final = a.S_final;
     ca.seg_state = reinterpret_cast<float *>(ws + p.tiles + p.rec);
     ca.seg_decay = reinterpret_cast<float *>(ws + p.tiles + p.rec + p.seg_state);
-    // segment 0 reads the initial state while the last one writes the final one
-    ca.s0_copy = p.n_seg > 1 && a.S0 && a.S0 == a.S_final
-                     ? reinterpret_cast<float *>(ws + p.tiles + p.rec + p.seg_state + p.seg_decay) : nullptr;
     ca.n_seq = a.n_seq; ca.n_tok = a.n_tok; ca.H = a.H; ca.G = a.G; ca.P = a.P;
     ca.blocks_per_group = p.blocks_per_group;
-    ca.seg_chunks = p.seg_chunks;
+    ca.seg0 = p.n_seg > 1 ? 1 : 0;
     ca.n_seg = p.n_seg;
     cudaError_t e;
     if (a.n_tok > 0) {
@@ -1053,7 +1058,7 @@ cudaError_t launch_tc(const SsmArgs &a, char *ws, int sms) {
         ssm_chain_kernel<N, true><<<dim3(p.blocks, a.n_seq, p.n_seg - 1), stc::THREADS, SMEM, a.stream>>>(ca, maps);
         if ((e = launched()) != cudaSuccess) return e;
     }
-    ssm_chain_kernel<N, false><<<dim3(p.blocks, a.n_seq, p.n_seg), stc::THREADS, SMEM, a.stream>>>(ca, maps);
+    ssm_chain_kernel<N, false><<<dim3(p.blocks, a.n_seq, p.n_seg > 1 ? p.n_seg - 1 : 1), stc::THREADS, SMEM, a.stream>>>(ca, maps);
     return launched();
 }
 
