@@ -543,14 +543,18 @@ def _token_ld(name, t, shape, dtype):
     if t.dtype is not dtype or t.shape != shape:
         _bad(name, t, shape, dtype)
     st = t.stride()
-    want = 1
-    for i in range(len(shape) - 1, 0, -1):
-        if st[i] != want and shape[i] != 1:
-            raise ValueError(f"{name}: the elements of a token must be packed (strides {st})")
-        want *= shape[i]
-    if shape[0] <= 1:
+    if len(shape) == 3:
+        n, rows, width = shape
+        packed = (st[2] == 1 or width == 1) and (st[1] == width or rows == 1)
+        width *= rows
+    else:
+        n, width = shape
+        packed = st[1] == 1 or width == 1
+    if not packed:
+        raise ValueError(f"{name}: the elements of a token must be packed (strides {st})")
+    if n <= 1:
         return 0
-    if st[0] < want:
+    if st[0] < width:
         raise ValueError(f"{name}: tokens overlap (strides {st})")
     return st[0]
 
@@ -630,13 +634,13 @@ def ssm_prefill(x, B, C, dt_logit, conv_w, A, b_dt, *, conv_b=None, D=None, z=No
     else:
         n_seq = num_seqs if num_seqs is not None else (S0.shape[0] if S0 is not None else 1)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
+        out = x.new_empty(x.shape, dtype=x.dtype if out_dtype is None else out_dtype)
     dims, hist, state = _ssm_dims(x, B, C, dt_logit, conv_w, conv_b, A, b_dt, D, z, out, n_seq)
     if want_state:
         if S_final is None:
-            S_final = torch.empty(state, dtype=F32, device=x.device)
+            S_final = A.new_empty(state)
         if conv_tail is None:
-            conv_tail = torch.empty(hist, dtype=x.dtype, device=x.device)
+            conv_tail = x.new_empty(hist)
     _packed("S0", S0, state, F32)
     _packed("S_final", S_final, state, F32)
     _packed("conv_hist", conv_hist, hist, x.dtype)
@@ -663,7 +667,7 @@ def ssm_decode_step(x, B, C, dt_logit, conv_w, conv_hist, A, b_dt, S, *, conv_b=
     [B, H] (rows may lie apart); conv_hist [B, 3, H P + 2 G N] and S [B, H, N, P] advance
     in place.  out_dtype defaults to x.dtype.  Returns out [B, H, P]."""
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
+        out = x.new_empty(x.shape, dtype=x.dtype if out_dtype is None else out_dtype)
     dims, hist, state = _ssm_dims(x, B, C, dt_logit, conv_w, conv_b, A, b_dt, D, z, out, x.shape[0])
     if conv_hist is None or S is None:
         raise ValueError("conv_hist and S are required")
@@ -702,11 +706,11 @@ def quant_fp8(x, block_rows=1, *, q=None, scale=None, stream=None):
         raise ValueError("block_rows: 1 or 128 expected")
     shape = (-(-rows // block_rows), -(-cols // 128))
     if q is None:
-        q = torch.empty((rows, cols), dtype=E4M3, device=x.device)
+        q = x.new_empty((rows, cols), dtype=E4M3)
     elif q.dtype is not E4M3 or q.shape != (rows, cols):
         _bad("q", q, (rows, cols), E4M3)
     if scale is None:
-        scale = torch.empty(shape, dtype=F32, device=x.device)
+        scale = x.new_empty(shape, dtype=F32)
     if x.dtype is not BF16 and x.dtype is not F32:
         raise TypeError(f"x: dtype {x.dtype}, expected {BF16} or {F32}")
     _packed("scale", scale, shape, F32)
@@ -730,7 +734,7 @@ def gemm_fp8(a, a_scale, b, b_scale, *, out=None, out_dtype=torch.bfloat16, stre
     if b.dtype is not E4M3 or b.shape[1] != K:
         _bad("b", b, (N, K), E4M3)
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=a.device)
+        out = a.new_empty((M, N), dtype=out_dtype)
     if out.dtype is not BF16 and out.dtype is not F32:
         raise TypeError(f"out: dtype {out.dtype}, expected {F32} or {BF16}")
     if out.shape != (M, N):
