@@ -379,7 +379,8 @@ __device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMap
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + Sm::OFF_BAR);
     uint64_t *bar_sc = full + 2, *bar_u = full + 3, *bar_y = full + 4, *full_z = full + 5;
     uint64_t *bar_x = full + 7, *bar_w = full + 8;   // the computing warps' operands, and decayed scores, are there
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(full + 9);
+    uint64_t *bar_m = full + 9;   // a chunk's meeting
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(full + 10);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tslot + 1);
     float *cw = reinterpret_cast<float *>(sm + Sm::OFF_CW);
     uint32_t *mx = reinterpret_cast<uint32_t *>(sm + Sm::OFF_MAX);
@@ -419,7 +420,7 @@ __device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMap
     auto seg_ptr = [&](int k) { return a.seg_state + ((seg_base + k) * N + srow) * 128 + sc0; };
     if (warp == MMA_WARP) umma::tmem_alloc(tslot, 512);
     if (tid == 0) {
-        for (int i = 0; i < 9; ++i) umma::mbar_init(full + i, i < 7 ? 1 : CWARPS);
+        for (int i = 0; i < 10; ++i) umma::mbar_init(full + i, i < 7 ? 1 : i < 9 ? CWARPS : CWARPS + 1);
         *abort_flag = 0;
         umma::fence_mbar_init();
     }
@@ -450,9 +451,13 @@ __device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMap
         *abort_flag = 1;
         atomicOr(&g_ssm_err, 1u);
     };
-    // Once a chunk the computing warps and the two that serve them meet: the previous chunk
-    // is done with shared and tensor memory.
-    auto meet = [] { umma::named_bar_sync(1, 32 * (CWARPS + 2)); };
+    // Once a chunk the computing warps and the copying one meet: the previous chunk is done
+    // with shared memory, and the maxima are there.  A warp arrives when its own part is,
+    // and waits where it needs the others'.
+    auto arrive = [&] {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_m);
+    };
 
     if (!computes) {
         regs_dec<SERVE_REGS>();
@@ -485,7 +490,6 @@ __device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMap
             if (!STATE_ONLY && chunks > 0) scores(0);
             for (int c = 0; c < chunks; ++c) {
                 const uint32_t st = (uint32_t)((c & 1) * (Sm::TILE >> 4));
-                meet();
                 wait(bar_x, (uint32_t)c & 1u);
                 __syncwarp();
                 umma::tc_fence_after();
@@ -575,7 +579,9 @@ __device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMap
                 }
             }
             for (int c = 0; c < chunks; ++c) {
-                meet();
+                if (c >= 1) wait(STATE_ONLY ? bar_u : bar_y, (uint32_t)(c - 1) & 1u);   // the products have read the tiles
+                arrive();
+                wait(bar_m, (uint32_t)c & 1u);
                 if (one) {
                     const bool go = *abort_flag == 0;
                     if (c >= 1 && c + 1 < chunks && go) issue(c + 1);
@@ -589,7 +595,8 @@ __device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMap
                 __syncwarp();
             }
             if (!STATE_ONLY && chunks > 0) {
-                meet();
+                arrive();
+                wait(bar_m, (uint32_t)chunks & 1u);
                 if (one) {   // the last two tiles (the last only if it is whole); the copies end before the CTA does
                     if (chunks > 1) store_out(chunks - 2);
                     if (begin + (c_lo + chunks) * Q <= end) store_out(chunks - 1);
@@ -605,7 +612,6 @@ __device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMap
                         umma::mbar_wait_bounded(full_z + b, (uint32_t)((chunks - 1 - b) / 2) & 1u, 1u << 16);
                 }
         }
-        if (!STATE_ONLY && chunks > 0 && warp == MMA_WARP) meet();
     } else {
         regs_inc<COMPUTE_REGS>();
         const uint32_t lane_off = (uint32_t)(32 * q) << 16;
@@ -770,12 +776,13 @@ __device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMap
         // maxima of this chunk, of the next (written from its convolution on) and of the one
         // after (cleared now; its last readers, of the previous chunk, have met since)
         uint32_t *m_now = mx, *m_next = mx + 4, *m_after = mx + 8;
+        arrive();
         for (int c = 0; c < chunks; ++c) {
             const int b = c & 1;
             const uint32_t ph = (uint32_t)c & 1u, ph_full = (uint32_t)(c >> 1) & 1u;
             const float *rec0 = reinterpret_cast<const float *>(sm + Sm::OFF_REC) + b * 2 * REC, *rec1 = rec0 + REC;
             const float *recv = hv ? rec1 : rec0;
-            meet();
+            wait(bar_m, ph);
             if (tid < 4) m_after[tid] = 0;
 
             // ---- scales; operands into shared memory
@@ -891,6 +898,7 @@ __device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMap
                 for (int j = 0; j < 16; ++j) S[j] = ffma2(dec2, S[j], fmul2(add2, as_float2(v[2 * j], v[2 * j + 1])));
                 if (STATE_ONLY) { decay0 *= rec0[R_DEC]; decay1 *= rec1[R_DEC]; }
             }
+            if (STATE_ONLY && c + 1 < chunks) arrive();
             if (!STATE_ONLY) {
                 state_max(m_next);
                 // ---- y before its gate
@@ -900,6 +908,7 @@ __device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMap
                 wait(bar_w, ph);   // x of the other warps
                 const uint4 xa = lds128(p_o), xb = lds128(p_o ^ 16);
                 const uint32_t xw[8] = {xa.x, xa.y, xa.z, xa.w, xb.x, xb.y, xb.z, xb.w};
+                if (c + 1 < chunks) arrive();   // y needs nothing that the others may overwrite
                 wait(bar_y, ph);
                 umma::tc_fence_after();
                 uint32_t yi[16], yw[16];
@@ -921,7 +930,7 @@ __device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMap
         }
         if (!STATE_ONLY && chunks > 0) {
             gate(chunks - 1);
-            meet();
+            arrive();
         }
         float *const to = !owner || *abort_flag                         ? nullptr
                           : STATE_ONLY || (seg == 0 && last_seg > 0)    ? seg_ptr(seg)
