@@ -98,11 +98,15 @@ cudaError_t get_pool(cudaMemPool_t *pool) {
         props.handleTypes = cudaMemHandleTypeNone;
         props.location.type = cudaMemLocationTypeDevice;
         props.location.id = dev;
+        // nothing of this belongs to a stream, so a capture in progress need not end for it
+        cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+        if ((e = cudaThreadExchangeStreamCaptureMode(&mode)) != cudaSuccess) return e;
         cudaMemPool_t p;
         e = cudaMemPoolCreate(&p, &props);
-        if (e != cudaSuccess) return e;
         uint64_t keep = UINT64_MAX;
-        e = cudaMemPoolSetAttribute(p, cudaMemPoolAttrReleaseThreshold, &keep);
+        if (e == cudaSuccess) e = cudaMemPoolSetAttribute(p, cudaMemPoolAttrReleaseThreshold, &keep);
+        const cudaError_t back = cudaThreadExchangeStreamCaptureMode(&mode);
+        if (e == cudaSuccess) e = back;
         if (e != cudaSuccess) return e;
         g_pools[dev] = p;
     }

@@ -1,6 +1,10 @@
 """The selective state-space mixer at its edges: values that are not finite inside a
 sequence, several streams at once, buffers of the caller's own layout, long segmented
 prompts in place, and the wait self-test of its pipelines."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -109,3 +113,66 @@ def test_expired_wait_is_reported(cuda_device, family):
     lens = [70]
     agree(so.make_inputs(lens, 2, 1, P, N, BF16, cuda_device), lens)
     assert gdn.device_error_status() == (0, 0)
+
+
+FIRST_CALLS = """
+import sys, torch
+sys.path.insert(0, "tests")
+import ssm_oracle as so
+from linear_attention_token_shortconv_b200 import gdn
+dev = torch.device("cuda:0")
+ins = [so.make_inputs([700, 300], 4, 1, 64, 128, d, dev) for d in (torch.bfloat16, torch.float32)]
+cu = torch.tensor([0, 700, 1000], dtype=torch.int32, device=dev)
+one = so.make_inputs([1, 1], 4, 1, 64, 128, torch.bfloat16, dev)
+a, b = torch.randn(2048, 512, device=dev), torch.randn(2048, 512, device=dev)
+def calls():
+    outs = []
+    for i in ins:
+        outs += gdn.ssm_prefill(i["x"], i["B"], i["C"], i["dt"], i["conv_w"], i["A"], i["b_dt"], conv_b=i["conv_b"],
+                                D=i["D"], z=i["z"], S0=i["S0"], conv_hist=i["hist"], cu_seqlens=cu)
+    S, hist = one["S0"].clone(), one["hist"].clone()
+    outs += [gdn.ssm_decode_step(one["x"], one["B"], one["C"], one["dt"], one["conv_w"], hist, one["A"], one["b_dt"], S), S]
+    for rows in (2048, 100, 3):
+        outs.append(gdn.gemm_fp8(*gdn.quant_fp8(a[:rows]), *gdn.quant_fp8(b, 128)))
+    return outs
+s = torch.cuda.Stream()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g, stream=s):
+    got = calls()
+g.replay()
+g.replay()
+torch.cuda.synchronize()
+for u, v in zip(got, calls()):
+    assert torch.equal(u, v)
+print("same")
+"""
+
+
+def test_first_calls_of_a_process_captured(cuda_device):
+    """What a first call sets up (attributes, the pool, the pairs that fit) needs no call
+    outside a capture."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stdout[-500:] + r.stderr[-2000:]
+
+
+def test_offsets_out_of_range(cuda_device):
+    """Offsets past the tokens, negative or falling are clamped: the sequences that are
+    well formed come out right and nothing outside out and the states is written."""
+    lens, H = [60, 90, 50], 4
+    for dtype in (F32, BF16):
+        inp = so.make_inputs(lens, H, 1, P, N, dtype, cuda_device, seed=8)
+        clean, Sc, _ = prefill(inp, lens)
+        guard = torch.full((3, H, P), 5.0, dtype=dtype, device=cuda_device)
+        for cu, whole in (([-7, 60, 150, 4000], [0, 1, 2]), ([0, 60, 40, 200], [0])):
+            buf = torch.cat([guard, torch.zeros_like(clean), guard])
+            out, S, _ = gdn.ssm_prefill(inp["x"], inp["B"], inp["C"], inp["dt"], inp["conv_w"], inp["A"], inp["b_dt"],
+                                        conv_b=inp["conv_b"], D=inp["D"], z=inp["z"], S0=inp["S0"],
+                                        conv_hist=inp["hist"], out=buf[3:-3],
+                                        cu_seqlens=torch.tensor(cu, dtype=torch.int32, device=cuda_device))
+            assert torch.equal(buf[:3], guard) and torch.equal(buf[-3:], guard)
+            for n in whole:
+                b, e = sum(lens[:n]), sum(lens[:n + 1])
+                assert torch.equal(S[n], Sc[n])
+                if len(whole) == 3:
+                    assert torch.equal(out[b:e], clean[b:e])
