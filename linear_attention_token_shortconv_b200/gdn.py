@@ -578,6 +578,15 @@ def _addresses(*ts):
     return dev, ptrs
 
 
+def _made(like, shape, dtype, stream):
+    """A result tensor on like's device, of the stream that will write it: what frees it may
+    hand it on to that stream's later work only."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
 def _call(fn, where, dev, stream, *args):
     """Runs a library call on device `dev`, on `stream` or that device's current one."""
     if dev == torch.cuda.current_device():
@@ -634,13 +643,13 @@ def ssm_prefill(x, B, C, dt_logit, conv_w, A, b_dt, *, conv_b=None, D=None, z=No
     else:
         n_seq = num_seqs if num_seqs is not None else (S0.shape[0] if S0 is not None else 1)
     if out is None:
-        out = x.new_empty(x.shape, dtype=x.dtype if out_dtype is None else out_dtype)
+        out = _made(x, x.shape, x.dtype if out_dtype is None else out_dtype, stream)
     dims, hist, state = _ssm_dims(x, B, C, dt_logit, conv_w, conv_b, A, b_dt, D, z, out, n_seq)
     if want_state:
         if S_final is None:
-            S_final = A.new_empty(state)
+            S_final = _made(A, state, F32, stream)
         if conv_tail is None:
-            conv_tail = x.new_empty(hist)
+            conv_tail = _made(x, hist, x.dtype, stream)
     _packed("S0", S0, state, F32)
     _packed("S_final", S_final, state, F32)
     _packed("conv_hist", conv_hist, hist, x.dtype)
@@ -667,7 +676,7 @@ def ssm_decode_step(x, B, C, dt_logit, conv_w, conv_hist, A, b_dt, S, *, conv_b=
     [B, H] (rows may lie apart); conv_hist [B, 3, H P + 2 G N] and S [B, H, N, P] advance
     in place.  out_dtype defaults to x.dtype.  Returns out [B, H, P]."""
     if out is None:
-        out = x.new_empty(x.shape, dtype=x.dtype if out_dtype is None else out_dtype)
+        out = _made(x, x.shape, x.dtype if out_dtype is None else out_dtype, stream)
     dims, hist, state = _ssm_dims(x, B, C, dt_logit, conv_w, conv_b, A, b_dt, D, z, out, x.shape[0])
     if conv_hist is None or S is None:
         raise ValueError("conv_hist and S are required")
@@ -706,11 +715,11 @@ def quant_fp8(x, block_rows=1, *, q=None, scale=None, stream=None):
         raise ValueError("block_rows: 1 or 128 expected")
     shape = (-(-rows // block_rows), -(-cols // 128))
     if q is None:
-        q = x.new_empty((rows, cols), dtype=E4M3)
+        q = _made(x, (rows, cols), E4M3, stream)
     elif q.dtype is not E4M3 or q.shape != (rows, cols):
         _bad("q", q, (rows, cols), E4M3)
     if scale is None:
-        scale = x.new_empty(shape, dtype=F32)
+        scale = _made(x, shape, F32, stream)
     if x.dtype is not BF16 and x.dtype is not F32:
         raise TypeError(f"x: dtype {x.dtype}, expected {BF16} or {F32}")
     _packed("scale", scale, shape, F32)
@@ -734,7 +743,7 @@ def gemm_fp8(a, a_scale, b, b_scale, *, out=None, out_dtype=torch.bfloat16, stre
     if b.dtype is not E4M3 or b.shape[1] != K:
         _bad("b", b, (N, K), E4M3)
     if out is None:
-        out = a.new_empty((M, N), dtype=out_dtype)
+        out = _made(a, (M, N), out_dtype, stream)
     if out.dtype is not BF16 and out.dtype is not F32:
         raise TypeError(f"out: dtype {out.dtype}, expected {F32} or {BF16}")
     if out.shape != (M, N):

@@ -115,6 +115,29 @@ def test_expired_wait_is_reported(cuda_device, family):
     assert gdn.device_error_status() == (0, 0)
 
 
+def test_results_belong_to_their_stream(cuda_device):
+    """A result that is dropped while its stream may still write it is not handed to work
+    of another stream."""
+    i = so.make_inputs([300], 4, 1, P, N, BF16, cuda_device)
+    x = torch.randn(700, 512, device=cuda_device)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    calls = [lambda: gdn.quant_fp8(x, stream=s),
+             lambda: (gdn.gemm_fp8(*gdn.quant_fp8(x, stream=s), *gdn.quant_fp8(x, 128, stream=s), stream=s),),
+             lambda: gdn.ssm_prefill(i["x"], i["B"], i["C"], i["dt"], i["conv_w"], i["A"], i["b_dt"], stream=s),
+             lambda: (gdn.ssm_decode_step(i["x"], i["B"], i["C"], i["dt"], i["conv_w"],
+                                          i["x"].new_zeros(300, 3, i["conv_w"].shape[0]), i["A"], i["b_dt"],
+                                          torch.zeros(300, 4, N, P, device=cuda_device), stream=s),)]
+    for call in calls:
+        torch.cuda.synchronize()
+        results = call()
+        kinds = [(r.data_ptr(), r.shape, r.dtype) for r in results]
+        del results
+        taken = [torch.empty(shape, dtype=dtype, device=cuda_device) for _, shape, dtype in kinds]
+        assert not {t.data_ptr() for t in taken} & {p for p, _, _ in kinds}
+    torch.cuda.synchronize()
+
+
 FIRST_CALLS = """
 import sys, torch
 sys.path.insert(0, "tests")
