@@ -38,6 +38,7 @@ using ssm::seq_range;
 namespace stc {
 constexpr int Q = 64;             // tokens per chunk
 constexpr int PREP_THREADS = 512;
+constexpr int MIN_SEG = 3;        // chunks of a segment
 constexpr int REC = 368;          // floats of one (chunk, head) record
 // record: L log2 e [64] | u [64] | u e^R [64] | 2^ec e^L [64] | 2^ec umax [64] |
 // u e^{L_31 - L} of the first 32 tokens | e^L_end, umax
@@ -156,7 +157,72 @@ struct PrepArgs {
     int n_seq, n_tok, H, G, hp;
     uint8_t *tiles;   // [slot][G][N / 64][KB]
     float *rec;       // [slot][H][REC]
+    int2 *cuts;       // [n_seq]: segments of the sequence, first of its rows
+    int4 *rows;       // [cap]: sequence (-1: none), segment from 1 on, and the sequence's cut
+    int slots;
+    int cap, even;    // rows of segments (0: none); an even share of the chunks
 };
+
+// Chunks of the segments behind the first, which is half as long.
+__device__ __forceinline__ int seg_chunks_of(int chunks, int parts) {
+    return parts < 3 ? max(chunks, 1) : (2 * chunks + 2 * parts - 2) / (2 * parts - 1);
+}
+
+// Which sequences are cut, by one block: those of more than 1.6 even shares, into one
+// segment and as many more as their part of the rows, of MIN_SEG chunks at least; none of
+// them where the longest of the first launch and of the second together are no shorter.
+__device__ void cut_sequences(const PrepArgs &a) {
+    constexpr int WARPS = stc::PREP_THREADS / 32;
+    __shared__ int sums[5][WARPS];
+    const int n = threadIdx.x, lane = n & 31, warp = n >> 5;
+    int chunks = 0;
+    if (n < a.n_seq) {
+        int begin, end;
+        ssm::seq_range(a.cu, a.n_seq, a.n_tok, n, begin, end);
+        chunks = (end - begin + stc::Q - 1) / stc::Q;
+    }
+    const bool is_long = 5LL * chunks > 8LL * a.even;
+    const int part = __reduce_add_sync(0xffffffffu, is_long ? chunks : 0);
+    if (lane == 0) sums[0][warp] = part;
+    __syncthreads();
+    long long all = 0;
+    for (int w = 0; w < WARPS; ++w) all += sums[0][w];
+    int more = is_long ? (int)min((long long)a.cap * chunks / all, (long long)chunks / stc::MIN_SEG - 1) : 0;
+    if (more < 2) more = 0;   // two segments would run one after the other
+    // longest whole, of the first launch (a state's chunk takes half as long) and of the second
+    const int s = seg_chunks_of(chunks, 1 + more), first = more ? (s + 1) / 2 : chunks;
+    const int l = __reduce_max_sync(0xffffffffu, chunks), f = __reduce_max_sync(0xffffffffu, max(first, more ? (s * 17) / 32 : 0));
+    const int r2 = __reduce_max_sync(0xffffffffu, more ? s : 0);
+    if (lane == 0) {
+        sums[1][warp] = l;
+        sums[2][warp] = f;
+        sums[3][warp] = r2;
+    }
+    __syncthreads();
+    int whole = 0, one = 0, two = 0;
+    for (int w = 0; w < WARPS; ++w) {
+        whole = max(whole, sums[1][w]);
+        one = max(one, sums[2][w]);
+        two = max(two, sums[3][w]);
+    }
+    if (one + two + 2 >= whole) more = 0;
+    int upto = more;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+    }
+    if (lane == 31) sums[4][warp] = upto;
+    __syncthreads();
+    int total = 0;
+    for (int w = 0; w < WARPS; ++w) {
+        if (w < warp) upto += sums[4][w];
+        total += sums[4][w];
+    }
+    if (n < a.n_seq) a.cuts[n] = make_int2(1 + more, upto - more);
+    for (int k = 0; k < more; ++k) a.rows[upto - more + k] = make_int4(n, 1 + k, 1 + more, upto - more);
+    for (int r = total + n; r < a.cap; r += stc::PREP_THREADS) a.rows[r] = make_int4(-1, 0, 0, 0);
+}
 
 }  // namespace
 
@@ -168,6 +234,10 @@ __global__ void __launch_bounds__(stc::PREP_THREADS, 2) ssm_prep_kernel(const Pr
     __shared__ float dts[Q][33];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int slot = blockIdx.x, g = blockIdx.y;
+    if (slot == a.slots) {   // one more block
+        if (g == 0) cut_sequences(a);
+        return;
+    }
     // the sequence whose first slot is the last one at or before this slot
     int lo = 0, hi = a.n_seq, begin, end;
     while (hi - lo > 1) {
@@ -338,10 +408,12 @@ struct ChainArgs {
     const float *rec;
     bf16 *out;
     float *S_final;
-    float *seg_state;   // [n_seq][blocks][n_seg - 1][N][128], then decays [n_seq][blocks][n_seg - 1][2]
-    float *seg_decay;
-    int n_seq, n_tok, H, G, P, blocks_per_group, n_seg;
-    int seg0;                       // the main pass's first segment
+    float *seg_state;   // [cap][blocks][N][128]: of segment k of a sequence in row first + k
+    float *seg_decay;   // [cap][blocks][2]
+    const int2 *cuts;   // as in PrepArgs
+    const int4 *rows;
+    int n_seq, n_tok, H, G, P, blocks_per_group;
+    int cap;            // rows of segments; 0: no sequence is cut
 };
 struct ChainMaps {
     CUtensorMap z, out;   // [N_tok][H P], boxes of 64 columns x 64 tokens
@@ -349,7 +421,6 @@ struct ChainMaps {
 }  // namespace
 
 namespace stc {
-constexpr int MIN_SEG = 3;   // chunks of a segment
 template <int N> struct Smem {
     static constexpr int TILE = (N / 64) * KB;
     static constexpr int OFF_X = 2 * TILE;             // x'' fp16, token rows x 128 columns (two 64-column blocks)
@@ -371,7 +442,8 @@ static_assert(Smem<128>::SIZE <= 232448, "227 KB per block");
 // into seg_state with the product of its decays.  Otherwise the whole mixer over the
 // segment.
 template <int N, bool STATE_ONLY>
-__device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMaps &maps, const int seg) {
+__device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMaps &maps, const int n, const int seg,
+                                              const int2 cut) {
     using namespace stc;
     using Sm = Smem<N>;
     extern __shared__ uint8_t smem_raw[];
@@ -387,7 +459,7 @@ __device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMap
     int *odd = reinterpret_cast<int *>(sm + Sm::OFF_ODD);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int q = warp & 3, cg = warp >> 2;
-    const int blk = blockIdx.x, n = blockIdx.y;
+    const int blk = blockIdx.x;
     // columns: heads h0 + half * (P == 64); the second half of a group's last block may be empty
     const int R = a.H / a.G, g = blk / a.blocks_per_group, bi = blk % a.blocks_per_group;
     const int col0 = bi * 128, gcols = R * a.P;                       // columns within the group
@@ -398,10 +470,7 @@ __device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMap
     int begin, end;
     seq_range(a.cu, a.n_seq, a.n_tok, n, begin, end);
     const int all_chunks = (end - begin + Q - 1) / Q;
-    // this sequence's segments: MIN_SEG chunks each at least, the first half as long as the others
-    const int parts = min(a.n_seg, all_chunks / MIN_SEG);
-    const int seg_chunks = parts < 3 ? max(all_chunks, 1) : (2 * all_chunks + 2 * parts - 2) / (2 * parts - 1);
-    const int first = parts < 3 ? seg_chunks : (seg_chunks + 1) / 2;
+    const int seg_chunks = seg_chunks_of(all_chunks, cut.x), first = cut.x < 3 ? seg_chunks : (seg_chunks + 1) / 2;
     const int c_lo = seg == 0 ? 0 : first + (seg - 1) * seg_chunks;
     const int c_hi = min(seg == 0 ? first : c_lo + seg_chunks, all_chunks);
     const int chunks = max(0, c_hi - c_lo);
@@ -416,8 +485,9 @@ __device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMap
     const int shead = cg < 2 ? head0 : head1;
     const int spc = a.P == 64 ? sc0 & 63 : sc0;                       // column within the head
     const size_t sbase = (((size_t)n * a.H + shead) * N + srow) * a.P + spc;
-    const size_t seg_base = ((size_t)n * gridDim.x + blk) * (a.n_seg - 1);   // of this chain's segments
-    auto seg_ptr = [&](int k) { return a.seg_state + ((seg_base + k) * N + srow) * 128 + sc0; };
+    auto seg_at = [&](int k) { return (size_t)(cut.y + k) * gridDim.x + blk; };
+    auto seg_ptr = [&](int k) { return a.seg_state + (seg_at(k) * N + srow) * 128 + sc0; };
+
     if (warp == MMA_WARP) umma::tmem_alloc(tslot, 512);
     if (tid == 0) {
         for (int i = 0; i < 10; ++i) umma::mbar_init(full + i, i < 7 ? 1 : i < 9 ? CWARPS : CWARPS + 1);
@@ -624,7 +694,7 @@ __device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMap
             const float *p = joined ? seg_ptr(0) : seg > 0 || !a.S0 ? nullptr : a.S0 + sbase;
             for (int k = 0; p && k < (joined ? seg : 1); ++k) {
                 if (k > 0) p = seg_ptr(k);
-                const float d = k > 0 ? __ldg(a.seg_decay + (seg_base + k) * 2 + (cg >> 1)) : 0.f;
+                const float d = k > 0 ? __ldg(a.seg_decay + seg_at(k) * 2 + (cg >> 1)) : 0.f;
 #pragma unroll
                 for (int j = 0; j < 16; j += 2) {
                     const float4 v = *reinterpret_cast<const float4 *>(p + 2 * j);
@@ -948,7 +1018,7 @@ __device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMap
             for (int j = 0; j < 16; j += 2)
                 *reinterpret_cast<float4 *>(to + 2 * j) = make_float4(S[j].x, S[j].y, S[j + 1].x, S[j + 1].y);
             if (STATE_ONLY && lane == 0 && q == 0 && (cg & 1) == 0)
-                a.seg_decay[(seg_base + seg) * 2 + (cg >> 1)] = cg < 2 ? decay0 : decay1;
+                a.seg_decay[seg_at(seg) * 2 + (cg >> 1)] = cg < 2 ? decay0 : decay1;
         }
     }
     umma::tc_fence_before();
@@ -963,13 +1033,24 @@ __device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMap
     if (warp == MMA_WARP) umma::tmem_dealloc(tb, 512);
 }
 
-// FIRST: the mixer over segment 0, and beside it the states of the segments behind it.
-// Else the mixer over the segments from seg0 on.
+// FIRST: the mixer over segment 0 of every sequence, and behind them the states of the
+// segments that follow.  Else the mixer over those; or, with no cuts, over every sequence.
 template <int N, bool FIRST>
 __global__ void __launch_bounds__(stc::THREADS, 1)
 ssm_chain_kernel(const ChainArgs a, const __grid_constant__ ChainMaps maps) {
-    if (FIRST && blockIdx.z > 0) chain_segment<N, true>(a, maps, blockIdx.z);
-    else chain_segment<N, false>(a, maps, FIRST ? 0 : a.seg0 + blockIdx.z);
+    const int y = blockIdx.y;
+    if (FIRST && y < a.n_seq) {
+        chain_segment<N, false>(a, maps, y, 0, __ldg(a.cuts + y));
+        return;
+    }
+    int2 at = make_int2(y, 0), cut = make_int2(1, 0);
+    if (FIRST || a.cap > 0) {
+        const int4 row = __ldg(a.rows + (FIRST ? y - a.n_seq : y));
+        if (row.x < 0) return;
+        at = make_int2(row.x, row.y);
+        cut = make_int2(row.z, row.w);
+    }
+    chain_segment<N, FIRST>(a, maps, at.x, at.y, cut);
 }
 
 namespace {
@@ -977,16 +1058,20 @@ namespace {
 size_t round256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 struct Plan {
-    int blocks_per_group, blocks, slots, n_seg;
-    size_t tiles, rec, seg_state, seg_decay, bytes;
+    int blocks_per_group, blocks, slots, cap, even;
+    size_t tiles, rec, seg_state, seg_decay, cuts, rows, bytes;
 };
 
 // Segments: a chain (128 columns of a sequence) is sequential over its chunks, 4.6 us each
-// however many chains there are.  With fewer than half as many chains as SMs a sequence is
-// cut in sms / chains + 1: a first launch runs segment 0, half as long, and beside it the
-// states of the others, which take 2.4 us a chunk; a second one the others.  One prompt of
-// 32768 tokens, 32 heads of 128, N = 128: 793 us (885 with four equal segments, the state
-// of the first three by themselves before); 2 x 2048 tokens, 64 heads of 64: 161 us uncut, 130.
+// however many chains there are, so long sequences are cut while SMs would be idle.  A
+// first launch runs segment 0, half as long, of every sequence and beside it the states of
+// the others, which take 2.4 us a chunk; a second one the others, as many as there are SMs
+// (cap rows of blocks).  The lengths are on the device, so ssm_prep shares the rows out.
+// Cut and whole, us: one prompt of 32768 tokens, 32 heads of 128, N = 128: 801 (885 with
+// four equal segments, the states of three before them); 2 x 2048, 64 heads of 64: 130 and
+// 161; 8 prompts of 0 to 4095, 64 heads of 64: 264 and 324; 9000 + 100, 64 heads of 128:
+// 433 and 589.  What a batch pays that is not cut in the end: 4 x 4096: 293 and 291, 8 x
+// 1000, 32 heads: 97 and 94 (equal lengths that are given as such pay nothing).
 // Pieces of 2, 3 or 4 chunks at least: 768 tokens, 32 heads of 64: 56, 58, 65 us; 400
 // tokens, 16 heads: 51, 49, 49.
 Plan plan_for(const SsmArgs &a, int sms) {
@@ -995,19 +1080,18 @@ Plan plan_for(const SsmArgs &a, int sms) {
     p.blocks_per_group = (R * a.P + 127) / 128;
     p.blocks = a.G * p.blocks_per_group;
     p.slots = a.n_tok / stc::Q + a.n_seq;
-    const long long chains = (long long)p.blocks * a.n_seq;
-    const int longest = a.cu_seqlens ? a.n_tok : a.n_tok / a.n_seq;
-    p.n_seg = 1;
-    if (chains * 2 <= sms) {
-        const int most = (int)(sms / chains) + 1, pieces = (longest + stc::Q - 1) / stc::Q / stc::MIN_SEG;
-        p.n_seg = most < pieces ? most : pieces;
-        if (p.n_seg < 3) p.n_seg = 1;
-    }
+    p.even = (int)(((long long)p.slots * p.blocks + sms - 1) / sms);
+    p.cap = sms / p.blocks;
+    // no room, nothing long enough, or equal lengths whose part of the rows is too small
+    const int known = a.cu_seqlens ? 1 : a.n_seq;
+    if (p.cap / known < 2 || a.n_seq > stc::PREP_THREADS || a.n_tok / known < 3 * stc::MIN_SEG * stc::Q) p.cap = 0;
     p.tiles = round256((size_t)p.slots * a.G * (a.N / 64) * stc::KB);
     p.rec = round256((size_t)p.slots * a.H * stc::REC * 4);
-    p.seg_state = round256((size_t)chains * (p.n_seg - 1) * a.N * 128 * 4);
-    p.seg_decay = round256((size_t)chains * (p.n_seg - 1) * 2 * 4);
-    p.bytes = p.tiles + p.rec + p.seg_state + p.seg_decay;
+    p.seg_state = round256((size_t)p.cap * p.blocks * a.N * 128 * 4);
+    p.seg_decay = round256((size_t)p.cap * p.blocks * 2 * 4);
+    p.cuts = p.cap > 0 ? round256((size_t)a.n_seq * 8) : 0;
+    p.rows = round256((size_t)p.cap * 16);
+    p.bytes = p.tiles + p.rec + p.seg_state + p.seg_decay + p.cuts + p.rows;
     return p;
 }
 
@@ -1025,6 +1109,12 @@ cudaError_t launch_tc(const SsmArgs &a, char *ws, int sms) {
     pa.n_seq = a.n_seq; pa.n_tok = a.n_tok; pa.H = a.H; pa.G = a.G; pa.hp = a.H * a.P;
     pa.tiles = reinterpret_cast<uint8_t *>(ws);
     pa.rec = reinterpret_cast<float *>(ws + p.tiles);
+    char *w = ws + p.tiles + p.rec + p.seg_state + p.seg_decay;
+    pa.cuts = reinterpret_cast<int2 *>(w);
+    pa.rows = reinterpret_cast<int4 *>(w + p.cuts);
+    pa.slots = p.slots;
+    pa.cap = p.cap;
+    pa.even = p.even;
     ChainArgs ca = {};
     ca.x = static_cast<const bf16 *>(a.x);
     ca.z = static_cast<const bf16 *>(a.z);
@@ -1040,11 +1130,12 @@ cudaError_t launch_tc(const SsmArgs &a, char *ws, int sms) {
     ca.seg_decay = reinterpret_cast<float *>(ws + p.tiles + p.rec + p.seg_state);
     ca.n_seq = a.n_seq; ca.n_tok = a.n_tok; ca.H = a.H; ca.G = a.G; ca.P = a.P;
     ca.blocks_per_group = p.blocks_per_group;
-    ca.seg0 = p.n_seg > 1 ? 1 : 0;
-    ca.n_seg = p.n_seg;
+    ca.cuts = pa.cuts;
+    ca.rows = pa.rows;
+    ca.cap = p.cap;
     cudaError_t e;
     if (a.n_tok > 0) {
-        ssm_prep_kernel<N><<<dim3(p.slots, a.G), stc::PREP_THREADS, 0, a.stream>>>(pa);
+        ssm_prep_kernel<N><<<dim3(p.slots + (p.cap > 0), a.G), stc::PREP_THREADS, 0, a.stream>>>(pa);
         if ((e = launched()) != cudaSuccess) return e;
     }
     constexpr int SMEM = stc::Smem<N>::SIZE;
@@ -1060,14 +1151,14 @@ cudaError_t launch_tc(const SsmArgs &a, char *ws, int sms) {
     if ((e = cudaFuncSetAttribute(ssm_chain_kernel<N, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM)) !=
         cudaSuccess)
         return e;
-    if (p.n_seg > 1) {
+    if (p.cap > 0) {
         if ((e = cudaFuncSetAttribute(ssm_chain_kernel<N, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM)) !=
             cudaSuccess)
             return e;
-        ssm_chain_kernel<N, true><<<dim3(p.blocks, a.n_seq, p.n_seg - 1), stc::THREADS, SMEM, a.stream>>>(ca, maps);
+        ssm_chain_kernel<N, true><<<dim3(p.blocks, a.n_seq + p.cap), stc::THREADS, SMEM, a.stream>>>(ca, maps);
         if ((e = launched()) != cudaSuccess) return e;
     }
-    ssm_chain_kernel<N, false><<<dim3(p.blocks, a.n_seq, p.n_seg > 1 ? p.n_seg - 1 : 1), stc::THREADS, SMEM, a.stream>>>(ca, maps);
+    ssm_chain_kernel<N, false><<<dim3(p.blocks, p.cap > 0 ? p.cap : a.n_seq), stc::THREADS, SMEM, a.stream>>>(ca, maps);
     return launched();
 }
 

@@ -63,8 +63,9 @@ def test_not_finite_goes_where_the_formulas_take_it(cuda_device, dtype, place, v
         assert torch.isnan(out[HIT:, 0]).all() and torch.isnan(S[0, 0]).all()
 
 
-@pytest.mark.parametrize("lens,heads", [([2000], 4), ([700, 0, 1500, 64], 2), ([575, 576, 577, 129, 768], 6), ([127, 128, 3000], 40)],
-                         ids=["one", "ragged", "multiples", "many_heads"])
+@pytest.mark.parametrize("lens,heads", [([2000], 4), ([700, 0, 1500, 64], 2), ([575, 576, 577, 129, 768], 6), ([127, 128, 3000], 40),
+                                        ([1000, 70, 3000, 1, 500], 40), ([1500, 64, 1400, 5], 72)],
+                         ids=["one", "ragged", "multiples", "many_heads", "one_cut_of_five", "two_cut_of_four"])
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 def test_long_prompts_in_place(cuda_device, dtype, lens, heads):
     """Few heads, so that the sequence itself is split: state and history in place."""
