@@ -7,12 +7,12 @@
 // block of zeros gives zeros).  The maximum is taken over the bits of |x|, where a
 // NaN is larger than every number: a block with a NaN gets a NaN scale.
 //
-// Memory-bound: x read once, q written once.  Sixteen lanes hold the 128 columns of
-// one block row in 16-byte loads (8 elements a lane), so a row block needs four
-// shuffles; two row blocks per half warp are in flight at once.  The 128 x 128 block
-// stays in registers (64 values a thread) between its maximum and its conversion.
-// 16384 x 2048 bf16 by rows: 20.2 us in a graph (100.8 MB: 15.4 at the copy rate); 8513 x
-// 2064 fp32 by tiles: 14.8 us (88 MB: 13.4).
+// Memory-bound: x read once, q written once.  By rows, eight lanes hold a row block in
+// 16-element pieces, so its maximum needs three shuffles and its bytes leave 16 at a time;
+// two row blocks a lane are in flight at once.  The 128 x 128 block stays in registers (64
+// values a thread, 8 side by side) between its maximum and its conversion.
+// 16384 x 2048 bf16 by rows: 16.7 us in a graph (100.8 MB: 15.4 at the copy rate); 8513 x
+// 2064 fp32 by tiles: 15.7 us (88 MB: 13.4; with 16 values side by side 16.4).
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
@@ -73,15 +73,17 @@ template <> struct Raw8<float> {
     }
 };
 
-constexpr int QB = 2;   // row blocks per half warp (16384 x 2048 bf16: 20.2 us; 4: 20.8, 8: 22.5)
+// Eight lanes hold a row block, 16 elements each: two row blocks a lane 16.7 us (16384 x
+// 2048 bf16), one 18.4, four 17.0; sixteen lanes of 8 elements, two row blocks: 20.2.
+constexpr int QB = 2;
 
 template <typename T>
 __global__ void __launch_bounds__(256)
 quant_rows_kernel(const T *__restrict__ x, long long ld_x, uint32_t n_blocks, int cols, uint32_t cb,
                   uint8_t *__restrict__ q, long long ld_q, float *__restrict__ scale) {
-    const int sub = threadIdx.x & 15;
-    const uint32_t first = (blockIdx.x * 16 + (threadIdx.x >> 4)) * QB;
-    // row and column of this half warp's row blocks, which follow one another
+    const int sub = threadIdx.x & 7;
+    const uint32_t first = (blockIdx.x * 32 + (threadIdx.x >> 3)) * QB;
+    // row and column of these lanes' row blocks, which follow one another
     uint32_t r[QB], c[QB];
     r[0] = first / cb;
     c[0] = first - r[0] * cb;
@@ -91,25 +93,33 @@ quant_rows_kernel(const T *__restrict__ x, long long ld_x, uint32_t n_blocks, in
         r[i] = r[i - 1] + wrap;
         c[i] = wrap ? 0 : c[i - 1] + 1;
     }
-    Raw8<T> raw[QB];
+    Raw8<T> raw[QB][2];
 #pragma unroll
     for (int i = 0; i < QB; ++i) {
-        const int col = (int)c[i] * 128 + 8 * sub;
-        if (first + i < n_blocks && col < cols) raw[i].load(x + r[i] * ld_x + col);
-        else raw[i].zero();
+        const int col = (int)c[i] * 128 + 16 * sub;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (first + i < n_blocks && col < cols) raw[i][k].load(x + r[i] * ld_x + col + 8 * k);
+            else raw[i][k].zero();
+        }
     }
 #pragma unroll
     for (int i = 0; i < QB; ++i) {
-        float v[8];
-        raw[i].floats(v);
-        uint32_t m = amax8(v);
+        float v[2][8];
+        raw[i][0].floats(v[0]);
+        raw[i][1].floats(v[1]);
+        uint32_t m = max(amax8(v[0]), amax8(v[1]));
 #pragma unroll
-        for (int o = 1; o < 16; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
         const float amax = block_amax(m);
-        const int col = (int)c[i] * 128 + 8 * sub;
+        const int col = (int)c[i] * 128 + 16 * sub;
         if (first + i < n_blocks) {
             if (sub == 0) scale[first + i] = __fdiv_rn(amax, kFp8Max);
-            if (col < cols) *reinterpret_cast<uint2 *>(q + r[i] * ld_q + col) = to_e4m3x8(v, __fdiv_rn(kFp8Max, amax));
+            const float inv = __fdiv_rn(kFp8Max, amax);
+            if (col < cols) {
+                const uint2 a = to_e4m3x8(v[0], inv), b = to_e4m3x8(v[1], inv);
+                *reinterpret_cast<uint4 *>(q + r[i] * ld_q + col) = make_uint4(a.x, a.y, b.x, b.y);
+            }
         }
     }
 }
@@ -155,7 +165,7 @@ cudaError_t launch_quant(int rows, int cols, const void *x, long long ld_x, int 
                          float *scale, cudaStream_t stream) {
     const int cb = (cols + 127) / 128;
     if (block_rows == 1) {
-        const long long n = (long long)rows * cb, per_cta = 16 * QB;
+        const long long n = (long long)rows * cb, per_cta = 32 * QB;
         quant_rows_kernel<T><<<(unsigned)((n + per_cta - 1) / per_cta), 256, 0, stream>>>(
             static_cast<const T *>(x), ld_x, (uint32_t)n, cols, (uint32_t)cb, static_cast<uint8_t *>(q), ld_q, scale);
     } else {
