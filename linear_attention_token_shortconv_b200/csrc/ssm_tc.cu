@@ -490,7 +490,7 @@ __device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMap
 
     if (warp == MMA_WARP) umma::tmem_alloc(tslot, 512);
     if (tid == 0) {
-        for (int i = 0; i < 10; ++i) umma::mbar_init(full + i, i < 7 ? 1 : i < 9 ? CWARPS : CWARPS + 1);
+        for (int i = 0; i < 10; ++i) umma::mbar_init(full + i, i < 7 ? 1 : i < 9 || STATE_ONLY ? CWARPS : CWARPS + 1);
         *abort_flag = 0;
         umma::fence_mbar_init();
     }
@@ -560,20 +560,22 @@ __device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMap
             if (!STATE_ONLY && chunks > 0) scores(0);
             for (int c = 0; c < chunks; ++c) {
                 const uint32_t st = (uint32_t)((c & 1) * (Sm::TILE >> 4));
-                wait(bar_x, (uint32_t)c & 1u);
+                // the states' chunks alternate between two buffers
+                const int second = STATE_ONLY ? c & 1 : 0;
+                wait(second ? bar_w : bar_x, (uint32_t)(STATE_ONLY ? c >> 1 : c) & 1u);
                 __syncwarp();
                 umma::tc_fence_after();
                 if (elect_one()) {
                     constexpr uint32_t idu = umma::idesc_f16(128, 128, true, true);
                     const uint64_t da = d_tile_mn + st;
-                    const uint64_t dxh = d_x + ((Sm::OFF_XH - Sm::OFF_X) >> 4), dxl = d_x + ((Sm::OFF_XL - Sm::OFF_X) >> 4);
+                    const uint64_t dxh = d_x + (((second ? Sm::OFF_Z : Sm::OFF_XH) - Sm::OFF_X) >> 4), dxl = dxh + (16384 >> 4);
 #pragma unroll
                     for (int p = 0; p < 3; ++p)   // hi hi, hi lo, lo hi
 #pragma unroll
                         for (int k = 0; k < Q / 16; ++k)
-                            umma::mma_f16(T_U, da + (((p == 2 ? OFF_LO : 0) + k * 2048) >> 4),
+                            umma::mma_f16(second ? T_YW : T_U, da + (((p == 2 ? OFF_LO : 0) + k * 2048) >> 4),
                                           (p == 1 ? dxl : dxh) + ((k * 2048) >> 4), idu, p > 0 || k > 0);
-                    umma::mma_commit(bar_u);
+                    umma::mma_commit(second ? bar_y : bar_u);
                     if (!STATE_ONLY) {
                         constexpr uint32_t id = umma::idesc_f16(128, 64, false, true);
                         const uint64_t dt = d_tile + st;
@@ -648,14 +650,20 @@ __device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMap
                     if (!STATE_ONLY && a.z) issue_z(1);
                 }
             }
-            for (int c = 0; c < chunks; ++c) {
-                if (c >= 1) wait(STATE_ONLY ? bar_u : bar_y, (uint32_t)(c - 1) & 1u);   // the products have read the tiles
+            // chunk c's products, which follow its records' last reader, have read its tile
+            for (int c = 0; STATE_ONLY && c + 2 < chunks; ++c) {
+                wait(c & 1 ? bar_y : bar_u, (uint32_t)(c >> 1) & 1u);
+                if (one && *abort_flag == 0) issue(c + 2);
+                __syncwarp();
+            }
+            for (int c = 0; !STATE_ONLY && c < chunks; ++c) {
+                if (c >= 1) wait(bar_y, (uint32_t)(c - 1) & 1u);
                 arrive();
                 wait(bar_m, (uint32_t)c & 1u);
                 if (one) {
                     const bool go = *abort_flag == 0;
                     if (c >= 1 && c + 1 < chunks && go) issue(c + 1);
-                    if (!STATE_ONLY && c >= 2) {
+                    if (c >= 2) {
                         // out of chunk c - 2, gated before this meeting, leaves; its tile takes z of chunk c
                         store_out(c - 2);
                         umma::bulk_wait_read<0>();
@@ -843,11 +851,78 @@ __device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMap
                 o[1] = w[1];
             }
         };
+        // operands of the x in xh, weighted by their records' R_W, in shared memory; the plain
+        // one for y only
+        auto store_x = [&](const float *w, float xs, uint32_t to) {
+            const float4 wr4 = *reinterpret_cast<const float4 *>(w + R_W + 4 * warp);
+            const float wr[4] = {wr4.x, wr4.y, wr4.z, wr4.w};
+            const float2 xs2 = make_float2(xs, xs);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t p = (p_x ^ (16 * i)) + 128 * i;
+                uint32_t x2[2], hi2[2], lo2[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float2 u = fmul2(xh[i][e], xs2), v = fmul2(u, make_float2(wr[i], wr[i]));
+                    x2[e] = pack(u);
+                    hi2[e] = pack(v);
+                    const float2 h = half2_float2(hi2[e]);
+                    lo2[e] = umma::pack_half2(v.x - h.x, v.y - h.y);
+                }
+                if (!STATE_ONLY) sts64(p, x2[0], x2[1]);
+                sts64(p + to, hi2[0], hi2[1]);
+                sts64(p + to + 16384, lo2[0], lo2[1]);
+            }
+        };
+        if constexpr (STATE_ONLY) {
+            // A chunk's products run under the next one's convolution and stores: the
+            // operands (in z's place) and the sums (in y's) alternate between two buffers.
+            float dec = 0.f, add = 0.f;   // of this thread's half, of the last chunk stored
+            auto store = [&](int c) {
+                const float *r = reinterpret_cast<const float *>(sm + Sm::OFF_REC) + (c & 1) * 2 * REC;
+                wait(bar_m, (uint32_t)c & 1u);
+                const uint2 m = *reinterpret_cast<const uint2 *>(mx + 4 * (c % 3));
+                if (tid < 2) mx[4 * ((c + 2) % 3) + tid] = 0;   // chunk c - 1's, which all have read
+                float xs0, xs1, i0, i1;
+                scale_pow2(m.x, 13, xs0, i0);
+                scale_pow2(m.y, 13, xs1, i1);
+                wait(full + (c & 1), (uint32_t)(c >> 1) & 1u);
+                store_x(half ? r + REC : r, half ? xs1 : xs0, (c & 1 ? Sm::OFF_Z : Sm::OFF_XH) - Sm::OFF_X);
+                dec = (cg < 2 ? r : r + REC)[R_DEC];
+                add = (cg < 2 ? r : r + REC)[R_UMAX] * (cg < 2 ? i0 : i1);
+                decay0 *= r[R_DEC];
+                decay1 *= r[REC + R_DEC];
+                umma::fence_proxy_async_smem();
+                umma::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(c & 1 ? bar_w : bar_x);
+                if (c + 1 < chunks) fetch(c + 1);
+            };
+            if (chunks > 0) {
+                arrive();
+                store(0);
+            }
+            for (int c = 0; c < chunks; ++c) {
+                const float2 dec2 = make_float2(dec, dec), add2 = make_float2(add, add);
+                if (c + 1 < chunks) {
+                    convolve(c + 1, mx + 4 * ((c + 1) % 3));
+                    arrive();
+                    store(c + 1);
+                }
+                wait(c & 1 ? bar_y : bar_u, (uint32_t)(c >> 1) & 1u);
+                umma::tc_fence_after();
+                uint32_t v[32];
+                umma::tmem_ld32_nowait((c & 1 ? T_YW : T_U) + lane_off + sc0, v);
+                umma::tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) S[j] = ffma2(dec2, S[j], fmul2(add2, as_float2(v[2 * j], v[2 * j + 1])));
+            }
+        }
         // maxima of this chunk, of the next (written from its convolution on) and of the one
         // after (cleared now; its last readers, of the previous chunk, have met since)
         uint32_t *m_now = mx, *m_next = mx + 4, *m_after = mx + 8;
-        arrive();
-        for (int c = 0; c < chunks; ++c) {
+        if (!STATE_ONLY) arrive();
+        for (int c = 0; !STATE_ONLY && c < chunks; ++c) {
             const int b = c & 1;
             const uint32_t ph = (uint32_t)c & 1u, ph_full = (uint32_t)(c >> 1) & 1u;
             const float *rec0 = reinterpret_cast<const float *>(sm + Sm::OFF_REC) + b * 2 * REC, *rec1 = rec0 + REC;
@@ -862,28 +937,7 @@ __device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMap
             scale_pow2(mxv.y, 13, xs1, xinv1);
             float sinv = 0.f;                    // of the rows of y of this thread
             wait(full + b, ph_full);
-            {
-                const float4 wr4 = *reinterpret_cast<const float4 *>((half ? rec1 : rec0) + R_W + 4 * warp);
-                const float wr[4] = {wr4.x, wr4.y, wr4.z, wr4.w};
-                const float xs = half ? xs1 : xs0;
-                const float2 xs2 = make_float2(xs, xs);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t p = (p_x ^ (16 * i)) + 128 * i;
-                    uint32_t x2[2], hi2[2], lo2[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float2 u = fmul2(xh[i][e], xs2), v = fmul2(u, make_float2(wr[i], wr[i]));
-                        x2[e] = pack(u);
-                        hi2[e] = pack(v);
-                        const float2 h = half2_float2(hi2[e]);
-                        lo2[e] = umma::pack_half2(v.x - h.x, v.y - h.y);
-                    }
-                    if (!STATE_ONLY) sts64(p, x2[0], x2[1]);
-                    sts64(p + (Sm::OFF_XH - Sm::OFF_X), hi2[0], hi2[1]);
-                    sts64(p + (Sm::OFF_XL - Sm::OFF_X), lo2[0], lo2[1]);
-                }
-            }
+            store_x(half ? rec1 : rec0, half ? xs1 : xs0, Sm::OFF_XH - Sm::OFF_X);
             if (!STATE_ONLY) {
                 float s0, s1, i0, i1;
                 scale_pow2(mxv.z, 13, s0, i0);
@@ -966,9 +1020,7 @@ __device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMap
                 umma::tmem_ld_wait();
 #pragma unroll
                 for (int j = 0; j < 16; ++j) S[j] = ffma2(dec2, S[j], fmul2(add2, as_float2(v[2 * j], v[2 * j + 1])));
-                if (STATE_ONLY) { decay0 *= rec0[R_DEC]; decay1 *= rec1[R_DEC]; }
             }
-            if (STATE_ONLY && c + 1 < chunks) arrive();
             if (!STATE_ONLY) {
                 state_max(m_next);
                 // ---- y before its gate
