@@ -896,9 +896,9 @@ __device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMap
                 umma::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(c & 1 ? bar_w : bar_x);
-                if (c + 1 < chunks) fetch(c + 1);
             };
             if (chunks > 0) {
+                if (chunks > 1) fetch(1);
                 arrive();
                 store(0);
             }
@@ -906,6 +906,7 @@ __device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMap
                 const float2 dec2 = make_float2(dec, dec), add2 = make_float2(add, add);
                 if (c + 1 < chunks) {
                     convolve(c + 1, mx + 4 * ((c + 1) % 3));
+                    if (c + 2 < chunks) fetch(c + 2);
                     arrive();
                     store(c + 1);
                 }
