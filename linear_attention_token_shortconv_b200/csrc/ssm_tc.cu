@@ -1118,12 +1118,12 @@ struct Plan {
 // Segments: a chain (128 columns of a sequence) is sequential over its chunks, 4.6 us each
 // however many chains there are, so long sequences are cut while SMs would be idle.  A
 // first launch runs segment 0, half as long, of every sequence and beside it the states of
-// the others, which take 2.4 us a chunk; a second one the others, as many as there are SMs
+// the others, which take about 2 us a chunk; a second one the others, as many as there are SMs
 // (cap rows of blocks).  The lengths are on the device, so ssm_prep shares the rows out.
-// Cut and whole, us: one prompt of 32768 tokens, 32 heads of 128, N = 128: 801 (885 with
-// four equal segments, the states of three before them); 2 x 2048, 64 heads of 64: 130 and
+// Cut and whole, us: one prompt of 32768 tokens, 32 heads of 128, N = 128: 757 (first
+// segment 0.4 of the others: 773, 0.55: 767; uncut about 2360); 2 x 2048, 64 heads of 64: 130 and
 // 161; 8 prompts of 0 to 4095, 64 heads of 64: 264 and 324; 9000 + 100, 64 heads of 128:
-// 433 and 589.  What a batch pays that is not cut in the end: 4 x 4096: 293 and 291, 8 x
+// 409 and 589.  What a batch pays that is not cut in the end: 4 x 4096: 293 and 291, 8 x
 // 1000, 32 heads: 97 and 94 (equal lengths that are given as such pay nothing).
 // Pieces of 2, 3 or 4 chunks at least: 768 tokens, 32 heads of 64: 56, 58, 65 us; 400
 // tokens, 16 heads: 51, 49, 49.
