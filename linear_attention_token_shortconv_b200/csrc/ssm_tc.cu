@@ -1120,11 +1120,12 @@ struct Plan {
 // first launch runs segment 0, half as long, of every sequence and beside it the states of
 // the others, which take about 2 us a chunk; a second one the others, as many as there are SMs
 // (cap rows of blocks).  The lengths are on the device, so ssm_prep shares the rows out.
-// Cut and whole, us: one prompt of 32768 tokens, 32 heads of 128, N = 128: 757 (first
-// segment 0.4 of the others: 773, 0.55: 767; uncut about 2360); 2 x 2048, 64 heads of 64: 130 and
-// 161; 8 prompts of 0 to 4095, 64 heads of 64: 264 and 324; 9000 + 100, 64 heads of 128:
-// 409 and 589.  What a batch pays that is not cut in the end: 4 x 4096: 293 and 291, 8 x
-// 1000, 32 heads: 97 and 94 (equal lengths that are given as such pay nothing).
+// Cut and whole, us: one prompt of 32768 tokens, 32 heads of 128, N = 128: 757 and 2078
+// (with segment 0 0.4 or 0.55 of the others: 773, 767); 4000 tokens, 16 heads of 64: 87 and
+// 270; 2 x 2048, 64 heads of 64: 128 and 158; 8 prompts of 0 to 4095, 64 heads of 64: 262
+// and 325; 9000 + 100, 64 heads of 128: 407 and 591.  What a batch pays that is not cut in
+// the end: 4 x 4096: 293 and 291, 8 x 1000, 32 heads: 97 and 94 (equal lengths that are
+// given as such pay nothing).
 // Pieces of 2, 3 or 4 chunks at least: 768 tokens, 32 heads of 64: 56, 58, 65 us; 400
 // tokens, 16 heads: 51, 49, 49.
 Plan plan_for(const SsmArgs &a, int sms) {
