@@ -63,6 +63,29 @@ def test_not_finite_goes_where_the_formulas_take_it(cuda_device, dtype, place, v
         assert torch.isnan(out[HIT:, 0]).all() and torch.isnan(S[0, 0]).all()
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("hit", [5, 700, 1990])
+def test_not_finite_in_a_long_prompt(cuda_device, dtype, hit):
+    """The same where the sequence is cut: NaN in one column of x goes through the segments."""
+    T = 2000
+    inp = so.make_inputs([T], H, G, P, N, dtype, cuda_device, seed=12)
+    clean, Sc, _ = prefill(inp, [T])
+    inp["proj"][hit, HP + 5] = float("nan")
+    out, S, _ = prefill(inp, [T])
+    reach = torch.zeros(T, H, P, dtype=torch.bool, device=cuda_device)
+    reach[hit:, 0, 5] = True
+    assert torch.isnan(out[reach]).all() and torch.isnan(S[0, 0, :, 5]).all()
+    near = reach.clone()
+    near[:, 0] = True                       # one power of two scales a head's values in a chunk
+    assert torch.equal(out[~near], clean[~near])
+    # two results of one value: twice its rounding (2^-8), or twice 2^-18 and some
+    rel = 2.0 ** -7 if dtype == BF16 else 2.0 ** -16
+    size = clean[~reach].float().abs().max()
+    assert (out[~reach].float() - clean[~reach].float()).abs().max() <= rel * size
+    keep = [c for c in range(P) if c != 5]
+    assert torch.equal(S[0, 1:], Sc[0, 1:]) and torch.isfinite(S[0, 0, :, keep]).all()
+
+
 @pytest.mark.parametrize("lens,heads", [([2000], 4), ([700, 0, 1500, 64], 2), ([575, 576, 577, 129, 768], 6), ([127, 128, 3000], 40),
                                         ([1000, 70, 3000, 1, 500], 40), ([1500, 64, 1400, 5], 72)],
                          ids=["one", "ragged", "multiples", "many_heads", "one_cut_of_five", "two_cut_of_four"])
