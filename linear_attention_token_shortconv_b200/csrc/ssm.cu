@@ -35,7 +35,19 @@ template <typename T> Raw<T> raw_of(const SsmArgs &a) {
 
 constexpr int ACT_TOK = 16;   // consecutive tokens per thread of ssm_act
 
-// act [N_tok, channels] = SiLU(conv + bias); step [N_tok, H] = (D_t, a_t).
+// e^{-t} as hi + lo.  Near 1, where a state remembers thousands of tokens, the rounding of
+// one fp32 decay is the same at every like step and adds up (738 tokens: 6.6e-6 of the
+// state), so its remainder, from e^{-t} - 1, is not dropped.  Below 1/2 the memory is short.
+__device__ __forceinline__ float2 decay_pair(float t) {
+    if (t < 0.69f) {
+        const float e = expm1f(-t), hi = 1.f + e;
+        return make_float2(hi, e - (hi - 1.f));
+    }
+    return make_float2(expf(-t), 0.f);
+}
+
+// act [N_tok, channels] = SiLU(conv + bias); step [N_tok, H] = (D_t, a_t, a_t's remainder
+// relative to it).
 // blockIdx.x: run of ACT_TOK packed tokens, blockIdx.y * 256 + threadIdx.x: four
 // channels, then (past the channels) one head.
 template <typename T>
@@ -43,7 +55,7 @@ __global__ void __launch_bounds__(256)
 ssm_act_kernel(const Raw<T> raw, const T *__restrict__ hist, const float *__restrict__ conv_w,
                const float *__restrict__ conv_b, const T *__restrict__ dt, long long ld_dt,
                const float *__restrict__ A, const float *__restrict__ b_dt, const int32_t *__restrict__ cu, int n_seq,
-               int n_tok, int H, float *__restrict__ act, float2 *__restrict__ step) {
+               int n_tok, int H, float *__restrict__ act, float4 *__restrict__ step) {
     const int chans = raw.hp + 2 * raw.gn;
     const int v = blockIdx.y * blockDim.x + threadIdx.x;
     const int t0 = blockIdx.x * ACT_TOK, t1 = min(t0 + ACT_TOK, n_tok);
@@ -53,7 +65,8 @@ ssm_act_kernel(const Raw<T> raw, const T *__restrict__ hist, const float *__rest
         const float rate = expf(__ldg(A + h)), bias = __ldg(b_dt + h);
         for (int t = t0; t < t1; ++t) {
             const float d = softplus_acc(to_f32(dt[t * ld_dt + h]) + bias);
-            step[(size_t)t * H + h] = make_float2(d, expf(-rate * d));
+            const float2 a = decay_pair(rate * d);
+            step[(size_t)t * H + h] = make_float4(d, a.x, a.y == 0.f ? 0.f : a.y / a.x, 0.f);
         }
         return;
     }
@@ -121,13 +134,13 @@ struct Segments {
 
 template <int N, typename T, typename Tout, bool STATE_ONLY>
 __global__ void __launch_bounds__(SCAN_THREADS)
-ssm_scan_kernel(const float *__restrict__ act, const float2 *__restrict__ step, const float *__restrict__ Dw,
+ssm_scan_kernel(const float *__restrict__ act, const float4 *__restrict__ step, const float *__restrict__ Dw,
                 const T *__restrict__ z, long long ld_z, const float *S0, const int32_t *__restrict__ cu, int n_seq,
                 int n_tok, int H, int G, int P, const Segments seg, Tout *__restrict__ out, float *S_final) {
     constexpr int R = N / 8;             // state rows of a thread
     struct Stage {
         float b[SCAN_TOK][N], c[SCAN_TOK][N], x[SCAN_TOK][SCAN_COLS];
-        float2 d[SCAN_TOK];
+        float4 d[SCAN_TOK];
     };
     __shared__ __align__(16) Stage stages[2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -164,7 +177,7 @@ ssm_scan_kernel(const float *__restrict__ act, const float2 *__restrict__ step, 
             const int r = i / (SCAN_COLS / 4), q = i % (SCAN_COLS / 4);
             copy_async<16>(&st.x[r][4 * q], rows + (r < len ? (size_t)r * chans : 0) + h * P + p0 + 4 * q, r < len);
         }
-        if (tid < SCAN_TOK) copy_async<8>(&st.d[tid], step + (size_t)(t0 + (tid < len ? tid : 0)) * H + h, tid < len);
+        if (tid < SCAN_TOK) copy_async<16>(&st.d[tid], step + (size_t)(t0 + (tid < len ? tid : 0)) * H + h, tid < len);
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     if (begin < end) load(begin, stages[0]);
@@ -204,12 +217,14 @@ ssm_scan_kernel(const float *__restrict__ act, const float2 *__restrict__ step, 
         __syncthreads();
         // four tokens at a time: their recurrences follow one another, but their parts of y
         // (8 values) are added over the eight slices together, one value staying in each lane
+        float rest = 0.f;   // of these tokens' decays
         for (int r = 0; r < len; r += 4) {
             float v[8];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const float2 da = st.d[r + u];
+                const float4 da = st.d[r + u];
                 const float a = r + u < len ? da.y : 1.f;
+                rest += da.z;
                 const float2 x = *reinterpret_cast<const float2 *>(&st.x[r + u][lcol]);
                 const float2 dx = make_float2(da.x * x.x, da.x * x.y), aa = make_float2(a, a);
                 if (STATE_ONLY) decay *= a;
@@ -249,6 +264,10 @@ ssm_scan_kernel(const float *__restrict__ act, const float2 *__restrict__ step, 
                 }
             }
         }
+        // the decays' remainders, once a stage: 3 % of the time; at every token 14
+#pragma unroll
+        for (int i = 0; i < R; ++i) S[i] = ffma2(make_float2(rest, rest), S[i], S[i]);
+        if (STATE_ONLY) decay = fmaf(rest, decay, decay);
         __syncthreads();   // before the stage is loaded again
     }
     float *const to = STATE_ONLY ? seg.state + slot * one : k == last && S_final ? S_final + n * one : nullptr;
@@ -310,7 +329,7 @@ ScanPlan scan_plan(const SsmArgs &a, int sms) {
     ScanPlan p = {};
     const size_t chans = (size_t)a.H * a.P + 2 * (size_t)a.G * a.N, one = (size_t)a.H * a.N * a.P * 4;
     p.act = round256((size_t)a.n_tok * chans * 4);
-    p.step = round256((size_t)a.n_tok * a.H * 8);
+    p.step = round256((size_t)a.n_tok * a.H * 16);
     p.slots = a.n_seq;
     p.from = INT_MAX;
     p.len = 1;
@@ -330,7 +349,7 @@ ScanPlan scan_plan(const SsmArgs &a, int sms) {
 }
 
 template <int N, typename T, typename Tout>
-cudaError_t launch_scan(const SsmArgs &a, const float *act, const float2 *step, const ScanPlan &p, const Segments &seg) {
+cudaError_t launch_scan(const SsmArgs &a, const float *act, const float4 *step, const ScanPlan &p, const Segments &seg) {
     const dim3 grid(a.H * (a.P / SCAN_COLS), p.slots);
     if (p.from < INT_MAX) {
         ssm_scan_kernel<N, T, Tout, true><<<grid, SCAN_THREADS, 0, a.stream>>>(
@@ -350,7 +369,7 @@ cudaError_t launch_fp32(const SsmArgs &a, char *ws, int sms) {
     const ScanPlan p = scan_plan(a, sms);
     const int chans = a.H * a.P + 2 * a.G * a.N;
     float *act = reinterpret_cast<float *>(ws);
-    float2 *step = reinterpret_cast<float2 *>(ws + p.act);
+    float4 *step = reinterpret_cast<float4 *>(ws + p.act);
     if (a.n_tok > 0) {
         const dim3 grid((a.n_tok + ACT_TOK - 1) / ACT_TOK, (chans / 4 + a.H + 255) / 256);
         ssm_act_kernel<T><<<grid, 256, 0, a.stream>>>(raw_of<T>(a), static_cast<const T *>(a.hist), a.conv_w, a.conv_b,
@@ -414,7 +433,7 @@ ssm_decode_kernel(const Raw<T> raw, const T *__restrict__ dt, long long ld_dt, c
 #pragma unroll
     for (int i = 0; i < NV; ++i) s[i] = __ldcs(reinterpret_cast<const float4 *>(Sh + (size_t)i * ROWS * P));
     const float d = softplus_acc(to_f32(dt[b * ld_dt + h]) + __ldg(b_dt + h));
-    const float a = expf(-expf(__ldg(A + h)) * d);
+    const float2 a = decay_pair(expf(__ldg(A + h)) * d);
     for (int i = tid; i < COLS + 2 * N; i += THREADS) {
         const int c = i < COLS       ? col0 + i
                       : i < COLS + N ? raw.hp + g * N + (i - COLS)
@@ -438,10 +457,10 @@ ssm_decode_kernel(const Raw<T> raw, const T *__restrict__ dt, long long ld_dt, c
     for (int i = 0; i < NV; ++i) {
         const int row = row0 + i * ROWS;
         const float bb = bs[row], cc = cs[row];
-        s[i].x = fmaf(a, s[i].x, bb * x.x); y.x = fmaf(cc, s[i].x, y.x);
-        s[i].y = fmaf(a, s[i].y, bb * x.y); y.y = fmaf(cc, s[i].y, y.y);
-        s[i].z = fmaf(a, s[i].z, bb * x.z); y.z = fmaf(cc, s[i].z, y.z);
-        s[i].w = fmaf(a, s[i].w, bb * x.w); y.w = fmaf(cc, s[i].w, y.w);
+        s[i].x = fmaf(a.x, s[i].x, fmaf(a.y, s[i].x, bb * x.x)); y.x = fmaf(cc, s[i].x, y.x);
+        s[i].y = fmaf(a.x, s[i].y, fmaf(a.y, s[i].y, bb * x.y)); y.y = fmaf(cc, s[i].y, y.y);
+        s[i].z = fmaf(a.x, s[i].z, fmaf(a.y, s[i].z, bb * x.z)); y.z = fmaf(cc, s[i].z, y.z);
+        s[i].w = fmaf(a.x, s[i].w, fmaf(a.y, s[i].w, bb * x.w)); y.w = fmaf(cc, s[i].w, y.w);
         __stcs(reinterpret_cast<float4 *>(Sh + (size_t)i * ROWS * P), s[i]);
     }
     *reinterpret_cast<float4 *>(&part[row0][4 * q]) = y;

@@ -101,6 +101,17 @@ def test_long_prompts_in_place(cuda_device, dtype, lens, heads):
     assert torch.equal(again, out) and torch.equal(S_in, S) and torch.equal(tail_in, tail)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_long_memory(cuda_device, dtype):
+    """Decays within 1e-3 of 1 and the same at every token: rounded to fp32 each would be
+    off by up to 2^-25 in the same direction, 5000 of them by 1e-4 of the state."""
+    lens = [5000]
+    inp = so.make_inputs(lens, H, G, P, N, dtype, cuda_device, seed=13)
+    inp["proj"][:, 2 * HP + 2 * GN:] = 0.0
+    inp["A"] = torch.tensor([-3.0, -4.3, -5.1, -6.7], device=cuda_device)
+    agree(inp, lens)
+
+
 def test_two_streams_at_once(cuda_device):
     """Calls on two streams do not share their scratch memory."""
     cases = [([900, 300], 4, 21), ([500, 1, 64], 8, 22)]
