@@ -84,14 +84,16 @@ __device__ __forceinline__ float rcp(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-// x / (1 + e^-x) of a pair with one reciprocal, 1 / a = b / (a b): the special-function
-// unit (16 results a clock) is what the chain has least of.  The exponent is kept below
-// 60 so that the product is finite; there x 2^-60 stands for x e^x.
+// x E / (1 + E), E = e^x, of a pair with one reciprocal, 1 / a = b / (a b): the special-
+// function unit (16 results a clock) is what the chain has least of.  E is kept below 2^60
+// so that the product is finite, which changes nothing: there E / (1 + E) rounds to 1.  Far
+// below zero E goes to 0, and x E with it (-inf: NaN, as in the formula).
 __device__ __forceinline__ float2 silu2(float2 x) {
-    const float2 e = fmul2(x, make_float2(-stc::kLog2e, -stc::kLog2e));
-    const float2 d = fadd2(make_float2(ex2(fminf(e.x, 60.f)), ex2(fminf(e.y, 60.f))), make_float2(1.f, 1.f));
+    const float2 l = fmul2(x, make_float2(stc::kLog2e, stc::kLog2e));
+    const float2 e = make_float2(ex2(fminf(l.x, 60.f)), ex2(fminf(l.y, 60.f)));
+    const float2 d = fadd2(e, make_float2(1.f, 1.f));
     const float r = rcp(d.x * d.y);
-    return fmul2(fmul2(x, make_float2(r, r)), make_float2(d.y, d.x));
+    return fmul2(x, fmul2(e, fmul2(make_float2(r, r), make_float2(d.y, d.x))));
 }
 
 __device__ __forceinline__ float2 half2_float2(uint32_t h) {
