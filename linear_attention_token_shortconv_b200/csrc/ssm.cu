@@ -14,16 +14,20 @@
 // warp sharing the columns and adding their parts of y by shuffles, four tokens
 // together.  What bounds it is the chain of tokens, at one or two warps a scheduler; few
 // and long sequences are cut into segments, whose states a first pass finds.
-// 1000 + 999 tokens, 16 heads of 64, N = 64: 74 us, of it 13 for ssm_act (111 uncut).
+// 1000 + 999 tokens, 16 heads of 64, N = 64: 76 us, of it 13 for ssm_act (111 uncut).
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <climits>
 
 #include "ssm.cuh"
 
 namespace gdn {
 using ssm::Raw;
+using ssm::decay_pair;
 using ssm::load4;
+using ssm::next_decay;
+using ssm::relative_rest;
 using ssm::seq_range;
 
 namespace {
@@ -35,19 +39,8 @@ template <typename T> Raw<T> raw_of(const SsmArgs &a) {
 
 constexpr int ACT_TOK = 16;   // consecutive tokens per thread of ssm_act
 
-// e^{-t} as hi + lo.  Near 1, where a state remembers thousands of tokens, the rounding of
-// one fp32 decay is the same at every like step and adds up (738 tokens: 6.6e-6 of the
-// state), so its remainder, from e^{-t} - 1, is not dropped.  Below 1/2 the memory is short.
-__device__ __forceinline__ float2 decay_pair(float t) {
-    if (t < 0.69f) {
-        const float e = expm1f(-t), hi = 1.f + e;
-        return make_float2(hi, e - (hi - 1.f));
-    }
-    return make_float2(expf(-t), 0.f);
-}
-
 // act [N_tok, channels] = SiLU(conv + bias); step [N_tok, H] = (D_t, a_t, a_t's remainder
-// relative to it).
+// relative to it, -log a_t).
 // blockIdx.x: run of ACT_TOK packed tokens, blockIdx.y * 256 + threadIdx.x: four
 // channels, then (past the channels) one head.
 template <typename T>
@@ -66,7 +59,8 @@ ssm_act_kernel(const Raw<T> raw, const T *__restrict__ hist, const float *__rest
         for (int t = t0; t < t1; ++t) {
             const float d = softplus_acc(to_f32(dt[t * ld_dt + h]) + bias);
             const float2 a = decay_pair(rate * d);
-            step[(size_t)t * H + h] = make_float4(d, a.x, a.y == 0.f ? 0.f : a.y / a.x, 0.f);
+            // the log is bounded so that sums of it stay finite; e^-10000 is 0
+            step[(size_t)t * H + h] = make_float4(d, a.x, relative_rest(a), fminf(rate * d, 1e4f));
         }
         return;
     }
@@ -120,7 +114,7 @@ template <int B> __device__ __forceinline__ void copy_async(void *dst, const voi
 
 // Sequences of at least `from` tokens in segments of `len` (a multiple of SCAN_TOK).
 // STATE_ONLY runs every segment but a sequence's last from zero, segment 0 from S0, and
-// leaves the state and the product of its decays; the main pass starts each segment from
+// leaves the state and the sum of its log-decays; the main pass starts each segment from
 // those before it, joined.
 struct Segments {
     int from, len;           // from = INT_MAX: no sequence
@@ -128,7 +122,7 @@ struct Segments {
     // the blocks that all sequences have start first, and spread over the SMs
     int slots;
     float *state;            // [slot][H][N][P]
-    float *decay;            // [slot][H]
+    float *decay;            // [slot][H]: -log
     float *s0_copy;          // S0 where the final state replaces it, else NULL
 };
 
@@ -185,6 +179,7 @@ ssm_scan_kernel(const float *__restrict__ act, const float4 *__restrict__ step, 
     auto at = [&](int i) { return ((size_t)h * N + 32 * (i / 4) + 4 * slice + (i & 3)) * P + p0 + lcol; };
     const size_t one = (size_t)H * N * P;
     float2 S[R];
+    float carry = 0.f;   // relative remainder of the decays that S has not been given yet
 #pragma unroll
     for (int i = 0; i < R; ++i) S[i] = make_float2(0.f, 0.f);
     if (STATE_ONLY || k == 0) {
@@ -197,14 +192,19 @@ ssm_scan_kernel(const float *__restrict__ act, const float4 *__restrict__ step, 
     } else {
         for (int i0 = 0; i0 < k; ++i0) {   // S <- decay S + state
             const size_t j = i0 == 0 ? n : later + i0;
-            const float d = i0 > 0 ? seg.decay[j * H + h] : 0.f;
+            float d = 0.f;
+            if (i0 > 0) {
+                const float2 a = decay_pair(seg.decay[j * H + h]);
+                carry += relative_rest(a);
+                d = next_decay(a.x, carry);
+            }
 #pragma unroll
             for (int i = 0; i < R; ++i)
                 S[i] = ffma2(make_float2(d, d), S[i], *reinterpret_cast<const float2 *>(seg.state + j * one + at(i)));
         }
     }
     const float dw = Dw ? __ldg(Dw + h) : 0.f;
-    float decay = 1.f;
+    float log_hi = 0.f, log_lo = 0.f;   // sum of the segment's log-decays
     for (int t0 = begin, b = 0; t0 < end; t0 += SCAN_TOK, b ^= 1) {
         const int len = min(SCAN_TOK, end - t0);
         const Stage &st = stages[b];
@@ -217,17 +217,19 @@ ssm_scan_kernel(const float *__restrict__ act, const float4 *__restrict__ step, 
         __syncthreads();
         // four tokens at a time: their recurrences follow one another, but their parts of y
         // (8 values) are added over the eight slices together, one value staying in each lane
-        float rest = 0.f;   // of these tokens' decays
+        // takes what the stage before left: once a stage 3 % of the time, at every token 14
+        const float first = next_decay(st.d[0].y, carry);
+        float logs = 0.f;
         for (int r = 0; r < len; r += 4) {
             float v[8];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const float4 da = st.d[r + u];
-                const float a = r + u < len ? da.y : 1.f;
-                rest += da.z;
+                const float a = r + u >= len ? 1.f : u == 0 && r == 0 ? first : da.y;
+                carry += da.z;
                 const float2 x = *reinterpret_cast<const float2 *>(&st.x[r + u][lcol]);
                 const float2 dx = make_float2(da.x * x.x, da.x * x.y), aa = make_float2(a, a);
-                if (STATE_ONLY) decay *= a;
+                if (STATE_ONLY) logs += da.w;
                 float2 y = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int i4 = 0; i4 < R / 4; ++i4) {
@@ -264,18 +266,26 @@ ssm_scan_kernel(const float *__restrict__ act, const float4 *__restrict__ step, 
                 }
             }
         }
-        // the decays' remainders, once a stage: 3 % of the time; at every token 14
-#pragma unroll
-        for (int i = 0; i < R; ++i) S[i] = ffma2(make_float2(rest, rest), S[i], S[i]);
-        if (STATE_ONLY) decay = fmaf(rest, decay, decay);
+        if (STATE_ONLY) {
+            // two sums, since equal addends are rounded alike
+            const float sum = log_hi + logs;
+            log_lo += logs - (sum - log_hi);
+            log_hi = sum;
+        }
         __syncthreads();   // before the stage is loaded again
+    }
+    // what is left of the remainders, but not to an infinity
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        S[i].x = fmaf(carry, fminf(fmaxf(S[i].x, -FLT_MAX), FLT_MAX), S[i].x);
+        S[i].y = fmaf(carry, fminf(fmaxf(S[i].y, -FLT_MAX), FLT_MAX), S[i].y);
     }
     float *const to = STATE_ONLY ? seg.state + slot * one : k == last && S_final ? S_final + n * one : nullptr;
     if (to) {
 #pragma unroll
         for (int i = 0; i < R; ++i) *reinterpret_cast<float2 *>(to + at(i)) = S[i];
     }
-    if (STATE_ONLY && p0 == 0 && tid == 0) seg.decay[(size_t)slot * H + h] = decay;
+    if (STATE_ONLY && p0 == 0 && tid == 0) seg.decay[(size_t)slot * H + h] = log_hi + log_lo;
 }
 
 // tail [n, j] = the raw channels of token end - 3 + j of sequence n, or the row of

@@ -33,6 +33,29 @@ __device__ __forceinline__ float4 load4(const bf16 *p) {
 // and is held to fp32 accuracy.  x = -inf gives 0 * inf = NaN as in the formula.
 __device__ __forceinline__ float silu(float x) { return x / (1.0f + expf(-x)); }
 
+// e^{-t} as hi + lo.  Near 1, where a state remembers thousands of tokens, the rounding of
+// one fp32 decay is the same at every like step and adds up (738 tokens: 6.6e-6 of the
+// state), so its remainder, from e^{-t} - 1, is not dropped.  Below 1/2 the memory is short.
+__device__ __forceinline__ float2 decay_pair(float t) {
+    if (t < 0.69f) {
+        const float e = expm1f(-t), hi = 1.f + e;
+        return make_float2(hi, e - (hi - 1.f));
+    }
+    return make_float2(expf(-t), 0.f);
+}
+__device__ __forceinline__ float relative_rest(float2 a) { return a.y == 0.f ? 0.f : a.y / a.x; }
+
+// a (1 + carry) as one fp32 factor; carry becomes what that rounding leaves, for the next
+// factor.  So a product of decays stays within one rounding of the true one however long it
+// is.  A remainder added to the state instead, S + rest S, is rounded in its turn, and where
+// rest S is a few units of S the same way thousands of times (1e-4 of a state after 32768
+// tokens); it would also make NaN of an infinite state.
+__device__ __forceinline__ float next_decay(float a, float &carry) {
+    const float d = fmaf(carry, a, a);
+    carry = a > 0.5f ? carry - __fdividef(d - a, a) : 0.f;
+    return d;
+}
+
 // The mixer's channels [x (H P) | B (G N) | C (G N)] and their three raw sources.
 template <typename T> struct Raw {
     const T *x, *B, *C;
