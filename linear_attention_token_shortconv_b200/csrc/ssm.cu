@@ -37,6 +37,10 @@ template <typename T> Raw<T> raw_of(const SsmArgs &a) {
                   a.ld_x, a.ld_B, a.ld_C, a.H * a.P, a.G * a.N};
 }
 
+// What a decay's remainder is applied to: an infinity times it would be NaN, or the other
+// infinity.
+__device__ __forceinline__ float finite(float s) { return fminf(fmaxf(s, -FLT_MAX), FLT_MAX); }
+
 constexpr int ACT_TOK = 16;   // consecutive tokens per thread of ssm_act
 
 // act [N_tok, channels] = SiLU(conv + bias); step [N_tok, H] = (D_t, a_t, a_t's remainder
@@ -274,11 +278,11 @@ ssm_scan_kernel(const float *__restrict__ act, const float4 *__restrict__ step, 
         }
         __syncthreads();   // before the stage is loaded again
     }
-    // what is left of the remainders, but not to an infinity
+    // what is left of the remainders
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        S[i].x = fmaf(carry, fminf(fmaxf(S[i].x, -FLT_MAX), FLT_MAX), S[i].x);
-        S[i].y = fmaf(carry, fminf(fmaxf(S[i].y, -FLT_MAX), FLT_MAX), S[i].y);
+        S[i].x = fmaf(carry, finite(S[i].x), S[i].x);
+        S[i].y = fmaf(carry, finite(S[i].y), S[i].y);
     }
     float *const to = STATE_ONLY ? seg.state + slot * one : k == last && S_final ? S_final + n * one : nullptr;
     if (to) {
@@ -467,10 +471,10 @@ ssm_decode_kernel(const Raw<T> raw, const T *__restrict__ dt, long long ld_dt, c
     for (int i = 0; i < NV; ++i) {
         const int row = row0 + i * ROWS;
         const float bb = bs[row], cc = cs[row];
-        s[i].x = fmaf(a.x, s[i].x, fmaf(a.y, s[i].x, bb * x.x)); y.x = fmaf(cc, s[i].x, y.x);
-        s[i].y = fmaf(a.x, s[i].y, fmaf(a.y, s[i].y, bb * x.y)); y.y = fmaf(cc, s[i].y, y.y);
-        s[i].z = fmaf(a.x, s[i].z, fmaf(a.y, s[i].z, bb * x.z)); y.z = fmaf(cc, s[i].z, y.z);
-        s[i].w = fmaf(a.x, s[i].w, fmaf(a.y, s[i].w, bb * x.w)); y.w = fmaf(cc, s[i].w, y.w);
+        s[i].x = fmaf(a.x, s[i].x, fmaf(a.y, finite(s[i].x), bb * x.x)); y.x = fmaf(cc, s[i].x, y.x);
+        s[i].y = fmaf(a.x, s[i].y, fmaf(a.y, finite(s[i].y), bb * x.y)); y.y = fmaf(cc, s[i].y, y.y);
+        s[i].z = fmaf(a.x, s[i].z, fmaf(a.y, finite(s[i].z), bb * x.z)); y.z = fmaf(cc, s[i].z, y.z);
+        s[i].w = fmaf(a.x, s[i].w, fmaf(a.y, finite(s[i].w), bb * x.w)); y.w = fmaf(cc, s[i].w, y.w);
         __stcs(reinterpret_cast<float4 *>(Sh + (size_t)i * ROWS * P), s[i]);
     }
     *reinterpret_cast<float4 *>(&part[row0][4 * q]) = y;

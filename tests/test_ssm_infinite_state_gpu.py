@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import ssm_oracle as so
+from linear_attention_token_shortconv_b200 import gdn
 from test_ssm_gpu import BF16, F32, bounds, check, prefill
 
 pytestmark = pytest.mark.gpu
@@ -45,3 +46,21 @@ def test_prefill(cuda_device, dtype, T):
     rel, operands = bounds(dtype, dtype)
     check(out[:, ~hit], y[:, ~hit], ya[:, :, ~hit], rel, operands)
     assert torch.equal(out[:, hit].double(), y[:, hit])          # infinities, by their sign
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_step(cuda_device, dtype):
+    steps = 5
+    inp = _slow(so.make_inputs([steps], H, G, P, N, dtype, cuda_device, seed=52))
+    y, Sr, tail, ya, Sa = so.batch(inp, [steps])
+    S, hist = inp["S0"].clone(), inp["hist"].clone()
+    outs = []
+    for t in range(steps):
+        sl = slice(t, t + 1)
+        outs.append(gdn.ssm_decode_step(inp["x"][sl], inp["B"][sl], inp["C"][sl], inp["dt"][sl], inp["conv_w"], hist,
+                                        inp["A"], inp["b_dt"], S, conv_b=inp["conv_b"], D=inp["D"], z=inp["z"][sl]))
+    _same_state(S, Sr, Sa)
+    hit = _columns(cuda_device)
+    out = torch.cat(outs)
+    check(out[:, ~hit], y[:, ~hit], ya[:, :, ~hit], bounds(dtype, dtype)[0])
+    assert torch.equal(out[:, hit].double(), y[:, hit]) and torch.equal(hist, tail)
