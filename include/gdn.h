@@ -375,9 +375,9 @@ typedef struct {
  *   conv_hist [N_seq, 3, H P + 2 G N] in_dtype: the raw channels of the three tokens
  *             before each sequence, oldest first, or NULL for zeros
  *   cu_seqlens [N_seq + 1] int32 DEVICE prefix offsets as for gdn_prefill, or NULL for
- *             equal lengths.  cu[N_seq] may be less than N_tok: the tokens behind it
- *             are not read and their rows of out stay as they were.  Offsets are
- *             clamped to [0, N_tok] and to non-decreasing pairs.
+ *             equal lengths.  cu[N_seq] may be less than N_tok: what the tokens behind
+ *             it hold has no effect and their rows of out stay as they were.  Offsets
+ *             are clamped to [0, N_tok] and to non-decreasing pairs.
  *   out       [N_tok, H, P] packed, out_dtype, written
  *   S_final   [N_seq, H, N, P] fp32 final states, written, or NULL; may be S0
  *   conv_tail [N_seq, 3, H P + 2 G N] in_dtype, written, or NULL: the history that

@@ -56,11 +56,19 @@ ssm_act_kernel(const Raw<T> raw, const T *__restrict__ hist, const float *__rest
     const int chans = raw.hp + 2 * raw.gn;
     const int v = blockIdx.y * blockDim.x + threadIdx.x;
     const int t0 = blockIdx.x * ACT_TOK, t1 = min(t0 + ACT_TOK, n_tok);
+    int n, begin, end;   // the sequence of t0
+    auto locate = [&] {
+        n = cu ? seq_of_token(cu, n_seq, t0) : t0 / (n_tok / n_seq);
+        seq_range(cu, n_seq, n_tok, n, begin, end);
+    };
     if (v >= chans / 4) {
         const int h = v - chans / 4;
         if (h >= H) return;
         const float rate = expf(__ldg(A + h)), bias = __ldg(b_dt + h);
+        locate();
         for (int t = t0; t < t1; ++t) {
+            while (t >= end && n + 1 < n_seq) seq_range(cu, n_seq, n_tok, ++n, begin, end);
+            if (t < begin || t >= end) continue;   // behind the last sequence
             const float d = softplus_acc(to_f32(dt[t * ld_dt + h]) + bias);
             const float2 a = decay_pair(rate * d);
             // the log is bounded so that sums of it stay finite; e^-10000 is 0
@@ -73,9 +81,7 @@ ssm_act_kernel(const Raw<T> raw, const T *__restrict__ hist, const float *__rest
 #pragma unroll
     for (int e = 0; e < 4; ++e) w[e] = __ldg(reinterpret_cast<const float4 *>(conv_w) + c + e);
     const float4 b4 = conv_b ? __ldg(reinterpret_cast<const float4 *>(conv_b) + v) : make_float4(0, 0, 0, 0);
-    int n = cu ? seq_of_token(cu, n_seq, t0) : t0 / (n_tok / n_seq);
-    int begin, end;
-    seq_range(cu, n_seq, n_tok, n, begin, end);
+    locate();
     float4 r[4];   // raw rows t - 3 .. t
     bool fresh = true;
     for (int t = t0; t < t1; ++t) {
