@@ -45,14 +45,16 @@ __device__ __forceinline__ float2 decay_pair(float t) {
 }
 __device__ __forceinline__ float relative_rest(float2 a) { return a.y == 0.f ? 0.f : a.y / a.x; }
 
-// a (1 + carry) as one fp32 factor; carry becomes what that rounding leaves, for the next
-// factor.  So a product of decays stays within one rounding of the true one however long it
-// is.  A remainder added to the state instead, S + rest S, is rounded in its turn, and where
-// rest S is a few units of S the same way thousands of times (1e-4 of a state after 32768
-// tokens); it would also make NaN of an infinite state.
+// a (1 + carry) as one fp32 factor d; carry becomes what that rounding leaves, for the next
+// factor.  So a product of decays stays within a rounding or two of the true one however
+// long it is.  (What is left of a (1 + carry) is a (1 + carry) - d, and relative to d that
+// over a: the division is left out, for it changes carry by 1 - a of itself, and a state
+// remembers 1 / (1 - a) decays.)  A remainder added to the state instead, S + rest S, is
+// rounded in its turn, and where rest S is a few units of S the same way thousands of times
+// (1e-4 of a state after 32768 tokens); it would also make NaN of an infinite state.
 __device__ __forceinline__ float next_decay(float a, float &carry) {
     const float d = fmaf(carry, a, a);
-    carry = a > 0.5f ? carry - __fdividef(d - a, a) : 0.f;
+    carry = fmaf(carry, a, a - d);
     return d;
 }
 

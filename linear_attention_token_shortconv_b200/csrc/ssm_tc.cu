@@ -41,8 +41,8 @@ constexpr int PREP_THREADS = 512;
 constexpr int MIN_SEG = 3;        // chunks of a segment
 constexpr int REC = 368;          // floats of one (chunk, head) record
 // record: L log2 e [64] | u [64] | u e^R [64] | 2^ec e^L [64] | 2^ec umax [64] |
-// u e^{L_31 - L} of the first 32 tokens | e^L_end, umax
-constexpr int R_L = 0, R_U = 64, R_W = 128, R_YI = 192, R_YW = 256, R_UH = 320, R_DEC = 352, R_UMAX = 353;
+// u e^{L_31 - L} of the first 32 tokens | e^L_end, its relative remainder, L_end, umax
+constexpr int R_L = 0, R_U = 64, R_W = 128, R_YI = 192, R_YW = 256, R_UH = 320, R_END = 352;
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr uint32_t MAX_POLLS = 1u << 24;
 // 16 warps compute; one more issues the MMAs and one the copies (and two idle: registers
@@ -393,8 +393,8 @@ __global__ void __launch_bounds__(stc::PREP_THREADS, 2) ssm_prep_kernel(const Pr
             const float in_half = __shfl_down_sync(0xffffffffu, suf0, 1);
             rec[R_UH + lane] = u[0] * expf(lane == 31 ? 0.f : in_half);
             if (lane == 0) {
-                rec[R_DEC] = expf(total);
-                rec[R_UMAX] = inv;
+                const float2 a = ssm::decay_pair(-total);
+                *reinterpret_cast<float4 *>(rec + R_END) = make_float4(a.x, ssm::relative_rest(a), total, inv);
             }
         }
     }
@@ -411,7 +411,7 @@ struct ChainArgs {
     bf16 *out;
     float *S_final;
     float *seg_state;   // [cap][blocks][N][128]: of segment k of a sequence in row first + k
-    float *seg_decay;   // [cap][blocks][2]
+    float *seg_decay;   // [cap][blocks][2]: log
     const int2 *cuts;   // as in PrepArgs
     const int4 *rows;
     int n_seq, n_tok, H, G, P, blocks_per_group;
@@ -441,7 +441,7 @@ static_assert(Smem<128>::SIZE <= 232448, "227 KB per block");
 }  // namespace stc
 
 // One CTA per 128 columns of a sequence's segment.  STATE_ONLY: only the state, from zero,
-// into seg_state with the product of its decays.  Otherwise the whole mixer over the
+// into seg_state with the sum of its log-decays.  Otherwise the whole mixer over the
 // segment.
 template <int N, bool STATE_ONLY>
 __device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMaps &maps, const int n, const int seg,
@@ -658,8 +658,17 @@ __device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMap
                 if (one && *abort_flag == 0) issue(c + 2);
                 __syncwarp();
             }
+            float carry = 0.f;   // of this lane's half
             for (int c = 0; !STATE_ONLY && c < chunks; ++c) {
                 if (c >= 1) wait(bar_y, (uint32_t)(c - 1) & 1u);
+                // the decays that the state takes, in place, before the meeting: this warp has time
+                wait(full + (c & 1), (uint32_t)(c >> 1) & 1u);
+                if (lane < 2) {
+                    float *e = reinterpret_cast<float *>(sm + Sm::OFF_REC) + ((c & 1) * 2 + lane) * REC + R_END;
+                    carry += e[1];
+                    e[0] = ssm::next_decay(e[0], carry);
+                    umma::fence_proxy_async_smem();   // before the stage is loaded again
+                }
                 arrive();
                 wait(bar_m, (uint32_t)c & 1u);
                 if (one) {
@@ -696,6 +705,7 @@ __device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMap
         regs_inc<COMPUTE_REGS>();
         const uint32_t lane_off = (uint32_t)(32 * q) << 16;
         float2 S[16];
+        float carry = 0.f;   // of the decays that join segments, or of a states' pass (the copying warp's, of the chunks' else)
 #pragma unroll
         for (int j = 0; j < 16; ++j) S[j] = make_float2(0.f, 0.f);
         if (owner) {
@@ -704,7 +714,12 @@ __device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMap
             const float *p = joined ? seg_ptr(0) : seg > 0 || !a.S0 ? nullptr : a.S0 + sbase;
             for (int k = 0; p && k < (joined ? seg : 1); ++k) {
                 if (k > 0) p = seg_ptr(k);
-                const float d = k > 0 ? __ldg(a.seg_decay + seg_at(k) * 2 + (cg >> 1)) : 0.f;
+                float d = 0.f;
+                if (k > 0) {
+                    const float2 e = ssm::decay_pair(-__ldg(a.seg_decay + seg_at(k) * 2 + (cg >> 1)));
+                    carry += ssm::relative_rest(e);
+                    d = ssm::next_decay(e.x, carry);
+                }
 #pragma unroll
                 for (int j = 0; j < 16; j += 2) {
                     const float4 v = *reinterpret_cast<const float4 *>(p + 2 * j);
@@ -794,7 +809,7 @@ __device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMap
         };
 
         const float dskip = !STATE_ONLY && a.D ? __ldg(a.D + (q < 2 ? head0 : head1)) : 0.f;
-        float decay0 = 1.f, decay1 = 1.f;   // of the whole segment (state pass)
+        float log_hi = 0.f, log_lo = 0.f;   // sum of the segment's log-decays (state pass)
         // operand addresses of this thread: a row's 16-byte chunks k, k ^ 1, ... differ by an
         // exclusive or with the chunk's bits
         const uint32_t p_x = sT + Sm::OFF_X + half * 8192 + umma::sw128_offset(4 * warp, (lane & 15) >> 1) + 8 * (lane & 1);
@@ -890,10 +905,13 @@ __device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMap
                 scale_pow2(m.y, 13, xs1, i1);
                 wait(full + (c & 1), (uint32_t)(c >> 1) & 1u);
                 store_x(half ? r + REC : r, half ? xs1 : xs0, (c & 1 ? Sm::OFF_Z : Sm::OFF_XH) - Sm::OFF_X);
-                dec = (cg < 2 ? r : r + REC)[R_DEC];
-                add = (cg < 2 ? r : r + REC)[R_UMAX] * (cg < 2 ? i0 : i1);
-                decay0 *= r[R_DEC];
-                decay1 *= r[REC + R_DEC];
+                const float4 e = *reinterpret_cast<const float4 *>((cg < 2 ? r : r + REC) + R_END);
+                carry += e.y;
+                dec = ssm::next_decay(e.x, carry);
+                add = e.w * (cg < 2 ? i0 : i1);
+                const float sum = log_hi + e.z;   // two sums, since equal addends are rounded alike
+                log_lo += e.z - (sum - log_hi);
+                log_hi = sum;
                 umma::fence_proxy_async_smem();
                 umma::tc_fence_before();
                 __syncwarp();
@@ -1015,8 +1033,8 @@ __device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMap
             wait(bar_u, ph);
             umma::tc_fence_after();
             {
-                const float *rs = cg < 2 ? rec0 : rec1;
-                const float dec = rs[R_DEC], add = rs[R_UMAX] * (cg < 2 ? xinv0 : xinv1);
+                const float *rs = (cg < 2 ? rec0 : rec1) + R_END;
+                const float dec = rs[0], add = rs[3] * (cg < 2 ? xinv0 : xinv1);
                 const float2 dec2 = make_float2(dec, dec), add2 = make_float2(add, add);
                 uint32_t v[32];
                 umma::tmem_ld32_nowait(T_U + lane_off + sc0, v);
@@ -1073,7 +1091,7 @@ __device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMap
             for (int j = 0; j < 16; j += 2)
                 *reinterpret_cast<float4 *>(to + 2 * j) = make_float4(S[j].x, S[j].y, S[j + 1].x, S[j + 1].y);
             if (STATE_ONLY && lane == 0 && q == 0 && (cg & 1) == 0)
-                a.seg_decay[seg_at(seg) * 2 + (cg >> 1)] = cg < 2 ? decay0 : decay1;
+                a.seg_decay[seg_at(seg) * 2 + (cg >> 1)] = log_hi + log_lo;
         }
     }
     umma::tc_fence_before();

@@ -20,7 +20,7 @@ import pytest
 import torch
 
 import ssm_oracle as so
-from test_ssm_gpu import E32, F32, bounds, check, prefill
+from test_ssm_gpu import BF16, E32, F32, bounds, check, prefill
 
 pytestmark = pytest.mark.gpu
 
@@ -50,7 +50,7 @@ def _same_state(S, Sr, Sa, updates, name):
     assert bool((drift.abs() <= 2.0 ** -19 + walk / math.sqrt(N * P)).all()), (name, drift.tolist())
 
 
-@pytest.mark.parametrize("dtype", [F32], ids=["f32"])
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 def test_equal_steps(cuda_device, dtype):
     """The state before the prompt is far larger than what the prompt adds, and is still
     there at its end.  Alone the prompt is cut into segments; beside 600 empty sequences
