@@ -393,11 +393,12 @@ typedef struct {
  * heads up to 65535 (GDN_ERR_UNSUPPORTED above).
  * The state is held to fp32 on every path.  With bf16 tensors and a bf16 result the
  * products of y take fp16-rounded operands with fp32 sums (chunks of 64 tokens on the
- * tensor cores); there the 64 tokens' values of x of one head, and its state, share one
- * power of two: values are as accurate as stated down to 2^-15 of the largest in the
- * state and 2^-27 of it in y.  Otherwise all arithmetic is fp32.  Infinities and NaN go
- * where the formulas take them, never to an earlier token (an infinite x may come out as
- * NaN).  Up to four kernels on `stream`, and
+ * tensor cores); there the 64 tokens' values of x of one head share one power of two, and
+ * so does its state: x down to 2^-15 of the largest of them enters the state, and x or
+ * state down to 2^-27 of the largest enters y, as accurately as stated.  Otherwise all
+ * arithmetic is fp32.  Infinities and NaN go where the formulas take them, never to an
+ * earlier token; an infinite state stays infinite (with bf16 tensors and a bf16 result an
+ * infinite x, B or dt_logit may come out as NaN).  Up to four kernels on `stream`, and
  * a stream-ordered workspace of at most gdn_ssm_prefill_workspace_size() bytes from the
  * library's pool.  An expired wait raises GDN_ERRF_SSM.
  */

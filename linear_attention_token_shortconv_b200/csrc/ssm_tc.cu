@@ -14,8 +14,9 @@
 // hi + lo (22 bits; the product lo lo, 2^-22 of the whole, is left out), three MMAs into
 // one fp32 accumulator.  y is rounded to bf16, so its products take one fp16 operand
 // each (2^-11 against the result's 2^-9).  fp16's narrow range does not show: every row
-// of B and C is scaled by its own power of two, x and the state by one per chunk and
-// head, D_s by one per chunk, and the powers are multiplied back in fp32.
+// of B, of C and of the decayed scores is scaled by its own power of two, the weights of
+// the state's x by one per chunk, x and the state by one per chunk and head, and the
+// powers are multiplied back in fp32.
 //
 // Tokens past a sequence's end are zeros in the tiles and zeroed in x: a tile never
 // holds another sequence's rows, so its NaN stays there.
@@ -39,10 +40,11 @@ namespace stc {
 constexpr int Q = 64;             // tokens per chunk
 constexpr int PREP_THREADS = 512;
 constexpr int MIN_SEG = 3;        // chunks of a segment
-constexpr int REC = 368;          // floats of one (chunk, head) record
-// record: L log2 e [64] | u [64] | u e^R [64] | 2^ec e^L [64] | 2^ec umax [64] |
-// u e^{L_31 - L} of the first 32 tokens | e^L_end, its relative remainder, L_end, umax
-constexpr int R_L = 0, R_U = 64, R_W = 128, R_YI = 192, R_YW = 256, R_UH = 320, R_END = 352;
+constexpr int REC = 420;          // floats of one (chunk, head) record
+// record, with u = 2^eb D below 1, w and r powers of two: L log2 e [64] | u [64] | w u e^R [64] |
+// 2^ec e^L [64] | 2^ec umax / r [64] | u e^{L_31 - L} of the first 32 tokens |
+// L log2 e + log2 r [64] | e^L_end, its relative remainder, L_end, umax / w
+constexpr int R_L = 0, R_U = 64, R_W = 128, R_YI = 192, R_YW = 256, R_UH = 320, R_LR = 352, R_END = 416;
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr uint32_t MAX_POLLS = 1u << 24;
 // 16 warps compute; one more issues the MMAs and one the copies (and two idle: registers
@@ -378,23 +380,49 @@ __global__ void __launch_bounds__(stc::PREP_THREADS, 2) ssm_prep_kernel(const Pr
             const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(finite_abs(u[0]), finite_abs(u[1]))));
             float s, inv;
             scale_pow2(m, -1, s, inv);   // u < 1
+            float w[2];
+            int lr[2];   // log2 u - L, rounded up
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                u[i] *= s;
+                w[i] = u[i] * expf(i ? aft1 : aft0);
+                pre[i] *= kLog2e;
+                lr[i] = max(__float2int_ru(__log2f(finite_abs(u[i])) - pre[i]), -30000);
+            }
+            // Row t of the decayed scores is made of u_s e^{L_t - L_s}; its own power of two r
+            // brings the largest of them, 2^{L_t + max_{s <= t} (log2 u_s - L_s)}, to 1/4 .. 1
+            // (r at most 2^100: what is smaller than that against the chunk's u is nothing).
+            // The maxima of both halves side by side in one word, |L| < 12000.
+            uint32_t top = __byte_perm(lr[0], lr[1], 0x5410);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t p = __shfl_up_sync(0xffffffffu, top, o);
+                if (lane >= o) top = __vmaxs2(top, p);
+            }
+            lr[0] = (short)(top & 0xffff);
+            lr[1] = max((short)(top >> 16), (short)(__shfl_sync(0xffffffffu, top, 31) & 0xffff));
+            // The state's operands: the largest u e^R to 1/2 .. 1, whatever u was before a decay.
+            const uint32_t mw = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(finite_abs(w[0]), finite_abs(w[1]))));
+            float sw, invw;
+            scale_pow2(mw, -1, sw, invw);
             float *rec = a.rec + ((size_t)slot * a.H + h) * REC;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int r = lane + 32 * i;
-                u[i] *= s;
-                rec[R_L + r] = pre[i] * kLog2e;
+                const float k = fminf(-ceilf(pre[i] + lr[i]), 100.f);
+                rec[R_L + r] = pre[i];
                 rec[R_U + r] = u[i];
-                rec[R_W + r] = u[i] * expf(i ? aft1 : aft0);
-                rec[R_YI + r] = ec[r] * expf(pre[i]);
-                rec[R_YW + r] = ec[r] * inv;
+                rec[R_W + r] = w[i] * sw;
+                rec[R_YI + r] = ec[r] * exp2f(pre[i]);
+                rec[R_YW + r] = ec[r] * inv * __uint_as_float((uint32_t)(127 - (int)k) << 23);
+                rec[R_LR + r] = pre[i] + k;
             }
             // e^{L_31 - L_s}, the sum after s inside the first half
             const float in_half = __shfl_down_sync(0xffffffffu, suf0, 1);
             rec[R_UH + lane] = u[0] * expf(lane == 31 ? 0.f : in_half);
             if (lane == 0) {
                 const float2 a = ssm::decay_pair(-total);
-                *reinterpret_cast<float4 *>(rec + R_END) = make_float4(a.x, ssm::relative_rest(a), total, inv);
+                *reinterpret_cast<float4 *>(rec + R_END) = make_float4(a.x, ssm::relative_rest(a), total, inv * invw);
             }
         }
     }
@@ -989,7 +1017,7 @@ __device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMap
                 if ((q & 1) || cg < 2) {   // tokens 0 .. 31 see nothing of 32 .. 63
                     uint32_t sc[16];
                     umma::tmem_ld16_nowait(T_SC + lane_off + 64 * hv + 16 * cg, sc);
-                    const float Lt = recv[R_L + t];
+                    const float Lt = recv[R_LR + t];   // times the row's power of two
                     umma::tmem_ld_wait();
                     if ((q & 1) && cg < 2) {
                         // t > 31 >= s: e^{L_t - L_s} = e^{L_t - L_31} e^{L_31 - L_s}, both at most 1
