@@ -12,8 +12,7 @@ pytestmark = pytest.mark.gpu
 
 
 def _inputs(T, dtype, device, P, N, seed):
-    inp = so.make_inputs([T], 4, 2, P, N, dtype, device, seed=seed, gate=False, state=False, bias=False)
-    return inp
+    return so.make_inputs([T], 4, 2, P, N, dtype, device, seed=seed, gate=False, state=False, bias=False)
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
@@ -50,3 +49,16 @@ def test_rows_of_unlike_size(cuda_device, dtype):
     inp["proj"][:, 2 * hp:2 * hp + gn] *= torch.exp2(e.round())[:, None].to(dtype)
     inp["dt"][:] += (e / 8).to(dtype)[:, None]
     agree(inp, [T])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("P,N", [(64, 128), (128, 64)])
+@pytest.mark.parametrize("at", [3, 40, 70])
+def test_large_x_forgotten(cuda_device, dtype, P, N, at):
+    """A token whose x is 2^12 times its neighbours', near the documented 2^15, which fast
+    decays take away inside the chunk."""
+    inp = _inputs(100, dtype, cuda_device, P, N, seed=64)
+    hp = 4 * P
+    inp["proj"][at, hp:2 * hp] *= 2.0 ** 12
+    inp["A"] = torch.full((4,), 5.0, device=cuda_device)
+    agree(inp, [100])
