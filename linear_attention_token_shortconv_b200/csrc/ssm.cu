@@ -113,13 +113,10 @@ ssm_act_kernel(const Raw<T> raw, const T *__restrict__ hist, const float *__rest
 
 constexpr int SCAN_COLS = 16, SCAN_TOK = 16, SCAN_THREADS = 64;
 
-// An asynchronous copy of B bytes to shared memory, zeros where `in` is false.
-template <int B> __device__ __forceinline__ void copy_async(void *dst, const void *src, bool in) {
+// An asynchronous copy of 16 bytes to shared memory, zeros where `in` is false.
+__device__ __forceinline__ void copy_async(void *dst, const void *src, bool in) {
     const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
-    if constexpr (B == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(in ? 16 : 0) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d), "l"(src), "n"(B), "r"(in ? B : 0) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
 
 // Sequences of at least `from` tokens in segments of `len` (a multiple of SCAN_TOK).
@@ -174,14 +171,14 @@ ssm_scan_kernel(const float *__restrict__ act, const float4 *__restrict__ step, 
         for (int i = tid; i < SCAN_TOK * (N / 4); i += SCAN_THREADS) {
             const int r = i / (N / 4), q = i % (N / 4);
             const float *src = rows + (r < len ? (size_t)r * chans : 0) + H * P + g * N + 4 * q;
-            copy_async<16>(&st.b[r][4 * q], src, r < len);
-            if (!STATE_ONLY) copy_async<16>(&st.c[r][4 * q], src + G * N, r < len);
+            copy_async(&st.b[r][4 * q], src, r < len);
+            if (!STATE_ONLY) copy_async(&st.c[r][4 * q], src + G * N, r < len);
         }
         for (int i = tid; i < SCAN_TOK * (SCAN_COLS / 4); i += SCAN_THREADS) {
             const int r = i / (SCAN_COLS / 4), q = i % (SCAN_COLS / 4);
-            copy_async<16>(&st.x[r][4 * q], rows + (r < len ? (size_t)r * chans : 0) + h * P + p0 + 4 * q, r < len);
+            copy_async(&st.x[r][4 * q], rows + (r < len ? (size_t)r * chans : 0) + h * P + p0 + 4 * q, r < len);
         }
-        if (tid < SCAN_TOK) copy_async<16>(&st.d[tid], step + (size_t)(t0 + (tid < len ? tid : 0)) * H + h, tid < len);
+        if (tid < SCAN_TOK) copy_async(&st.d[tid], step + (size_t)(t0 + (tid < len ? tid : 0)) * H + h, tid < len);
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     if (begin < end) load(begin, stages[0]);

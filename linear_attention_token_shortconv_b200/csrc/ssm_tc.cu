@@ -733,7 +733,7 @@ __device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMap
         regs_inc<COMPUTE_REGS>();
         const uint32_t lane_off = (uint32_t)(32 * q) << 16;
         float2 S[16];
-        float carry = 0.f;   // of the decays that join segments, or of a states' pass (the copying warp's, of the chunks' else)
+        float carry = 0.f;   // of the decays that join segments, or of a states' pass
 #pragma unroll
         for (int j = 0; j < 16; ++j) S[j] = make_float2(0.f, 0.f);
         if (owner) {
@@ -966,32 +966,30 @@ __device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMap
 #pragma unroll
                 for (int j = 0; j < 16; ++j) S[j] = ffma2(dec2, S[j], fmul2(add2, as_float2(v[2 * j], v[2 * j + 1])));
             }
-        }
-        // maxima of this chunk, of the next (written from its convolution on) and of the one
-        // after (cleared now; its last readers, of the previous chunk, have met since)
-        uint32_t *m_now = mx, *m_next = mx + 4, *m_after = mx + 8;
-        if (!STATE_ONLY) arrive();
-        for (int c = 0; !STATE_ONLY && c < chunks; ++c) {
-            const int b = c & 1;
-            const uint32_t ph = (uint32_t)c & 1u, ph_full = (uint32_t)(c >> 1) & 1u;
-            const float *rec0 = reinterpret_cast<const float *>(sm + Sm::OFF_REC) + b * 2 * REC, *rec1 = rec0 + REC;
-            const float *recv = hv ? rec1 : rec0;
-            wait(bar_m, ph);
-            if (tid < 4) m_after[tid] = 0;
+        } else {
+            // maxima of this chunk, of the next (written from its convolution on) and of the one
+            // after (cleared now; its last readers, of the previous chunk, have met since)
+            uint32_t *m_now = mx, *m_next = mx + 4, *m_after = mx + 8;
+            arrive();
+            for (int c = 0; c < chunks; ++c) {
+                const int b = c & 1;
+                const uint32_t ph = (uint32_t)c & 1u, ph_full = (uint32_t)(c >> 1) & 1u;
+                const float *rec0 = reinterpret_cast<const float *>(sm + Sm::OFF_REC) + b * 2 * REC, *rec1 = rec0 + REC;
+                const float *recv = hv ? rec1 : rec0;
+                wait(bar_m, ph);
+                if (tid < 4) m_after[tid] = 0;
 
-            // ---- scales; operands into shared memory
-            const uint4 mxv = *reinterpret_cast<const uint4 *>(m_now);
-            float xs0, xs1, xinv0, xinv1;
-            scale_pow2(mxv.x, 13, xs0, xinv0);
-            scale_pow2(mxv.y, 13, xs1, xinv1);
-            float sinv = 0.f;                    // of the rows of y of this thread
-            wait(full + b, ph_full);
-            store_x(half ? rec1 : rec0, half ? xs1 : xs0, Sm::OFF_XH - Sm::OFF_X);
-            if (!STATE_ONLY) {
+                // ---- scales; operands into shared memory
+                const uint4 mxv = *reinterpret_cast<const uint4 *>(m_now);
+                float xs0, xs1, xinv0, xinv1;
+                scale_pow2(mxv.x, 13, xs0, xinv0);
+                scale_pow2(mxv.y, 13, xs1, xinv1);
+                wait(full + b, ph_full);
+                store_x(half ? rec1 : rec0, half ? xs1 : xs0, Sm::OFF_XH - Sm::OFF_X);
                 float s0, s1, i0, i1;
                 scale_pow2(mxv.z, 13, s0, i0);
                 scale_pow2(mxv.w, 13, s1, i1);
-                sinv = hv ? i1 : i0;
+                const float sinv = hv ? i1 : i0;     // of the rows of y of this thread
                 const float ss = cg < 2 ? s0 : s1;
                 const float2 ss2 = make_float2(ss, ss);
                 if (srow < N) {
@@ -1049,28 +1047,20 @@ __device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMap
                 umma::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar_w);
-            } else {
-                umma::fence_proxy_async_smem();
-                umma::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar_x);
-                if (c + 1 < chunks) fetch(c + 1);
-            }
-            if (c + 1 < chunks) convolve(c + 1, m_next);
-            // ---- state
-            wait(bar_u, ph);
-            umma::tc_fence_after();
-            {
-                const float *rs = (cg < 2 ? rec0 : rec1) + R_END;
-                const float dec = rs[0], add = rs[3] * (cg < 2 ? xinv0 : xinv1);
-                const float2 dec2 = make_float2(dec, dec), add2 = make_float2(add, add);
-                uint32_t v[32];
-                umma::tmem_ld32_nowait(T_U + lane_off + sc0, v);
-                umma::tmem_ld_wait();
+                if (c + 1 < chunks) convolve(c + 1, m_next);
+                // ---- state
+                wait(bar_u, ph);
+                umma::tc_fence_after();
+                {
+                    const float *rs = (cg < 2 ? rec0 : rec1) + R_END;
+                    const float dec = rs[0], add = rs[3] * (cg < 2 ? xinv0 : xinv1);
+                    const float2 dec2 = make_float2(dec, dec), add2 = make_float2(add, add);
+                    uint32_t v[32];
+                    umma::tmem_ld32_nowait(T_U + lane_off + sc0, v);
+                    umma::tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 16; ++j) S[j] = ffma2(dec2, S[j], fmul2(add2, as_float2(v[2 * j], v[2 * j + 1])));
-            }
-            if (!STATE_ONLY) {
+                    for (int j = 0; j < 16; ++j) S[j] = ffma2(dec2, S[j], fmul2(add2, as_float2(v[2 * j], v[2 * j + 1])));
+                }
                 state_max(m_next);
                 // ---- y before its gate
                 const float fx = hv ? xinv1 : xinv0;
@@ -1093,15 +1083,15 @@ __device__ __forceinline__ void chain_segment(const ChainArgs &a, const ChainMap
                 for (int e = 0; e < 8; ++e)
                     y[e] = ffma2(as_float2(yi[2 * e], yi[2 * e + 1]), fi2,
                                  ffma2(as_float2(yw[2 * e], yw[2 * e + 1]), fw2, y[e]));
+                uint32_t *const done = m_now;
+                m_now = m_next;
+                m_next = m_after;
+                m_after = done;
             }
-            uint32_t *const done = m_now;
-            m_now = m_next;
-            m_next = m_after;
-            m_after = done;
-        }
-        if (!STATE_ONLY && chunks > 0) {
-            gate(chunks - 1);
-            arrive();
+            if (chunks > 0) {
+                gate(chunks - 1);
+                arrive();
+            }
         }
         float *const to = !owner || *abort_flag                         ? nullptr
                           : STATE_ONLY || (seg == 0 && last_seg > 0)    ? seg_ptr(seg)
