@@ -234,7 +234,7 @@ struct Tile {
 template <class Sh, typename Tout>
 __global__ void __launch_bounds__(Sh::THREADS, 1)
 gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const float *__restrict__ a_scale,
-                const float *__restrict__ b_scale, Tout *__restrict__ C, long long ldc, int split, int tma_out) {
+                const float *__restrict__ b_scale, Tout *__restrict__ C, long long ldc, int split, int bulk_n) {
     using namespace fp8;
     constexpr int BN = Sh::BN, NS = Sh::NS, NT = Sh::NT, EPC = Sh::EPC;
     constexpr bool SWAP = Sh::SWAP, PAIR = Sh::PAIR;
@@ -507,9 +507,11 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
                     for (int j = 0; j < EPC; ++j)
                         if (col0 + j < M) C[(col0 + j) * ldc + row] = from_f32<Tout>(el(j));
                 }
-            } else if (tma_out) {
+            } else if (bulk_n > 0) {
                 // rows of this warp through shared memory (128-byte rows, swizzled), then one
-                // bulk store per 128 bytes of columns; rows and columns outside C are not written
+                // bulk store per 128 bytes of columns.  It leaves out rows and columns outside its
+                // map, but columns in whole 16 bytes only, so the map ends at the last whole ones
+                // and what is behind them goes by itself.
                 constexpr int SC = 128 / (int)sizeof(Tout);        // columns of a 128-byte row
                 constexpr int GROUPS = Sh::OUT_WARP / 4096;        // of them in the buffer
                 uint8_t *buf = sm + Sh::OFF_OUT + (warp - 4) * Sh::OUT_WARP;
@@ -527,10 +529,16 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
                     if (lane == 0) {
 #pragma unroll
                         for (int gq = 0; gq < GROUPS && j0 + gq * SC < EPC; ++gq)
-                            if (col0 + j0 + gq * SC < N && row0 < M)
+                            if (col0 + j0 + gq * SC < bulk_n && row0 < M)
                                 umma::tma_store_3d(&maps.c, col0 + j0 + gq * SC, 0, row0, buf + gq * 4096);
                         umma::bulk_commit();
                     }
+                }
+                if (bulk_n < N && col0 + EPC > bulk_n && row < M) {
+                    Tout *crow = C + row * ldc + col0;
+#pragma unroll
+                    for (int j = 0; j < EPC; ++j)
+                        if (col0 + j >= bulk_n && col0 + j < N) crow[j] = from_f32<Tout>(el(j));
                 }
             } else if (row < M) {
                 Tout *crow = C + row * ldc + col0;
@@ -539,7 +547,7 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, int M, int N, int K, const
                     if (col0 + j < N) crow[j] = from_f32<Tout>(el(j));
             }
         }
-        if (tma_out && lane == 0) umma::bulk_wait_all();
+        if (bulk_n > 0 && lane == 0) umma::bulk_wait_all();
     }
     umma::tc_fence_before();
     __syncwarp();
@@ -637,9 +645,11 @@ cudaError_t launch_shape(int M, int N, int K, const void *A, long long lda, cons
     e = make_tma_mat_u8(reinterpret_cast<TmaMap *>(&m.b), Sh::SWAP ? A : B, K, Sh::SWAP ? M : N, Sh::SWAP ? lda : ldb,
                         Sh::PAIR ? Sh::B_ROWS / 2 : Sh::B_ROWS);
     if (e != cudaSuccess) return e;
-    const bool tma_out = !Sh::SWAP && (reinterpret_cast<uintptr_t>(C) & 15) == 0 && ldc * sizeof(Tout) % 16 == 0;
-    if (tma_out && (e = make_tma_mat_out(reinterpret_cast<TmaMap *>(&m.c), C, sizeof(Tout) == 2, N, M, ldc)) !=
-                       cudaSuccess)
+    // columns that bulk stores write: whole 16 bytes, where the rows are aligned to them
+    constexpr int VEC = 16 / (int)sizeof(Tout);
+    const int bulk_n = !Sh::SWAP && (reinterpret_cast<uintptr_t>(C) & 15) == 0 && ldc % VEC == 0 ? N / VEC * VEC : 0;
+    if (bulk_n > 0 && (e = make_tma_mat_out(reinterpret_cast<TmaMap *>(&m.c), C, sizeof(Tout) == 2, bulk_n, M, ldc)) !=
+                          cudaSuccess)
         return e;
     auto *kernel = gemm_fp8_kernel<Sh, Tout>;
     if ((e = allow_smem<Sh, Tout>(kernel)) != cudaSuccess) return e;
@@ -665,7 +675,7 @@ cudaError_t launch_shape(int M, int N, int K, const void *A, long long lda, cons
         if ((e = resident_pairs(kernel, cfg, sms, &pairs)) != cudaSuccess) return e;
         cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
     }
-    if ((e = cudaLaunchKernelEx(&cfg, kernel, m, M, N, K, a_scale, b_scale, static_cast<Tout *>(C), ldc, split, (int)tma_out)) !=
+    if ((e = cudaLaunchKernelEx(&cfg, kernel, m, M, N, K, a_scale, b_scale, static_cast<Tout *>(C), ldc, split, bulk_n)) !=
         cudaSuccess)
         return e;
     return launched();

@@ -128,7 +128,7 @@ cudaError_t make_tma_mat_u8(TmaMap *out, const void *base, int inner, int rows, 
 
 // A row-major result [rows][inner] of bf16 or fp32 (leading dimension ld elements, rows
 // 16-byte aligned) as a 3-D map {inner, 1, rows}, boxes of 128 bytes x 32 rows, 128-byte
-// swizzle.
+// swizzle.  inner is a multiple of 16 bytes: a store is cut off at whole 16 bytes only.
 cudaError_t make_tma_mat_out(TmaMap *out, const void *base, bool bf16, int inner, int rows, long long ld) {
     EncodeTiledFn fn;
     cudaError_t e = encoder(&fn);
