@@ -391,14 +391,16 @@ typedef struct {
  * bytes (GDN_ERR_ALIGNMENT otherwise); dt_logit, A, b_dt, D, cu_seqlens aligned to
  * their elements.  Token tensors may be NULL when total_tokens is 0.  Sequences and
  * heads up to 65535 (GDN_ERR_UNSUPPORTED above).
- * The state is held to fp32 on every path.  With bf16 tensors and a bf16 result the
- * products of y take fp16-rounded operands with fp32 sums (chunks of 64 tokens on the
- * tensor cores); there the 64 tokens' values of x of one head share one power of two, and
- * so does its state: x down to 2^-15 of the largest of them enters the state, and x or
- * state down to 2^-27 of the largest enters y, as accurately as stated.  Otherwise all
- * arithmetic is fp32.  Infinities and NaN go where the formulas take them, never to an
- * earlier token; an infinite state stays infinite (with bf16 tensors and a bf16 result an
- * infinite x, B or dt_logit may come out as NaN).  Up to four kernels on `stream`, and
+ * The state is held to fp32 on every path: it is rounded whenever tokens are added to it,
+ * 64 at a time with bf16 tensors and a bf16 result, else one at a time.  With bf16 tensors
+ * and a bf16 result the products run on the tensor cores: those of y take fp16-rounded
+ * operands with fp32 sums, and the 64 tokens' values of x of one head share one power of
+ * two, as do its state and each token's row of B.  x and B down to 2^-15 of the largest of
+ * them enter the state, and x or state down to 2^-27 of the largest enters y, as accurately
+ * as stated.  Otherwise all arithmetic is fp32.  Infinities and NaN go where the formulas
+ * take them, never to an earlier token; an infinite state stays infinite (with bf16 tensors
+ * and a bf16 result an infinite x, B or dt_logit may come out as NaN).  Up to four kernels
+ * on `stream`, and
  * a stream-ordered workspace of at most gdn_ssm_prefill_workspace_size() bytes from the
  * library's pool.  An expired wait raises GDN_ERRF_SSM.
  */

@@ -319,7 +319,9 @@ __global__ void __launch_bounds__(stc::PREP_THREADS, 2) ssm_prep_kernel(const Pr
                 for (int o = 1; o < VEC; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
             }
             float s, inv;
-            scale_pow2(m, 3, s, inv);   // |B'|, |C'| < 16: scores stay below 128 x 256
+            // B' < 2^14: its pairs keep 22 bits of an element down to 2^-15 of the row's largest;
+            // C' < 16: scores stay below 128 x 2^18
+            scale_pow2(m, isC ? 3 : 13, s, inv);
             if (v % VEC == 0) (isC ? ec : eb)[r] = inv;
             uint2 hi, lo2;
             const float2 u0 = fmul2(x[0], make_float2(s, s)), u1 = fmul2(x[1], make_float2(s, s));
@@ -390,8 +392,9 @@ __global__ void __launch_bounds__(stc::PREP_THREADS, 2) ssm_prep_kernel(const Pr
                 lr[i] = max(__float2int_ru(__log2f(finite_abs(u[i])) - pre[i]), -30000);
             }
             // Row t of the decayed scores is made of u_s e^{L_t - L_s}; its own power of two r
-            // brings the largest of them, 2^{L_t + max_{s <= t} (log2 u_s - L_s)}, to 1/4 .. 1
-            // (r at most 2^100: what is smaller than that against the chunk's u is nothing).
+            // brings the largest of them, 2^{L_t + max_{s <= t} (log2 u_s - L_s)}, to 2^-12 ..
+            // 2^-10, so that a score times it is below 2^15 (r at most 2^100: what is smaller
+            // than that against the chunk's u is nothing).
             // The maxima of both halves side by side in one word, |L| < 12000.
             uint32_t top = __byte_perm(lr[0], lr[1], 0x5410);
 #pragma unroll
@@ -409,7 +412,7 @@ __global__ void __launch_bounds__(stc::PREP_THREADS, 2) ssm_prep_kernel(const Pr
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int r = lane + 32 * i;
-                const float k = fminf(-ceilf(pre[i] + lr[i]), 100.f);
+                const float k = fminf(-10.f - ceilf(pre[i] + lr[i]), 100.f);
                 rec[R_L + r] = pre[i];
                 rec[R_U + r] = u[i];
                 rec[R_W + r] = w[i] * sw;
