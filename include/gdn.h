@@ -435,7 +435,7 @@ GDN_API gdn_status_t gdn_ssm_decode_step(const gdn_ssm_dims_t *dims, const void 
  * weights); the last block of a row or column may be smaller:
  *   amax = max(max |x|, 2^-64),  scale = amax / 448,  q = e4m3(x (448 / amax))
  * in fp32 with IEEE divisions, rounded to nearest even.  A block with a NaN gets a NaN
- * scale.
+ * scale; one with an infinity an infinite scale, NaN where it stands and zeros elsewhere.
  *   x      [rows, cols] in_dtype, rows ld_x elements apart
  *   q      [rows, cols] bytes, rows ld_q apart, written
  *   scale  [ceil(rows / block_rows), ceil(cols / 128)] fp32 packed, written
@@ -455,10 +455,11 @@ GDN_API gdn_status_t gdn_quant_fp8(int rows, int cols, const void *x, int64_t ld
  *   B       [N, K] e4m3 (a weight as [out features, in features]), rows ldb bytes
  *           apart; b_scale [ceil(N / 128), ceil(K / 128)] fp32 packed (block_rows = 128)
  *   C       [M, N] out_dtype, rows ldc elements apart, written
- * Products are exact, sums are fp32.  K, lda and ldb multiples of 16; A and B 16-byte
- * aligned, C to its elements (16 bytes and ldc a multiple of 16 bytes are faster).
- * M = 0 or N = 0 writes nothing.  One kernel; no workspace.  The sum's order depends on
- * the sizes only.  An expired wait raises GDN_ERRF_FP8.
+ * Products are exact, sums are fp32; a pair of scales is multiplied first, in fp32.
+ * K, lda and ldb multiples of 16; A and B 16-byte aligned, C to its elements (16 bytes
+ * and ldc a multiple of 16 bytes are faster).  M = 0 or N = 0 writes nothing.  One kernel;
+ * no workspace.  The sum's order depends on the sizes only.  An expired wait raises
+ * GDN_ERRF_FP8.
  */
 GDN_API gdn_status_t gdn_gemm_fp8(int M, int N, int K, const void *A, int64_t lda, const float *a_scale,
                                   const void *B, int64_t ldb, const float *b_scale, void *C, int64_t ldc,
@@ -507,7 +508,9 @@ GDN_API gdn_status_t gdn_prefill_noalloc(const gdn_dims_t *dims, const void *q, 
  * When both handles are non-NULL (cudaEvent_t values), each following call
  * records `begin` and `end` on its stream: gdn_prefill around all of its GPU
  * work on the tensor-core path (whose kernels overlap on two streams) and around
- * the state recurrence on the fp32 path; gdn_decode_step around its kernel.
+ * the state recurrence on the fp32 path; gdn_decode_step around its kernel;
+ * gdn_ssm_prefill and gdn_ssm_decode_step around all of theirs.  The GEMMs and
+ * gdn_quant_fp8 record nothing.
  * The hook stays until cleared with (NULL, NULL).  Recording adds no work to
  * the kernels; it lets a caller time the library's GPU work with CUDA events.
  */

@@ -26,8 +26,9 @@
 //
 // Measured.  16384 x 8512 x 2048, bf16: 244 us = 2.34 PFLOP/s in short runs, 295 where the
 // power limit holds the clock at 1.4 GHz; the MMAs alone need 174 at the rate of a 128 x
-// 256 x 128-byte block in 512 clocks.  What bounds it is
-// the operands' way into shared memory, 9 TB/s out of L2, with the power beside it.
+// 256 x 128-byte block in 512 clocks.  What bounds it is the round trip of a K block's
+// product through its two buffers (MMAs, commit, TMEM reads, scaling, hand-back: tensor
+// pipe 70 % active), with the clock beside it; L2 is at 39 %, DRAM lower.
 // 4 x 8512 x 2048: 6.4 us for 17.5 MB of weights, of it about 4 launch and first loads;
 // 333 x 2048 x 4112, fp32: 13.8 us, one wave of 96 tiles of 33 K blocks.
 #include <cuda.h>

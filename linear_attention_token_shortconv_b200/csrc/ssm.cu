@@ -14,7 +14,7 @@
 // warp sharing the columns and adding their parts of y by shuffles, four tokens
 // together.  What bounds it is the chain of tokens, at one or two warps a scheduler; few
 // and long sequences are cut into segments, whose states a first pass finds.
-// 1000 + 999 tokens, 16 heads of 64, N = 64: 76 us, of it 13 for ssm_act (111 uncut).
+// 1000 + 999 tokens, 16 heads of 64, N = 64: 76 us, of it 13 for ssm_act (129 uncut).
 #include <cuda_runtime.h>
 
 #include <cfloat>
@@ -329,12 +329,12 @@ cudaError_t launch_tail(const SsmArgs &a) {
 
 size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// Workspace of the fp32 prefill, and its segments.  A block alone on an SM takes 126 ns a
+// Workspace of the fp32 prefill, and its segments.  A block alone on an SM takes 129 ns a
 // token, a full SM 58 per block (N = 128), and segments cost half as much again for their
 // states.  So they are made where the sequences have no more blocks than there are SMs,
 // SCAN_FULL of them an SM, of the sequences that are longer than an even share of the work
-// (one of 8000 tokens, 16 heads of 64, N = 128: 1009 us whole, 471 with 3 to an SM, 333
-// with 6, 348 with 10; 4 of 2000 with 32 heads, more blocks than SMs: 467 whole, 697 cut).
+// (one of 8000 tokens, 16 heads of 64, N = 128: 1032 us whole, 479 with 3 to an SM, 343
+// with 6, 359 with 10; 4 of 2000 with 32 heads, more blocks than SMs: 482 whole, 633 cut).
 struct ScanPlan {
     int from, len, slots;
     size_t act, step, state, decay, s0_copy;

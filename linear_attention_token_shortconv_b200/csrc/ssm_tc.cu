@@ -1161,14 +1161,14 @@ struct Plan {
 // first launch runs segment 0, half as long, of every sequence and beside it the states of
 // the others, which take about 2 us a chunk; a second one the others, as many as there are SMs
 // (cap rows of blocks).  The lengths are on the device, so ssm_prep shares the rows out.
-// Cut and whole, us: one prompt of 32768 tokens, 32 heads of 128, N = 128: 757 and 2078
-// (with segment 0 0.4 or 0.55 of the others: 773, 767); 4000 tokens, 16 heads of 64: 87 and
-// 270; 2 x 2048, 64 heads of 64: 128 and 158; 8 prompts of 0 to 4095, 64 heads of 64: 262
-// and 325; 9000 + 100, 64 heads of 128: 407 and 591.  What a batch pays that is not cut in
-// the end: 4 x 4096: 293 and 291, 8 x 1000, 32 heads: 97 and 94 (equal lengths that are
+// Cut and whole, us: one prompt of 32768 tokens, 32 heads of 128, N = 128: 768 and 2140
+// (with segment 0 0.4 or 0.55 of the others: 784); 4000 tokens, 16 heads of 64: 88 and
+// 279; 2 x 2048, 64 heads of 64: 130 and 162; 8 prompts of 0 to 4095, 64 heads of 64: 271
+// and 332; 9000 + 100, 64 heads of 128: 411 and 609.  What a batch pays that is not cut in
+// the end: 4 x 4096: 304 and 303, 8 x 1000, 32 heads: 97 and 94 (equal lengths that are
 // given as such pay nothing).
-// Pieces of 2, 3 or 4 chunks at least: 768 tokens, 32 heads of 64: 56, 58, 65 us; 400
-// tokens, 16 heads: 51, 49, 49.
+// Pieces of 2, 3 or 4 chunks at least: 768 tokens, 32 heads of 64: 60, 62, 68 us; 400
+// tokens, 16 heads: 50, 49, 49.
 Plan plan_for(const SsmArgs &a, int sms) {
     Plan p;
     const int R = a.H / a.G;
