@@ -222,11 +222,12 @@ ssm_scan_kernel(const float *__restrict__ act, const float4 *__restrict__ step, 
             asm volatile("cp.async.wait_group 0;" ::: "memory");
         }
         __syncthreads();
-        // four tokens at a time: their recurrences follow one another, but their parts of y
-        // (8 values) are added over the eight slices together, one value staying in each lane
-        // takes what the stage before left: once a stage 3 % of the time, at every token 14
+        // the stage's first decay takes the remainders before it: once a stage 3 % of the time,
+        // at every token 14
         const float first = next_decay(st.d[0].y, carry);
         float logs = 0.f;
+        // four tokens at a time: their recurrences follow one another, but their parts of y
+        // (8 values) are added over the eight slices together, one value staying in each lane
         for (int r = 0; r < len; r += 4) {
             float v[8];
 #pragma unroll
